@@ -69,7 +69,11 @@ extern "C" {
 /* ---- device error bits (workspace error word) ------------------------------- */
 #define MLA_DEVERR_BAD_SLOT 1u       /* a dense slot outside [0, pool_rows): key skipped */
 #define MLA_DEVERR_TIMEOUT 2u        /* a bounded pipeline wait ran out: CTA gave up */
-#define MLA_DEVERR_BAD_LENGTH 4u     /* seq_lens[b] outside [0, kv_indptr[b+1]-kv_indptr[b]] */
+#define MLA_DEVERR_BAD_LENGTH 4u     /* seq_lens[b] outside [0, kv_indptr[b+1]-kv_indptr[b]];
+                                        a fork's child longer than its parent */
+#define MLA_DEVERR_BAD_POSITION 8u   /* mla_cache_append: a position outside the table */
+#define MLA_DEVERR_BAD_TABLE 16u     /* mla_cache_fork: a parent outside [0, num_parents), or
+                                        table offsets outside their lists */
 
 /* Element types of the DCP share buffers (mla_decode_dcp, mla_dcp_lse_merge_ranks). */
 #define MLA_DTYPE_BF16 0
@@ -402,6 +406,112 @@ int mla_decode_noalloc(const mla_plan_t* plan, const void* q_lat, const void* q_
                        const int32_t* kv_indices, const int32_t* kv_indptr, int32_t batch,
                        int32_t q_len, int32_t num_heads, float scale, float kv_scale,
                        void* o_lat, float* lse, void* stream);
+
+/*
+ * Cache append: one pass from the projections' outputs to what the decode
+ * reads.  For each of num_tokens tokens, with p = positions[t] and, for
+ * i in [0, 32), c_i = cos_sin[p, i], s_i = cos_sin[p, 32 + i]:
+ *   kv row   the token's latent row x (row_bytes columns: d_v latent, then 64
+ *            RoPE; row_bytes 576 for mla_decode's rows, 512 for
+ *            mla_sparse_decode's).  The first kv_norm_cols columns (0, d_v or
+ *            all of them) are RMS-normed, x_j * (mean x^2 + eps)^-1/2 *
+ *            kv_weight[j] (weight 1 where kv_weight is NULL); the last 64 are
+ *            then rotated; pool[slots[t]] = e4m3(y * (1 / kv_scale)), to
+ *            nearest even, saturating at +-448 (NaN stays NaN).  A negative
+ *            slot skips the row (a padding token).
+ *   queries  the token's num_heads rows of q_cols columns, RMS-normed over all
+ *            of them when q_norm is nonzero (times q_weight where non-NULL),
+ *            the last 64 rotated, written as bf16 to q_nope (the first
+ *            q_cols - 64) and q_pe (the last 64).
+ * Rotation of (a, b) by (c, s): (a c - b s, b c + a s); the pairs are columns
+ * (2 i, 2 i + 1), or (i, i + 32) when half_split is nonzero.  Everything is
+ * computed in fp32 and rounded once.
+ *   kv        bf16, token t's row at kv + t * kv_stride (elements); NULL: no
+ *             rows are appended (slots and pool may then be NULL)
+ *   kv_weight bf16 [kv_norm_cols] or NULL
+ *   slots     int32 [num_tokens], each in [0, pool_rows) or negative; the slots
+ *             of a call are distinct (of two tokens with one slot either may
+ *             be found there, in part or whole).  A slot past the pool sets
+ *             MLA_DEVERR_BAD_SLOT and its row is skipped.
+ *   q         bf16, head h of token t at q + t * q_token_stride +
+ *             h * q_head_stride; NULL (with num_heads 0): no queries
+ *   q_weight  bf16 [q_cols] or NULL; q_cols a multiple of 64 in [64, 576]
+ *   q_nope    bf16 [num_tokens, num_heads, q_cols - 64] (unused, may be NULL,
+ *             when q_cols is 64); q_pe bf16 [num_tokens, num_heads, 64];
+ *             neither overlaps q
+ *   positions int32 [num_tokens]; cos_sin fp32 [max_positions, 64].  A position
+ *             outside [0, max_positions) sets MLA_DEVERR_BAD_POSITION and
+ *             nothing of that token is written.
+ *   workspace at least MLA_WORKSPACE_HEADER_BYTES, 256-byte aligned: the error
+ *             word.  Calls may share it, also when they overlap.
+ * kv, weights, q, q_nope, q_pe, pool and cos_sin are 16-byte aligned and the
+ * strides multiples of 8 elements (else MLA_ERR_MISALIGNED); num_heads <= 128;
+ * eps >= 0 and finite; kv_scale finite and not zero.  num_tokens 0 is a no-op.
+ */
+int mla_cache_append(const void* kv, int64_t kv_stride, const void* kv_weight,
+                     int32_t kv_norm_cols, const int32_t* slots, void* pool, int64_t pool_rows,
+                     int32_t row_bytes, float kv_scale, const void* q, int64_t q_token_stride,
+                     int64_t q_head_stride, const void* q_weight, int32_t q_norm, int32_t q_cols,
+                     void* q_nope, void* q_pe, const int32_t* positions, const float* cos_sin,
+                     int64_t max_positions, int32_t half_split, float eps, int32_t num_tokens,
+                     int32_t num_heads, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Cache fork: the page tables of num_children requests that continue
+ * num_parents requests, and copies of the rows that they do not share.  Child f
+ * takes the first n_f = child_indptr[f+1] - child_indptr[f] positions of parent
+ * p = parents[f] (n_f at most the parent's length, kv_indptr[p+1] -
+ * kv_indptr[p]).  Its positions j < keep[f] name the parent's own slots; the
+ * others take fresh slots in order, and the rows are copied there:
+ *   table[child_indptr[f] + j] = kv_indices[kv_indptr[p] + j]         j < keep[f]
+ *                              = fresh[fresh_indptr[f] + j - keep[f]]  otherwise,
+ *   pool[table[...]] = pool[kv_indices[kv_indptr[p] + j]]              (bytes)
+ * keep[f] <= 0 copies every row, keep[f] >= n_f none.  The fresh slots of a
+ * call are distinct and none is a slot that the call copies from.
+ *   pool [pool_rows, row_bytes], row_bytes 576 or 512, 16-byte aligned
+ *   kv_indices int32 [num_indices]; kv_indptr int32 [num_parents + 1]
+ *   parents, keep int32 [num_children]; child_indptr, fresh_indptr int32
+ *   [num_children + 1]; fresh int32 [num_fresh]
+ *   table int32 [total], written; total = child_indptr[num_children] (a shape:
+ *   entries of table past the last child's are not touched)
+ * Found on the device: a slot outside the pool (MLA_DEVERR_BAD_SLOT: its row is
+ * not copied, the table entry names it all the same), a child longer than its
+ * parent (MLA_DEVERR_BAD_LENGTH) and a parent, offset or fresh entry outside
+ * its list (MLA_DEVERR_BAD_TABLE): the entry becomes -1 and no row is copied.
+ * workspace as for mla_cache_append.
+ */
+int mla_cache_fork(void* pool, int64_t pool_rows, int32_t row_bytes, const int32_t* kv_indices,
+                   int64_t num_indices, const int32_t* kv_indptr, int32_t num_parents,
+                   const int32_t* parents, const int32_t* keep, const int32_t* child_indptr,
+                   int32_t num_children, const int32_t* fresh, int64_t num_fresh,
+                   const int32_t* fresh_indptr, int32_t* table, int64_t total, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
+/*
+ * Cache compaction: gathers the live rows at the front of the pool and rewrites
+ * the page tables.  A row is live when an entry of kv_indices names it (any
+ * number of times: shared prefixes stay shared).  With L live rows, the k-th
+ * live row at or past L, in slot order, moves into the k-th free slot below L,
+ * so only rows that have to move do, and the free slots are then [L, pool_rows):
+ *   new_indices[i] = the slot of the row that kv_indices[i] named
+ *   live[0]        = L
+ * A negative entry stays as it is; one past the pool does too, and sets
+ * MLA_DEVERR_BAD_SLOT.  Rows at or past L keep their old bytes.  The result
+ * does not depend on timing.
+ *   pool [pool_rows, row_bytes], row_bytes 576 or 512, 16-byte aligned, in place
+ *   kv_indices int32 [num_indices]; new_indices int32 [num_indices], which may
+ *   be kv_indices itself (else they do not overlap); live int32 [1], all device
+ *   workspace of mla_cache_compact_workspace_bytes(pool_rows) bytes, 256-byte
+ *   aligned, zeroed header (calls that overlap do not share it)
+ * pool_rows < 2^31.
+ */
+int mla_cache_compact(void* pool, int64_t pool_rows, int32_t row_bytes,
+                      const int32_t* kv_indices, int64_t num_indices, int32_t* new_indices,
+                      int32_t* live, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of mla_cache_compact for a pool of pool_rows rows; 0 for an
+ * unsupported count. */
+int64_t mla_cache_compact_workspace_bytes(int64_t pool_rows);
 
 /* Static text for a status code. */
 const char* mla_status_string(int status);

@@ -9,6 +9,10 @@ plumbing of decode context parallelism (rank page tables, the exchange step).
 """
 from .mla import (  # noqa: F401
     MlaError,
+    cache_workspace,
+    mla_cache_append,
+    mla_cache_compact,
+    mla_cache_fork,
     mla_dcp_lse_merge_ranks,
     mla_decode,
     mla_decode_dcp,

@@ -71,22 +71,6 @@ bool fused_merge_ok(int64_t tiles, int32_t ns, int32_t rows_per_cta, int32_t mc)
     return nclus == 1 || nclus * (rows_per_cta / mc) <= kMaxMergeTerms;
 }
 
-int device_ok()
-{
-    static int cached[64];  // 0 unknown, 1 ok, 2 not ok
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
-    if (dev < 0 || dev >= 64) return MLA_ERR_UNSUPPORTED_DEVICE;
-    if (cached[dev] == 0) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-            return MLA_ERR_CUDA;
-        cached[dev] = (major == 10 && minor == 3) ? 1 : 2;
-    }
-    return cached[dev] == 1 ? MLA_OK : MLA_ERR_UNSUPPORTED_DEVICE;
-}
-
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int64_t workspace_for(int64_t items, int ns, int d_v)
@@ -204,6 +188,22 @@ void fill_plan(mla_plan_t* p, int32_t batch, int32_t q_len, int32_t heads, int32
 }
 
 }  // namespace
+
+int device_ok()
+{
+    static int cached[64];  // 0 unknown, 1 ok, 2 not ok
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return MLA_ERR_UNSUPPORTED_DEVICE;
+    if (cached[dev] == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return MLA_ERR_CUDA;
+        cached[dev] = (major == 10 && minor == 3) ? 1 : 2;
+    }
+    return cached[dev] == 1 ? MLA_OK : MLA_ERR_UNSUPPORTED_DEVICE;
+}
 
 // The bound of the split kernel's pipeline waits, in SM cycles (about a second
 // by default; mla_debug_wait_limit lowers it for tests of the timeout path).

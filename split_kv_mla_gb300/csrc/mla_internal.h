@@ -138,6 +138,9 @@ cudaError_t launch_dcp_merge(const void* parts, bool parts_f32, const float* lse
                              int32_t world, int64_t rows, int32_t d_v, uint16_t* o, float* lse,
                              cudaStream_t stream);
 
+// MLA_OK when the current device is one the library runs on, else a status.
+int device_ok();
+
 // Gather probe (mla_debug_gather).
 cudaError_t launch_gather_probe(const void* pool, int64_t pool_rows, int32_t row_bytes,
                                 const int32_t* indices, int64_t n, uint8_t* out, uint32_t* err,

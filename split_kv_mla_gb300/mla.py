@@ -27,6 +27,8 @@ MLA_WORKSPACE_HEADER_BYTES = 65536
 MLA_DEVERR_BAD_SLOT = 1
 MLA_DEVERR_TIMEOUT = 2
 MLA_DEVERR_BAD_LENGTH = 4
+MLA_DEVERR_BAD_POSITION = 8
+MLA_DEVERR_BAD_TABLE = 16
 MLA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 HEADER = os.path.join(_build.ROOT, "include", "mla_decode.h")
 
@@ -111,6 +113,13 @@ def load(build_if_missing: bool = True, path: Optional[str] = None):
             "mla_decode_dcp_splits": (ctypes.c_int, [P, vp, vp, vp, i64, vp, vp, vp, i32, i32,
                                                      i32, f32, f32, vp, i32, i32, i32, vp, vp,
                                                      vp, i64, vp]),
+            "mla_cache_append": (ctypes.c_int, [vp, i64, vp, i32, vp, vp, i64, i32, f32, vp, i64,
+                                                i64, vp, i32, i32, vp, vp, vp, vp, i64, i32, f32,
+                                                i32, i32, vp, i64, vp]),
+            "mla_cache_fork": (ctypes.c_int, [vp, i64, i32, vp, i64, vp, i32, vp, vp, vp, i32, vp,
+                                              i64, vp, vp, i64, vp, i64, vp]),
+            "mla_cache_compact": (ctypes.c_int, [vp, i64, i32, vp, i64, vp, vp, vp, i64, vp]),
+            "mla_cache_compact_workspace_bytes": (i64, [i64]),
             "mla_dcp_lse_merge_ranks": (ctypes.c_int, [vp, i32, vp, i32, i64, i32, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
@@ -472,3 +481,167 @@ def mla_decode_noalloc(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices
         _stream_ptr(stream))
     _check(rc, "mla_decode_noalloc")
     return o_lat, lse
+
+
+# ---- the cache: append, fork, compact ------------------------------------------------
+
+def _same_device(first: torch.Tensor, **tensors) -> None:
+    """All given tensors on `first`'s CUDA device, and that device current (the
+    library launches on the current device)."""
+    dev = first.device
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t as [..., columns] whose last dimension is contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t
+
+
+def _pool_2d(pool: torch.Tensor) -> torch.Tensor:
+    """The pool as [rows, row_bytes]: 2-D, or a [rows, 1, row_bytes] cache."""
+    if pool.element_size() != 1 or pool.dim() not in (2, 3) or (pool.dim() == 3 and
+                                                               pool.shape[1] != 1):
+        raise ValueError("pool must hold one byte per element, [rows, row_bytes]")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    return pool
+
+
+def cache_workspace(pool_rows: int = 0, device=None) -> torch.Tensor:
+    """A zeroed workspace for mla_cache_append and mla_cache_fork, and with the
+    pool's row count for mla_cache_compact too."""
+    n = MLA_WORKSPACE_HEADER_BYTES
+    if pool_rows:
+        n = int(load().mla_cache_compact_workspace_bytes(int(pool_rows)))
+        if n == 0:
+            raise ValueError(f"pool_rows {pool_rows} is not supported")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0, q=None,
+                     kv_weight=None, kv_norm_cols: int = 0, q_weight=None, q_norm: bool = False,
+                     eps: float = 1e-6, half_split: bool = False, q_nope=None, q_pe=None,
+                     workspace_t=None, stream=None):
+    """Norm, rotate and quantise the tokens' latent rows into their cache slots,
+    and norm and rotate their queries; returns (q_nope, q_pe).
+
+    kv bf16 [T, 576 or 512] (None: no rows), q bf16 [T, H, q_cols] (None: no
+    queries), rows contiguous, other strides free in steps of 8 elements;
+    positions int32 [T]; cos_sin fp32 [max_positions, 64], 32 cosines then 32
+    sines.  q_nope is None when q_cols is 64 (or without queries)."""
+    first = kv if kv is not None else q
+    if first is None:
+        raise ValueError("kv or q must be given")
+    _same_device(first, slots=slots, pool=pool, positions=positions, cos_sin=cos_sin, q=q,
+                 kv_weight=kv_weight, q_weight=q_weight, q_nope=q_nope, q_pe=q_pe,
+                 workspace=workspace_t)
+    T = first.shape[0]
+    kv_ptr = kv_stride = pool_rows = width = 0
+    if kv is not None:
+        if slots is None or pool is None:
+            raise ValueError("slots and pool must be given with kv")
+        p = _pool_2d(pool)
+        pool_rows, width = p.shape[0], p.shape[-1]
+        if _rows(kv, "kv").dim() != 2 or kv.shape[1] != width:
+            raise ValueError(f"kv must be [T, {width}], the pool's row width")
+        if slots.numel() != T:
+            raise ValueError("slots must have one entry per token")
+        if kv_weight is not None and kv_weight.numel() != kv_norm_cols:
+            raise ValueError("kv_weight must have kv_norm_cols entries")
+        kv_ptr, kv_stride = kv.data_ptr(), kv.stride(0)
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        raise ValueError("cos_sin must be [max_positions, 64]")
+    H = cols = q_ptr = qts = qhs = 0
+    if q is not None:
+        if _rows(q, "q").dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must be [T, H, q_cols]")
+        H, cols = q.shape[1], q.shape[2]
+        if q_weight is not None and q_weight.numel() != cols:
+            raise ValueError("q_weight must have q_cols entries")
+        q_ptr, qts, qhs = q.data_ptr(), q.stride(0), q.stride(1)
+        if q_nope is None and cols > 64:
+            q_nope = torch.empty(T, H, cols - 64, dtype=torch.bfloat16, device=q.device)
+        if q_pe is None:
+            q_pe = torch.empty(T, H, 64, dtype=torch.bfloat16, device=q.device)
+        if q_pe.numel() != T * H * 64 or (cols > 64 and q_nope.numel() != T * H * (cols - 64)):
+            raise ValueError("q_nope and q_pe must be [T, H, q_cols - 64] and [T, H, 64]")
+    if workspace_t is None:
+        workspace_t = cache_workspace(device=first.device)
+    _check(load().mla_cache_append(
+        kv_ptr or None, kv_stride, _dev_ptr(kv_weight, "kv_weight", torch.bfloat16),
+        int(kv_norm_cols), _dev_ptr(slots, "slots", torch.int32),
+        pool.data_ptr() if kv is not None else None, pool_rows, width, float(kv_scale),
+        q_ptr or None, qts, qhs, _dev_ptr(q_weight, "q_weight", torch.bfloat16),
+        1 if q_norm else 0, cols, _dev_ptr(q_nope, "q_nope", torch.bfloat16),
+        _dev_ptr(q_pe, "q_pe", torch.bfloat16), _dev_ptr(positions, "positions", torch.int32),
+        _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], 1 if half_split else 0,
+        float(eps), T, H, _dev_ptr(workspace_t, "workspace"), workspace_t.numel(),
+        _stream_ptr(stream)), "mla_cache_append")
+    return q_nope, q_pe
+
+
+def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, total: int, fresh,
+                   fresh_indptr, table=None, workspace_t=None, stream=None):
+    """Page tables of requests that continue `parents`, sharing their first
+    keep[f] slots and copying the other rows to fresh slots; returns the
+    children's kv_indices int32 [total] (their kv_indptr is child_indptr)."""
+    p = _pool_2d(pool)
+    _same_device(pool, kv_indices=kv_indices, kv_indptr=kv_indptr, parents=parents, keep=keep,
+                 child_indptr=child_indptr, fresh=fresh, fresh_indptr=fresh_indptr, table=table,
+                 workspace=workspace_t)
+    F = parents.numel()
+    if keep.numel() != F or child_indptr.numel() != F + 1 or fresh_indptr.numel() != F + 1:
+        raise ValueError("keep, child_indptr and fresh_indptr must match parents")
+    if table is None:
+        table = torch.empty(int(total), dtype=torch.int32, device=pool.device)
+    elif table.numel() < total:
+        raise ValueError("table must have total entries")
+    if workspace_t is None:
+        workspace_t = cache_workspace(device=pool.device)
+    i32 = torch.int32
+    _check(load().mla_cache_fork(
+        p.data_ptr(), p.shape[0], p.shape[-1], _dev_ptr(kv_indices, "kv_indices", i32),
+        kv_indices.numel(), _dev_ptr(kv_indptr, "kv_indptr", i32), max(0, kv_indptr.numel() - 1),
+        _dev_ptr(parents, "parents", i32), _dev_ptr(keep, "keep", i32),
+        _dev_ptr(child_indptr, "child_indptr", i32), F, _dev_ptr(fresh, "fresh", i32),
+        fresh.numel(), _dev_ptr(fresh_indptr, "fresh_indptr", i32),
+        _dev_ptr(table, "table", i32), int(total), _dev_ptr(workspace_t, "workspace"),
+        workspace_t.numel(), _stream_ptr(stream)), "mla_cache_fork")
+    return table
+
+
+def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t=None,
+                      stream=None):
+    """Move the rows that kv_indices names to the front of the pool, in place;
+    returns (new_indices, live): the rewritten table and the live row count
+    int32 [1] (rows from there on are free).  new_indices may be kv_indices."""
+    p = _pool_2d(pool)
+    _same_device(pool, kv_indices=kv_indices, new_indices=new_indices, live=live,
+                 workspace=workspace_t)
+    if new_indices is None:
+        new_indices = torch.empty_like(kv_indices)
+    elif new_indices.numel() != kv_indices.numel():
+        raise ValueError("new_indices must match kv_indices")
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=pool.device)
+    if workspace_t is None:
+        workspace_t = cache_workspace(p.shape[0], device=pool.device)
+    _check(load().mla_cache_compact(
+        p.data_ptr(), p.shape[0], p.shape[-1], _dev_ptr(kv_indices, "kv_indices", torch.int32),
+        kv_indices.numel(), _dev_ptr(new_indices, "new_indices", torch.int32),
+        _dev_ptr(live, "live", torch.int32), _dev_ptr(workspace_t, "workspace"),
+        workspace_t.numel(), _stream_ptr(stream)), "mla_cache_compact")
+    return new_indices, live

@@ -408,6 +408,53 @@ int mla_decode_noalloc(const mla_plan_t* plan, const void* q_lat, const void* q_
                        void* o_lat, float* lse, void* stream);
 
 /*
+ * A plan of mla_prefix_decode, from shapes alone; plain data like mla_plan_t.
+ */
+typedef struct {
+    int32_t tiles;           /* 64-row tiles of the batch * q_len * num_heads query rows */
+    int32_t ctas;            /* CTAs that share the (tile, 128-key block) pairs of the prefix */
+    int32_t parts;           /* most CTAs that one tile's blocks fall to (partials per row);
+                                0 when prefix_cap is 0 */
+    int32_t sm_count;
+    int64_t workspace_bytes; /* bytes of device workspace the call needs */
+    int64_t prefix_cap;      /* entries of prefix_indices */
+    mla_plan_t own;          /* the plan of the requests' own keys (mla_decode_plan) */
+} mla_prefix_plan_t;
+
+/*
+ * Plan of a decode over a shared prefix of up to prefix_cap positions and
+ * total_keys entries of the requests' own page tables.  Other arguments and
+ * limits as for mla_decode_plan (d_v 512, d_rope 64); prefix_cap <= 2^30.
+ */
+int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int64_t prefix_cap,
+                           int64_t total_keys, int32_t sm_count, mla_prefix_plan_t* out);
+
+/*
+ * Dense decode of a batch whose requests share a prefix: request b's keys are
+ * the prefix's P slots followed by its own seq_lens[b] slots, and the call gives
+ * what mla_decode gives on the joined page tables (S = P + seq_lens[b]; draft
+ * position t attends positions [0, S - q_len + t]), but the prefix's rows are
+ * fetched and multiplied once for the query rows of the whole batch.
+ *   prefix_indices int32 [prefix_cap]: the prefix's slots, in any order of the pool
+ *   prefix_len     int32 [1] device: P, the entries in use; NULL: all of them.
+ *                  Outside [0, prefix_cap] it is clamped and sets
+ *                  MLA_DEVERR_BAD_LENGTH.
+ *   seq_lens, kv_indices, kv_indptr: the requests' own keys, as for mla_decode
+ *                  (a request may have none; kv_indices may be NULL when
+ *                  total_keys was 0)
+ *   workspace >= plan->workspace_bytes bytes, 256-byte aligned, zeroed header;
+ *                  calls that share it must not overlap on the GPU
+ * Other arguments, layouts and device errors as for mla_decode.  The merge joins
+ * partials in a fixed order, so results do not vary from call to call.
+ */
+int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const void* q_pe,
+                      const void* pool, int64_t pool_rows, const int32_t* prefix_indices,
+                      const int32_t* prefix_len, const int32_t* seq_lens,
+                      const int32_t* kv_indices, const int32_t* kv_indptr, int32_t batch,
+                      int32_t q_len, int32_t num_heads, float scale, float kv_scale, void* o,
+                      float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * Cache append: one pass from the projections' outputs to what the decode
  * reads.  For each of num_tokens tokens, with p = positions[t] and, for
  * i in [0, 32), c_i = cos_sin[p, i], s_i = cos_sin[p, 32 + i]:

@@ -21,6 +21,9 @@ from .mla import (  # noqa: F401
     mla_decode_splits,
     mla_decode_plan,
     mla_plan_force_splits,
+    mla_prefix_decode,
+    mla_prefix_decode_plan,
+    mla_prefix_plan_t,
     mla_plan_t,
     mla_read_device_error,
     mla_sparse_decode,

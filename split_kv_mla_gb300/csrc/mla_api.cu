@@ -642,6 +642,188 @@ int mla_sparse_decode_splits(const mla_plan_t* plan, const void* q_nope, const v
                        topk, scale, kv_scale, o, lse, workspace, workspace_bytes, stream, false);
 }
 
+// ---- shared-prefix decode -----------------------------------------------------------------
+
+namespace {
+
+constexpr double kPrefixBlockUs = 1.6;   // a 128-key block of one 64-row tile
+constexpr double kPrefixRunUs = 6.0;     // a run's start (query tile, first block) and epilogue
+
+inline int64_t prefix_blocks(int64_t cap) { return ceil_div(cap, kPrefixKeys); }
+
+// Most partials of one tile when `tiles` tiles are dealt out to `ctas` CTAs in
+// equal runs: run borders fall at multiples of tiles / ctas tiles.
+int32_t prefix_parts(int64_t tiles, int64_t ctas)
+{
+    if (ctas % tiles == 0) return (int32_t)(ctas / tiles);
+    return (int32_t)(ceil_div(ctas, tiles) + 1);
+}
+
+struct PrefixLayout {   // byte offsets in the workspace
+    int64_t own_o, own_lse, o_part, lse_part, k_image, k_valid, q_image, q_scale, q_window, end;
+};
+
+// The requests' own partials first, where the split kernel's plan has them.
+PrefixLayout prefix_layout(const mla_prefix_plan_t* p)
+{
+    const int64_t rows = (int64_t)p->own.batch * p->own.q_len * p->own.num_heads;
+    const int64_t blocks = prefix_blocks(p->prefix_cap);
+    const int64_t tiles = p->parts > 0 ? p->tiles : 0;
+    int64_t at = MLA_WORKSPACE_HEADER_BYTES;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += align_up(bytes, 256);
+        return here;
+    };
+    PrefixLayout l;
+    l.own_o = take(rows * p->own.num_splits * kDenseDv * 4);
+    l.own_lse = take(rows * p->own.num_splits * 4);
+    l.o_part = take(rows * p->parts * kDenseDv * 4);
+    l.lse_part = take(rows * p->parts * 4);
+    l.k_image = take(blocks * kPrefixImage);
+    l.k_valid = take(blocks * 16);
+    l.q_image = take(tiles * kPrefixImage);
+    l.q_scale = take(tiles * kPrefixRows * 4);
+    l.q_window = take(tiles * kPrefixRows * 4);
+    l.end = at;
+    return l;
+}
+
+bool prefix_plan_ok(const mla_prefix_plan_t* p)
+{
+    const int64_t rows = (int64_t)p->own.batch * p->own.q_len * p->own.num_heads;
+    if (p->own.batch < 1 || !variant_ok(&p->own) || p->own.num_splits < 1 ||
+        p->own.num_splits > MLA_MAX_SPLITS || p->own.d_v != kDenseDv ||
+        p->own.d_rope != kDenseDr || p->own.total_keys < 0 || p->own.merge_cluster != 1 ||
+        p->own.workspace_bytes != needed_workspace(&p->own))
+        return false;
+    if (p->prefix_cap < 0 || p->prefix_cap > (1LL << 30)) return false;
+    if (p->tiles != ceil_div(rows, kPrefixRows)) return false;
+    if (p->prefix_cap == 0 ? p->parts != 0
+                           : p->ctas < 1 || p->parts != prefix_parts(p->tiles, p->ctas) ||
+                                 p->parts > MLA_MAX_SPLITS)
+        return false;
+    return p->workspace_bytes == prefix_layout(p).end;
+}
+
+}  // namespace
+
+int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int64_t prefix_cap,
+                           int64_t total_keys, int32_t sm_count, mla_prefix_plan_t* out)
+{
+    if (!out || prefix_cap < 0) return MLA_ERR_INVALID_ARG;
+    if (prefix_cap > (1LL << 30)) return MLA_ERR_UNSUPPORTED_SHAPE;
+    std::memset(out, 0, sizeof *out);
+    const int rc = mla_decode_plan(batch, q_len, num_heads, total_keys, kDenseDv, kDenseDr,
+                                   sm_count, &out->own);
+    if (rc != MLA_OK) return rc;
+    const int64_t rows = (int64_t)batch * q_len * num_heads;
+    if (rows > INT32_MAX) return MLA_ERR_UNSUPPORTED_SHAPE;
+    out->sm_count = sm_count;
+    out->prefix_cap = prefix_cap;
+    out->tiles = (int32_t)ceil_div(rows, kPrefixRows);
+    const int64_t tiles = out->tiles, blocks = prefix_blocks(prefix_cap);
+    if (tiles > 0 && blocks > 0) {
+        // Either every tile is cut into ns equal runs, one per CTA, or all SMs get
+        // an equal run of the tile-major sequence, which ends and starts inside
+        // tiles: the first has no second run in a CTA, the second no idle SM.
+        const int64_t U = tiles * blocks;
+        double best = 0.0;
+        auto consider = [&](int64_t ctas) {
+            const int64_t per = ceil_div(U, ctas);
+            const int64_t runs = ctas % tiles == 0 ? 1 : (per - 2 + blocks) / blocks + 1;
+            const int64_t parts = prefix_parts(tiles, ctas);
+            if (parts > MLA_MAX_SPLITS) return;
+            const double us = (double)per * kPrefixBlockUs + (double)runs * kPrefixRunUs +
+                              (double)rows * parts * kDenseDv * 8.0 / kBytesPerUs;
+            if (out->ctas == 0 || us < best) {
+                best = us;
+                out->ctas = (int32_t)ctas;
+                out->parts = (int32_t)parts;
+            }
+        };
+        for (int64_t ns = 1; ns <= blocks && ns * tiles <= sm_count; ++ns) consider(ns * tiles);
+        consider(U < sm_count ? U : sm_count);
+        if (out->ctas == 0) return MLA_ERR_UNSUPPORTED_SHAPE;
+    }
+    out->workspace_bytes = prefix_layout(out).end;
+    return MLA_OK;
+}
+
+int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const void* q_pe,
+                      const void* pool, int64_t pool_rows, const int32_t* prefix_indices,
+                      const int32_t* prefix_len, const int32_t* seq_lens,
+                      const int32_t* kv_indices, const int32_t* kv_indptr, int32_t batch,
+                      int32_t q_len, int32_t num_heads, float scale, float kv_scale, void* o,
+                      float* lse, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (!plan || plan->own.batch != batch || plan->own.q_len != q_len ||
+        plan->own.num_heads != num_heads)
+        return MLA_ERR_INVALID_ARG;
+    if (batch == 0) return MLA_OK;
+    if (!prefix_plan_ok(plan)) return MLA_ERR_INVALID_ARG;
+    if (!q_lat || !q_pe || !pool || !seq_lens || !kv_indptr || !o || pool_rows < 1 ||
+        (plan->prefix_cap > 0 && !prefix_indices) || (plan->own.total_keys > 0 && !kv_indices))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_lat) || !aligned16(q_pe) || !aligned16(pool) || !aligned16(o))
+        return MLA_ERR_MISALIGNED;
+    if (!std::isfinite(scale) || !std::isfinite(kv_scale)) return MLA_ERR_INVALID_ARG;
+    if (!workspace) return MLA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MLA_ERR_MISALIGNED;
+    if (workspace_bytes < plan->workspace_bytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    int rc = device_ok();
+    if (rc != MLA_OK) return rc;
+
+    const PrefixLayout l = prefix_layout(plan);
+    char* ws = static_cast<char*>(workspace);
+    PrefixArgs a{};
+    a.q_lat = static_cast<const uint16_t*>(q_lat);
+    a.q_pe = static_cast<const uint16_t*>(q_pe);
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.pool_rows = pool_rows;
+    a.prefix_indices = prefix_indices;
+    a.prefix_len = plan->prefix_cap > 0 ? prefix_len : nullptr;
+    a.prefix_cap = plan->prefix_cap;
+    a.seq_lens = seq_lens;
+    a.kv_indptr = kv_indptr;
+    a.batch = batch;
+    a.q_len = q_len;
+    a.num_heads = num_heads;
+    a.rows = (int64_t)batch * q_len * num_heads;
+    a.tiles = plan->tiles;
+    a.ctas = plan->ctas;
+    a.parts = plan->parts;
+    a.logit_scale = scale * kv_scale * kLog2e;
+    a.kv_scale = kv_scale;
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    a.k_image = reinterpret_cast<uint8_t*>(ws + l.k_image);
+    a.k_valid = reinterpret_cast<uint32_t*>(ws + l.k_valid);
+    a.q_image = reinterpret_cast<uint8_t*>(ws + l.q_image);
+    a.q_scale = reinterpret_cast<float*>(ws + l.q_scale);
+    a.q_window = reinterpret_cast<int32_t*>(ws + l.q_window);
+    a.o_part = reinterpret_cast<float*>(ws + l.o_part);
+    a.lse_part = reinterpret_cast<float*>(ws + l.lse_part);
+    a.o_own = reinterpret_cast<const float*>(ws + l.own_o);
+    a.lse_own = reinterpret_cast<const float*>(ws + l.own_lse);
+    // one split writes final rows (kv_scale applied), several leave raw partials
+    a.own_splits = plan->own.total_keys > 0 ? plan->own.num_splits : 0;
+    a.own_scale = plan->own.num_splits == 1 ? 1.f : kv_scale;
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.wait_limit = pipeline_wait_limit();
+    a.stall_probe = stall_probe_armed() ? 1 : 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (plan->parts > 0 && launch_prefix_split(a, s) != cudaSuccess) return MLA_ERR_LAUNCH_FAILED;
+    if (a.own_splits > 0) {
+        rc = dense_call(&plan->own, q_lat, q_pe, pool, pool_rows, seq_lens, kv_indices, kv_indptr,
+                        batch, q_len, num_heads, scale, kv_scale, ws + l.own_o,
+                        reinterpret_cast<float*>(ws + l.own_lse), workspace, workspace_bytes,
+                        stream, false, nullptr, 0, 1, true);
+        if (rc != MLA_OK) return rc;
+    }
+    return launch_prefix_merge(a, s) == cudaSuccess ? MLA_OK : MLA_ERR_LAUNCH_FAILED;
+}
+
 int mla_workspace_partials(const mla_plan_t* plan, void* workspace, float** o_part,
                            float** lse_part)
 {

@@ -138,6 +138,54 @@ cudaError_t launch_dcp_merge(const void* parts, bool parts_f32, const float* lse
                              int32_t world, int64_t rows, int32_t d_v, uint16_t* o, float* lse,
                              cudaStream_t stream);
 
+// ---- shared-prefix decode (mla_prefix.cu) -----------------------------------------------
+constexpr int kPrefixRows = 64;       // query rows of a tile
+constexpr int kPrefixKeys = 128;      // keys of a block
+constexpr int64_t kPrefixImage = 73728;   // bytes of a block's (a query tile's) operand image
+
+// Parameters of one shared-prefix call's kernels.
+struct PrefixArgs {
+    const uint16_t* q_lat;       // bf16 [batch * q_len, H, 512]
+    const uint16_t* q_pe;        // bf16 [batch * q_len, H, 64]
+    const uint8_t* pool;         // e4m3fn [pool_rows, 576]
+    int64_t pool_rows;
+    const int32_t* prefix_indices;
+    const int32_t* prefix_len;   // device length, or NULL: prefix_cap
+    int64_t prefix_cap;          // entries of prefix_indices
+    const int32_t* seq_lens;     // the requests' own keys
+    const int32_t* kv_indptr;
+    int32_t batch, q_len, num_heads;
+    int64_t rows;                // batch * q_len * num_heads
+    int32_t tiles;               // ceil(rows / kPrefixRows)
+    int32_t ctas;                // CTAs of the prefix kernel
+    int32_t parts;               // partial rows per output row from the prefix
+    float logit_scale;           // scale * kv_scale * log2(e)
+    float kv_scale;
+    // workspace
+    uint32_t* err;
+    uint8_t* k_image;            // [blocks][kPrefixImage]: keys as the MMA reads them
+    uint32_t* k_valid;           // [blocks][4]: bit per key
+    uint8_t* q_image;            // [tiles][kPrefixImage]: e4m3 terms of the queries
+    float* q_scale;              // [tiles * 64] raw dot -> base-2 logit
+    int32_t* q_window;           // [tiles * 64] prefix positions the row sees
+    float* o_part;               // [rows, parts, 512], normalised
+    float* lse_part;             // [rows, parts]
+    // the requests' own keys: partial rows of the split kernel
+    const float* o_own;          // [rows, own_splits, 512]
+    const float* lse_own;        // [rows, own_splits]
+    int32_t own_splits;          // 0: no request has keys of its own
+    float own_scale;             // o_own's units -> output units
+    uint16_t* o;                 // bf16 [rows, 512]
+    float* lse;                  // fp32 [rows] or NULL
+    long long wait_limit;
+    int32_t stall_probe;
+};
+
+// The operand images of the prefix and the queries, and the prefix's partials.
+cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream);
+// Merge of the prefix's and the requests' own partials into o and lse.
+cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
+
 // MLA_OK when the current device is one the library runs on, else a status.
 int device_ok();
 

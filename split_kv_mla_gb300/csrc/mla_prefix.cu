@@ -1,0 +1,880 @@
+// mla_prefix.cu -- decode of a batch whose requests share a prefix: the
+// prefix's keys are attended once by the query rows of the whole batch, 64 rows
+// per tile, instead of once per request.  See mla_prefix_decode in
+// include/mla_decode.h for the contract.
+//
+// Three kernels here (the requests' own keys go through the split kernel):
+//
+// * prepare: gathers the prefix's rows through its slot list into 128-key
+//   blocks laid out exactly as the MMA reads them (mla_layout.cuh), and splits
+//   each query row into two e4m3 terms the same way.  Both are then fetched with
+//   plain bulk copies of whole 16 KB chunks: a row gather cannot feed 64-row
+//   tiles (160 tile::gather4 copies of a block take ~3,800 cycles, a block's
+//   MMAs 2,700), and every tile reads the same blocks.
+// * prefix_split: per CTA a range of (tile, block) pairs.
+//     S^T[128 keys x 128] = K[128 x 576] . [q_hi | q_lo]^T      one MMA chain
+//     p = 2^(s - m),  O^T[512 x 64] += V^T[512 x 128] . (p_hi + p_lo)
+//   with K and V e4m3 as they are stored.  A query row, scaled to max |q| in
+//   [128, 256), is q_hi + 2^-5 q_lo, both e4m3: exact for a bf16 element within
+//   2^-14 of the row's maximum and within 2^-23 of that maximum below.
+//   p = p_hi + p_lo is an e4m3 term and the residual in e5m2, whose 2^-16
+//   smallest step lets both terms accumulate into the same columns without a
+//   scale of their own (a second set of columns does not fit: O^T takes 256 of
+//   TMEM's 512 columns at 64 rows, the two S^T buffers the others).  The pair
+//   carries about seven bits down to 2^-14 of p's unit, two more than that
+//   below the row's reference, where bf16 carries eight.
+// * prefix_merge: joins a row's partials by their base-2 LSEs.
+//
+// What bounds the split kernel: an MMA with N = 64 waits for its A operand from
+// shared memory (4 KB a K-step of 32 at 128 bytes a cycle, and 2 KB of B: 48
+// cycles for 32 cycles of multiplying).  QK stacks both terms along N (128
+// columns, 64 cycles, A read once); P.V cannot.  A block of 128 keys and 64 rows
+// so costs 18 x 64 + 32 x 48 = 2,688 cycles of the tensor pipe against 2,176 at
+// the bf16 rate.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "mla_internal.h"
+#include "mla_layout.cuh"
+#include "mla_sm100.cuh"
+#include "mla_softmax.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kDv = 512, kDr = 64, kWidth = kDv + kDr;
+constexpr int kRows = kPrefixRows;
+constexpr int kKeys = kPrefixKeys;
+constexpr int kChunk = kKeys * 128;           // bytes of one 128-column chunk of 128 rows
+constexpr int kRopeBytes = kKeys * 64;
+static_assert(4 * kChunk + kRopeBytes == kPrefixImage, "image of a block or a query tile");
+static_assert(2 * kRows == kKeys, "a query tile's two terms have a block's layout");
+constexpr int kQLoBits = 5;                   // q_lo is stored times 2^5
+constexpr float kQLoBack = 1.f / (1 << kQLoBits);
+
+// A grid kernel launched as a programmatic dependent of its predecessor.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
+                       cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// The prefix's length: the device value clamped to its list (prepare reports one
+// outside), or the list's own length.
+__device__ __forceinline__ int64_t prefix_length(const PrefixArgs& a)
+{
+    if (a.prefix_len == nullptr) return a.prefix_cap;
+    const int64_t n = __ldcg(a.prefix_len);
+    return n < 0 ? 0 : n > a.prefix_cap ? a.prefix_cap : n;
+}
+
+// The (tile, block) pairs, tile-major, are dealt out in equal runs: CTA g takes
+// pairs [g U / G, (g + 1) U / G) of U on G <= U CTAs.  With G a multiple of the
+// tile count the runs end at tile borders.  The CTA of pair u:
+__device__ __forceinline__ int64_t cta_of(int64_t u, int64_t U, int64_t G)
+{
+    return ((u + 1) * G - 1) / U;
+}
+
+// ---- prepare ----------------------------------------------------------------------------------
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepKeys = 32;     // keys per CTA
+constexpr int kPrepRows = kPrepThreads / 32;   // query rows per CTA, one per warp
+
+// Keys 32 c .. 32 c + 31 of the prefix into their block's image.
+__device__ void prepare_keys(const PrefixArgs& a, int64_t c)
+{
+    __shared__ int32_t slots[kPrepKeys];
+    const int tid = threadIdx.x;
+    const int64_t len = prefix_length(a);
+    const int64_t k0 = c * kPrepKeys;
+    if (c == 0 && tid == 0 && a.prefix_len != nullptr && __ldcg(a.prefix_len) != len)
+        atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
+    if (k0 >= (len + kKeys - 1) / kKeys * kKeys) return;   // past the last block
+    if (tid < kPrepKeys) {
+        int32_t s = k0 + tid < len ? __ldg(a.prefix_indices + k0 + tid) : -1;
+        if (k0 + tid < len && (s < 0 || s >= a.pool_rows)) {
+            atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
+            s = -1;
+        }
+        slots[tid] = s;
+        const uint32_t valid = __ballot_sync(0xffffffffu, s >= 0);
+        if (tid == 0) a.k_valid[c] = valid;
+    }
+    __syncthreads();
+    uint8_t* image = a.k_image + k0 / kKeys * kPrefixImage;
+    const int row0 = (int)(k0 % kKeys);
+    constexpr int kPieces = kWidth / 16;
+    constexpr int kPer = (kPrepKeys * kPieces + kPrepThreads - 1) / kPrepThreads;
+    uint4 v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int p = tid + i * kPrepThreads, row = p / kPieces;
+        v[i] = make_uint4(0, 0, 0, 0);   // keys that are masked become zero rows
+        if (p < kPrepKeys * kPieces && slots[row] >= 0)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(a.pool + (int64_t)slots[row] * kWidth) +
+                         p % kPieces);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int p = tid + i * kPrepThreads, row = p / kPieces;
+        if (p < kPrepKeys * kPieces)
+            *reinterpret_cast<uint4*>(image + tile_offset(row0 + row, p % kPieces * 16, kKeys)) =
+                v[i];
+    }
+}
+
+// Query row `item` (one warp) into its tile's image, rows 0..63 the high terms
+// and 64..127 the low ones; its logit scale and the prefix positions it sees.
+__device__ void prepare_query(const PrefixArgs& a, int64_t item)
+{
+    const int lane = threadIdx.x & 31;
+    if (item >= (int64_t)a.tiles * kRows) return;
+    const bool on = item < a.rows;
+    constexpr int kGroups = kWidth / 8;   // 8-column groups
+    constexpr int kVec = (kGroups + 31) / 32;
+    uint4 v[kVec];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int c = (lane + 32 * i) * 8;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (on && c < kWidth)
+            v[i] = c < kDv ? __ldg(reinterpret_cast<const uint4*>(a.q_lat + item * kDv + c))
+                           : __ldg(reinterpret_cast<const uint4*>(a.q_pe + item * kDr + (c - kDv)));
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
+                                     fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const int sh = q_shift(amax);
+    uint8_t* image = a.q_image + item / kRows * kPrefixImage;
+    const int row = (int)(item % kRows);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int c = (lane + 32 * i) * 8;
+        if (c >= kWidth) continue;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint16_t h[4], l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            split_pair<kQLoBits>(mul_pow2(__uint_as_float(w[k] << 16), sh),
+                                 mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh), h[k], l[k]);
+        *reinterpret_cast<uint2*>(image + tile_offset(row, c, kKeys)) =
+            make_uint2((uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16));
+        *reinterpret_cast<uint2*>(image + tile_offset(kRows + row, c, kKeys)) =
+            make_uint2((uint32_t)l[0] | ((uint32_t)l[1] << 16), (uint32_t)l[2] | ((uint32_t)l[3] << 16));
+    }
+    if (lane == 0) {
+        int64_t win = 0;
+        if (on) {
+            // draft row t sees positions <= P + S_b - q_len + t: all of the
+            // prefix unless the request's own keys are fewer than the drafts
+            const int64_t r = item / a.num_heads;
+            const int b = (int)(r / a.q_len), t = (int)(r % a.q_len);
+            const int cap = __ldg(a.kv_indptr + b + 1) - __ldg(a.kv_indptr + b);
+            const int len = min(max(__ldg(a.seq_lens + b), 0), max(cap, 0));
+            const int64_t P = prefix_length(a);
+            win = min(P, max((int64_t)0, P + len - a.q_len + t + 1));
+        }
+        a.q_scale[item] = on ? mul_pow2(a.logit_scale, -sh) : 0.f;
+        a.q_window[item] = (int32_t)win;
+    }
+}
+
+__global__ void __launch_bounds__(kPrepThreads)
+prefix_prepare_kernel(const PrefixArgs a, uint32_t key_ctas)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.x < key_ctas) prepare_keys(a, blockIdx.x);
+    else prepare_query(a, (int64_t)(blockIdx.x - key_ctas) * kPrepRows + (threadIdx.x >> 5));
+}
+
+// ---- prefix_split -----------------------------------------------------------------------------
+//
+// Warp 0 loads, warp 1 issues the MMAs, warps 4-11 are two softmax sets of four
+// warps; set s owns query rows 32 s .. 32 s + 31, warp w % 4 of a set the TMEM
+// lanes (keys) 32 (w % 4) .. + 31, one key per thread, as in the split kernel.
+// Warps 2-3 complete their warpgroup.
+//
+// A stage's four latent chunks are released one by one, as the P.V MMAs of that
+// chunk finish, so the next block's chunks stream in behind them; the RoPE
+// chunk, which only QK reads, has one buffer.  QK of block j + 1 runs while the
+// softmax works on block j, and P.V of block j - 1 before it.
+
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kSoftmaxWarp0 = 4;
+constexpr int kSets = 2, kSetRows = kRows / kSets;
+constexpr int kSoftmaxWarps = 4 * kSets;
+// 168 registers a thread at launch (384 x 168 <= 65536); the first warpgroup
+// gives back what the softmax warpgroups take.
+constexpr uint32_t kRegsLow = 56, kRegsHigh = 224;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split");
+
+// Softmax constants, in base-2 logit units: a row's reference moves when a
+// logit passes it by more than kTau, then to the block's maximum plus
+// kHeadroom; p is fed as 2^(s - m + kShift) <= 2^8.75 < 448.
+constexpr float kTau = 2.75f, kShift = 6.f, kHeadroom = 1.f;
+constexpr float kTop = kTau + kShift;
+
+constexpr int kOffRope = 2 * 4 * kChunk;
+constexpr int kOffQ = kOffRope + kRopeBytes;
+constexpr int kOffP = kOffQ + (int)kPrefixImage;
+constexpr int kPTerm = kKeys * kRows;            // bytes of one term of P^T
+constexpr int kOffMisc = kOffP + 2 * kPTerm;
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+static_assert(kRows * kDv * 4 <= kOffRope, "the epilogue stages its rows in the idle stages");
+
+struct PrefixShared {
+    uint64_t k_full[2][4], k_empty[2][4];   // per stage and chunk
+    uint64_t r_full, r_empty, q_full;
+    uint64_t s_full[2], s_free[2];
+    uint64_t p_full, pv_done;
+    uint64_t mma_drain;   // after an abort: every MMA issued has completed
+    uint64_t never;       // tests of the timeout path
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) float cq[kRows];
+    alignas(16) int win[kRows];
+    float red[kSoftmaxWarps][32];
+    float redt[kSoftmaxWarps][32];
+};
+constexpr int kSmemBytes = kOffMisc + (int)sizeof(PrefixShared);
+static_assert(kSmemBytes <= 227 * 1024, "one CTA's dynamic shared memory limit");
+
+// p (two rows) as an e4m3 term and the residual as an e5m2 term; returns the
+// sums that the MMA will see.  fp16 holds p <= 448 and the residual exactly
+// enough: p to 2^-12 of itself, the difference exactly.
+__device__ __forceinline__ float2 split_p(float a, float b, uint16_t& hi, uint16_t& lo)
+{
+    uint32_t p, back, rest, low, sum;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(p));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(p), "r"(back));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(low) : "h"(lo));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(sum) : "r"(back), "r"(low));
+    return __half22float2(*reinterpret_cast<const __half2*>(&sum));
+}
+
+// One run of blocks [b0, b1) of tile `tile`; `j0` blocks went before in this CTA
+// (the pipeline's phases go on counting).  Roles as above.  False after an abort.
+struct Run {
+    int64_t tile;
+    int b0, b1;
+    int part;      // which of the tile's partials this run is
+    int64_t j0;
+    int run;       // index of the run in this CTA
+};
+
+__device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, PrefixShared& ms,
+                                          const Run& r, int lane)
+{
+    volatile int* abort_flag = &ms.abort;
+    const int n = r.b1 - r.b0;
+    int64_t issued = 0, ropes = 0;   // latent chunks and RoPE chunks of this run
+    if (lane == 0) {
+        mbar_arrive_expect_tx(&ms.q_full, (uint32_t)kPrefixImage);
+        bulk_load(smem + kOffQ, a.q_image + r.tile * kPrefixImage, (uint32_t)kPrefixImage,
+                  &ms.q_full);
+    }
+    bool ok = true;
+    for (int j = 0; j < n && ok; ++j) {
+        const int64_t jj = r.j0 + j;
+        const int st = (int)(jj & 1);
+        const uint8_t* src = a.k_image + (int64_t)(r.b0 + j) * kPrefixImage;
+        for (int c = 0; c < 4 && ok; ++c) {
+            if (jj >= 2)
+                ok = warp_wait(&ms.k_empty[st][c], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
+                               a.wait_limit);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ms.k_full[st][c], kChunk);
+                bulk_load(smem + st * 4 * kChunk + c * kChunk, src + c * kChunk, kChunk,
+                          &ms.k_full[st][c]);
+            }
+            ++issued;
+        }
+        if (!ok) break;
+        if (jj >= 1)
+            ok = warp_wait(&ms.r_empty, (uint32_t)(jj - 1) & 1, abort_flag, 0, a.wait_limit);
+        if (!ok) break;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&ms.r_full, kRopeBytes);
+            bulk_load(smem + kOffRope, src + 4 * kChunk, kRopeBytes, &ms.r_full);
+        }
+        ++ropes;
+    }
+    // Never go on with copies in flight: the last two blocks' chunks, the RoPE
+    // chunk and the query tile must land.  A fresh flag and the full bound keep
+    // this going after an abort; otherwise they have landed long ago or soon will.
+    volatile int drain = 0;
+    for (int64_t i = issued > 8 ? issued - 8 : 0; i < issued; ++i) {
+        const int64_t jj = r.j0 + (i >> 2);
+        warp_wait(&ms.k_full[jj & 1][i & 3], (uint32_t)(jj >> 1) & 1, &drain);
+    }
+    if (ropes > 0) warp_wait(&ms.r_full, (uint32_t)(r.j0 + ropes - 1) & 1, &drain);
+    warp_wait(&ms.q_full, (uint32_t)r.run & 1, &drain);
+}
+
+__device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base, uint32_t tmem,
+                                         PrefixShared& ms, const Run& r)
+{
+    volatile int* abort_flag = &ms.abort;
+    const int n = r.b1 - r.b0;
+    constexpr uint32_t id_qk = idesc_e4m3(128, 2 * kRows, false, false);
+    constexpr uint32_t id_hi = idesc_e4m3(128, kRows, true, true);
+    constexpr uint32_t id_lo = idesc_e4m3(128, kRows, true, true, true);
+    const uint64_t k_lat = smem_desc(smem_base, 16, 1024, kSw128);
+    const uint64_t k_rope = smem_desc(smem_base + kOffRope, 16, 512, kSw64);
+    const uint64_t q_lat = smem_desc(smem_base + kOffQ, 16, 1024, kSw128);
+    const uint64_t q_rope = smem_desc(smem_base + kOffQ + 4 * kChunk, 16, 512, kSw64);
+    const uint64_t v_lat = smem_desc(smem_base, kChunk, 1024, kSw128);
+    const uint64_t p_hi = smem_desc(smem_base + kOffP, 128, 2048, kSwNone);
+    const uint64_t p_lo = smem_desc(smem_base + kOffP + kPTerm, 128, 2048, kSwNone);
+    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __shfl_sync(0xffffffffu, mbar_try_wait(bar, parity) ? 1 : 0, 0) != 0;
+    };
+    bool ok = warp_wait(&ms.q_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+    int next_qk = 0, next_pv = 0;
+    long long t_last = clock64();
+    for (uint32_t idle = 0; ok && next_pv < n;) {
+        bool did = false;
+        const int64_t jp = r.j0 + next_pv, jq = r.j0 + next_qk;
+        if (next_pv < next_qk && ready(&ms.p_full, (uint32_t)jp & 1)) {
+            tc_fence_after();
+            const int st = (int)(jp & 1);
+            const uint64_t v0 = v_lat + (uint64_t)((st * 4 * kChunk) >> 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint64_t v = v0 + (uint64_t)((c * kChunk + kk * 4096) >> 4);
+                    const uint64_t off = (uint64_t)((kk * 512) >> 4);
+                    const uint32_t d = tmem + kColO + c * kRows;
+                    umma_f8_warp(d, v, p_hi + off, id_hi, (next_pv > 0 || kk > 0) ? 1u : 0u);
+                    umma_f8_warp(d, v, p_lo + off, id_lo, 1u);
+                }
+                umma_commit_warp(&ms.k_empty[st][c]);
+            }
+            umma_commit_warp(&ms.pv_done);
+            ++next_pv;
+            did = true;
+        }
+        if (next_qk < n) {
+            const int st = (int)(jq & 1);
+            const uint32_t ph = (uint32_t)(jq >> 1) & 1;
+            if (ready(&ms.k_full[st][0], ph) &&
+                (jq < 2 || ready(&ms.s_free[st], (uint32_t)((jq - 2) >> 1) & 1))) {
+                tc_fence_after();
+                const uint64_t soff = (uint64_t)((st * 4 * kChunk) >> 4);
+                const uint32_t d = tmem + kColS + st * 2 * kRows;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c > 0 && ok)
+                        ok = warp_wait(&ms.k_full[st][c], ph, abort_flag, 0, a.wait_limit);
+                    if (ok) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f8_warp(d, k_lat + soff + (uint64_t)((c * kChunk + kk * 32) >> 4),
+                                         q_lat + (uint64_t)((c * kChunk + kk * 32) >> 4), id_qk,
+                                         (c > 0 || kk > 0) ? 1u : 0u);
+                    }
+                }
+                if (ok) ok = warp_wait(&ms.r_full, (uint32_t)jq & 1, abort_flag, 0, a.wait_limit);
+                if (!ok) break;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    umma_f8_warp(d, k_rope + (uint64_t)((kk * 32) >> 4),
+                                 q_rope + (uint64_t)((kk * 32) >> 4), id_qk, 1u);
+                umma_commit_warp(&ms.s_full[st]);
+                umma_commit_warp(&ms.r_empty);
+                ++next_qk;
+                did = true;
+            }
+        }
+        if (did) {
+            idle = 0;
+            continue;
+        }
+        if ((++idle & 63u) == 0) {
+            const long long now = clock64();
+            if (__shfl_sync(0xffffffffu, *abort_flag, 0) != 0) break;
+            if (idle == 64) t_last = now;   // first check of this idle stretch
+            else if (__shfl_sync(0xffffffffu, now - t_last > a.wait_limit ? 1 : 0, 0) != 0) {
+                *abort_flag = 1;
+                break;
+            }
+        }
+    }
+    // After an abort, MMAs already issued may still be running: wait for them
+    // (with the full bound) before the CTA releases TMEM and its stages.
+    if (__shfl_sync(0xffffffffu, *abort_flag != 0 ? 1 : 0, 0) != 0) {
+        umma_commit_warp(&ms.mma_drain);
+        volatile int drain = 0;
+        warp_wait(&ms.mma_drain, 0, &drain);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem, uint32_t tmem,
+                                             PrefixShared& ms, const Run& r, int warp, int lane)
+{
+    constexpr int R = kSetRows;
+    volatile int* abort_flag = &ms.abort;
+    const int set = (warp - kSoftmaxWarp0) / 4;
+    const int quad = warp & 3;
+    const uint32_t bar_id = 1u + (uint32_t)set;
+    const int r0 = set * R;
+    const int ti = quad * 32 + lane;                  // key within a block == TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    float* red = &ms.red[set * 4][0];
+    float* redt = &ms.redt[set * 4][0];
+    const int n = r.b1 - r.b0;
+
+    // the rows' logit scales and windows (every set its own rows)
+    if (ti < R) {
+        ms.cq[r0 + ti] = __ldcg(a.q_scale + r.tile * kRows + r0 + ti);
+        ms.win[r0 + ti] = __ldcg(a.q_window + r.tile * kRows + r0 + ti);
+    }
+    softmax_bar(bar_id);
+    int win_min = ms.win[r0 + lane];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        win_min = min(win_min, __shfl_xor_sync(0xffffffffu, win_min, off));
+
+    // x = logit - m + kShift, nm = kShift - m; a row without a reference yet
+    // (bit of `unset`, the same in every thread of the set) has nm = 0
+    float nm[R], l[R], lt[R];
+    uint32_t unset = 0xffffffffu;
+#pragma unroll
+    for (int k = 0; k < R; ++k) nm[k] = l[k] = lt[k] = 0.f;
+    bool alive = true;
+    if (a.stall_probe) warp_wait(&ms.never, 0, abort_flag, 0, a.wait_limit);
+    uint32_t vnext = __ldcg(a.k_valid + (int64_t)r.b0 * 4 + quad);
+    for (int j = 0; j < n; ++j) {
+        const int64_t jj = r.j0 + j;
+        const int st = (int)(jj & 1);
+        const uint32_t valid = vnext;
+        if (j + 1 < n) vnext = __ldcg(a.k_valid + (int64_t)(r.b0 + j + 1) * 4 + quad);
+        const bool ok = warp_wait(&ms.s_full[st], (uint32_t)(jj >> 1) & 1, abort_flag, 0,
+                                  a.wait_limit);
+        float x[R];
+        if (ok) {
+            tc_fence_after();
+            const uint32_t sa = lanes + kColS + st * 2 * kRows + r0;
+            uint32_t h0[16], l0[16], h1[16], l1[16];
+            tmem_ld16(sa, h0);
+            tmem_ld16(sa + kRows, l0);
+            tmem_ld16(sa + 16, h1);
+            tmem_ld16(sa + kRows + 16, l1);
+            tmem_wait_ld();
+            reg_fence(h0);
+            reg_fence(l0);
+            reg_fence(h1);
+            reg_fence(l1);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                x[k] = fmaf(__uint_as_float(l0[k]), kQLoBack, __uint_as_float(h0[k]));
+                x[16 + k] = fmaf(__uint_as_float(l1[k]), kQLoBack, __uint_as_float(h1[k]));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < R; ++k) x[k] = -CUDART_INF_F;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_free[st]);
+#pragma unroll
+        for (int g = 0; g < R / 4; ++g) {
+            const float4 c = reinterpret_cast<const float4*>(ms.cq + r0)[g];
+            x[4 * g] = fmaf(x[4 * g], c.x, nm[4 * g]);
+            x[4 * g + 1] = fmaf(x[4 * g + 1], c.y, nm[4 * g + 1]);
+            x[4 * g + 2] = fmaf(x[4 * g + 2], c.z, nm[4 * g + 2]);
+            x[4 * g + 3] = fmaf(x[4 * g + 3], c.w, nm[4 * g + 3]);
+        }
+        // masked: keys past the prefix or with a bad slot, and in the blocks past
+        // the shortest row's window the positions that a row does not see
+        const int pos = (r.b0 + j) * kKeys + ti;
+        if (valid != 0xffffffffu || (r.b0 + j + 1) * kKeys > win_min) {
+            const bool kval = (valid >> lane) & 1u;
+#pragma unroll
+            for (int g = 0; g < R / 4; ++g) {
+                const int4 w = reinterpret_cast<const int4*>(ms.win + r0)[g];
+                x[4 * g] = kval && pos < w.x ? x[4 * g] : -CUDART_INF_F;
+                x[4 * g + 1] = kval && pos < w.y ? x[4 * g + 1] : -CUDART_INF_F;
+                x[4 * g + 2] = kval && pos < w.z ? x[4 * g + 2] : -CUDART_INF_F;
+                x[4 * g + 3] = kval && pos < w.w ? x[4 * g + 3] : -CUDART_INF_F;
+            }
+        }
+        float top = x[0];
+#pragma unroll
+        for (int k = 1; k < R; ++k) top = fmaxf(top, x[k]);
+        bool need = top > kTop || !ok;
+        if (unset != 0) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) need |= ((unset >> k) & 1u) && x[k] > -CUDART_INF_F;
+        }
+        if (softmax_bar_or(bar_id, need)) {
+            // (bar.red above also tells of a warp that gave up)
+            if (softmax_bar_or(bar_id, !ok || *abort_flag)) {
+                alive = false;
+                break;
+            }
+            float v[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) v[k] = x[k];
+            red[quad * 32 + lane] = warp_transpose_reduce<R, true>(v, lane);
+            softmax_bar(bar_id);
+            uint32_t moved = 0;   // rows whose sums so far shrink
+            float shrink[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const float bm = fmaxf(fmaxf(red[k], red[32 + k]), fmaxf(red[64 + k], red[96 + k]));
+                const bool first = (unset >> k) & 1u;
+                shrink[k] = 1.f;
+                if (first ? bm > -CUDART_INF_F : bm > kTop) {
+                    const float delta = (kShift - kHeadroom) - bm;
+                    nm[k] += delta;
+                    x[k] += delta;
+                    unset &= ~(1u << k);
+                    if (!first) {
+                        shrink[k] = exp2f(delta);
+                        moved |= 1u << k;
+                        l[k] *= shrink[k];
+                        lt[k] *= shrink[k];
+                    }
+                }
+            }
+            if (moved != 0 &&
+                warp_wait(&ms.pv_done, (uint32_t)(jj - 1) & 1, abort_flag, 0, a.wait_limit)) {
+                // O^T holds the blocks before: scale the moved rows' columns
+                tc_fence_after();
+#pragma unroll 1
+                while (moved != 0) {
+                    const int row = __ffs(moved) - 1;
+                    moved &= moved - 1;
+                    float f = 1.f;
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+                        if (k == row) f = shrink[k];
+                    uint32_t o[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[c] = tmem_ld1(lanes + kColO + c * kRows + r0 + row);
+                    tmem_wait_ld();
+                    reg_fence(o);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_st1(lanes + kColO + c * kRows + r0 + row,
+                                 __float_as_uint(__uint_as_float(o[c]) * f));
+                }
+                tmem_wait_st();
+            }
+            softmax_bar(bar_id);   // `red` is free again
+        }
+        // P^T is stored as 16-row columns of 128 keys x 16 bytes, e4m3 terms
+        // then e5m2 terms
+        uint32_t hw[R / 4], lw[R / 4];
+#pragma unroll
+        for (int k = 0; k < R; k += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[k + u] = ex2_approx(x[k + u]);
+                l[k + u] += x[k + u];
+            }
+            uint16_t h0, l0, h1, l1;
+            const float2 t0 = split_p(x[k], x[k + 1], h0, l0);
+            const float2 t1 = split_p(x[k + 2], x[k + 3], h1, l1);
+            lt[k] += t0.x;
+            lt[k + 1] += t0.y;
+            lt[k + 2] += t1.x;
+            lt[k + 3] += t1.y;
+            hw[k / 4] = (uint32_t)h0 | ((uint32_t)h1 << 16);
+            lw[k / 4] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+        }
+        // the buffer is free when the P.V of the block before has finished
+        if (jj >= 1)
+            warp_wait(&ms.pv_done, (uint32_t)(jj - 1) & 1, abort_flag, 0, a.wait_limit);
+        uint8_t* prow = smem + kOffP + ti * 16 + (r0 / 16) * 2048;
+#pragma unroll
+        for (int g = 0; g < R / 16; ++g) {
+            *reinterpret_cast<uint4*>(prow + g * 2048) =
+                make_uint4(hw[4 * g], hw[4 * g + 1], hw[4 * g + 2], hw[4 * g + 3]);
+            *reinterpret_cast<uint4*>(prow + kPTerm + g * 2048) =
+                make_uint4(lw[4 * g], lw[4 * g + 1], lw[4 * g + 2], lw[4 * g + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full);
+    }
+
+    // ---- epilogue: sums over the keys, then the rows out of TMEM, normalised by
+    // what the MMA consumed (lt), and the LSE from the exact p (l) -------------------------
+    red[quad * 32 + lane] = warp_transpose_reduce<R, false>(l, lane);
+    redt[quad * 32 + lane] = warp_transpose_reduce<R, false>(lt, lane);
+    const bool have = alive && warp_wait(&ms.pv_done, (uint32_t)(r.j0 + n - 1) & 1, abort_flag, 0,
+                                         a.wait_limit);
+    if (have) tc_fence_after();
+    softmax_bar(bar_id);
+    float* stage = reinterpret_cast<float*>(smem);   // fp32 [64][512]
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (have) {
+            tmem_ld32(lanes + kColO + c * kRows + r0, o);
+            tmem_wait_ld();
+            reg_fence(o);
+        } else {
+#pragma unroll
+            for (int k = 0; k < R; ++k) o[k] = 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const float t = (redt[k] + redt[32 + k]) + (redt[64 + k] + redt[96 + k]);
+            stage[(r0 + k) * kDv + c * 128 + ti] =
+                t > 0.f ? __uint_as_float(o[k]) * rcp_approx(t) : 0.f;
+        }
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();
+    softmax_bar(bar_id);
+    if (ti < R) {
+        const int64_t item = r.tile * kRows + r0 + ti;
+        if (item < a.rows) {
+            const float sum = (red[ti] + red[32 + ti]) + (red[64 + ti] + red[96 + ti]);
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (k == ti) m = nm[k];
+            const int64_t at = item * a.parts + r.part;
+            a.lse_part[at] = sum > 0.f ? log2f(sum) - m : -CUDART_INF_F;
+            bulk_store(a.o_part + at * kDv, stage + (r0 + ti) * kDv, kDv * 4);
+            bulk_commit();
+            bulk_wait_read();
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_split_kernel(const PrefixArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PrefixShared& ms = *reinterpret_cast<PrefixShared*>(smem + kOffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the next kernel (the requests' own keys) may be scheduled as SMs fall idle
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            for (int c = 0; c < 4; ++c) {
+                mbar_init(&ms.k_full[i][c], 1);
+                mbar_init(&ms.k_empty[i][c], 1);
+            }
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.s_free[i], kSoftmaxWarps);
+        }
+        mbar_init(&ms.r_full, 1);
+        mbar_init(&ms.r_empty, 1);
+        mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.p_full, kSoftmaxWarps);
+        mbar_init(&ms.pv_done, 1);
+        mbar_init(&ms.mma_drain, 1);
+        mbar_init(&ms.never, 1);
+        ms.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ms.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    // the images come from the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem_base;
+    const uint32_t smem_base = smem_u32(smem);
+
+    const int64_t blocks = (prefix_length(a) + kKeys - 1) / kKeys;
+    const int64_t U = blocks * a.tiles, G = min((int64_t)gridDim.x, U), g = blockIdx.x;
+    const int64_t u_begin = g < G ? g * U / G : 0, u_end = g < G ? (g + 1) * U / G : 0;
+    auto run_at = [&](int64_t u, int64_t j0, int idx) {
+        Run r;
+        r.tile = u / blocks;
+        r.b0 = (int)(u % blocks);
+        r.b1 = (int)min(blocks, r.b0 + (u_end - u));
+        r.part = (int)(g - cta_of(r.tile * blocks, U, G));
+        r.j0 = j0;
+        r.run = idx;
+        return r;
+    };
+    // Registers move from the first warpgroup to the softmax warpgroups; each
+    // branch below holds all of its warpgroups' remaining code.  Every thread
+    // meets at the barrier that ends a run.
+    if (warp < kSoftmaxWarp0) {
+        regs_lower<kRegsLow>();
+        int64_t j0 = 0;
+        int idx = 0;
+        for (int64_t u = u_begin; u < u_end;) {
+            const Run r = run_at(u, j0, idx);
+            if (warp == kLoadWarp) load_role(a, smem, ms, r, lane);
+            else if (warp == kMmaWarp) mma_role(a, smem_base, tmem, ms, r);
+            tc_fence_before();
+            const bool stop = __syncthreads_or(ms.abort);
+            tc_fence_after();
+            if (stop) break;
+            u += r.b1 - r.b0;
+            j0 += r.b1 - r.b0;
+            ++idx;
+        }
+    } else {
+        regs_raise<kRegsHigh>();
+        int64_t j0 = 0;
+        int idx = 0;
+        for (int64_t u = u_begin; u < u_end;) {
+            const Run r = run_at(u, j0, idx);
+            softmax_role(a, smem, tmem, ms, r, warp, lane);
+            tc_fence_before();
+            const bool stop = __syncthreads_or(ms.abort);
+            tc_fence_after();
+            if (stop) break;
+            u += r.b1 - r.b0;
+            j0 += r.b1 - r.b0;
+            ++idx;
+        }
+    }
+    if (tid == 0 && ms.abort) atomicOr(a.err, MLA_DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---- prefix_merge -----------------------------------------------------------------------------
+//
+// One CTA per output row, four columns per thread.  The row's partials are the
+// prefix's (as many as CTAs took part of its tile) and the requests' own (one
+// per split): M = max lse, w = 2^(lse - M), o = sum w o_s / sum w, summed in
+// increasing order, lse = M + log2 sum w.  A partial of weight 0 is not read.
+
+constexpr int kMergeThreads = 128;
+constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;
+constexpr int kMergeAhead = 4;   // partials loaded before the weights are known
+
+__global__ void __launch_bounds__(kMergeThreads)
+prefix_merge_kernel(const PrefixArgs a)
+{
+    __shared__ float w_s[kMergeMax];
+    __shared__ float sum_s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t item = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
+    int np = 0;
+    const int64_t blocks = (prefix_length(a) + kKeys - 1) / kKeys;
+    if (blocks > 0 && a.parts > 0) {
+        const int64_t U = blocks * a.tiles, G = min((int64_t)a.ctas, U), tile = item / kRows;
+        np = (int)(cta_of((tile + 1) * blocks - 1, U, G) - cta_of(tile * blocks, U, G)) + 1;
+    }
+    const int n = np + a.own_splits;
+    const float* own = a.o_own + item * a.own_splits * kDv;
+    const float* part = a.o_part + item * a.parts * kDv;
+    const int c = tid * 4;
+    auto row_of = [&](int i) { return i < np ? part + (int64_t)i * kDv : own + (int64_t)(i - np) * kDv; };
+    float4 v[kMergeAhead];
+#pragma unroll
+    for (int i = 0; i < kMergeAhead; ++i)
+        if (i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(i) + c));
+    if (tid < 32) {
+        float m = -CUDART_INF_F;
+        for (int i = lane; i < n; i += 32) {
+            const float l = i < np ? __ldcg(a.lse_part + item * a.parts + i)
+                                   : __ldcg(a.lse_own + item * a.own_splits + (i - np));
+            w_s[i] = l;
+            m = fmaxf(m, l);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        float sum = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float w = w_s[i] == -CUDART_INF_F ? 0.f : exp2f(w_s[i] - m);
+            sum += w;
+            w_s[i] = w * (i < np ? a.kv_scale : a.own_scale);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) {
+            sum_s = sum;
+            if (a.lse != nullptr) a.lse[item] = sum > 0.f ? m + log2f(sum) : -CUDART_INF_F;
+        }
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, float4 x) {
+        if (w != 0.f) {
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kMergeAhead; ++i)
+        if (i < n) add(w_s[i], v[i]);
+    for (int i = kMergeAhead; i < n; ++i)
+        add(w_s[i], __ldcg(reinterpret_cast<const float4*>(row_of(i) + c)));
+    const float f = sum_s > 0.f ? 1.f / sum_s : 0.f;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(a.o + item * kDv + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream)
+{
+    static DeviceOnce once;
+    cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(prefix_split_kernel,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (a.prefix_cap + kKeys - 1) / kKeys;
+    const uint32_t key_ctas = (uint32_t)(blocks * (kKeys / kPrepKeys));
+    const int64_t ctas = key_ctas + (int64_t)a.tiles * (kRows / kPrepRows);
+    e = launch_pdl(prefix_prepare_kernel, dim3((unsigned)ctas), kPrepThreads, 0, stream, a, key_ctas);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefix_split_kernel, dim3((unsigned)a.ctas), kThreads, kSmemBytes, stream, a);
+}
+
+cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream)
+{
+    return launch_pdl(prefix_merge_kernel, dim3((unsigned)a.rows), kMergeThreads, 0, stream, a);
+}
+
+}  // namespace mla

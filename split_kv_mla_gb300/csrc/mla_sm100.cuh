@@ -138,6 +138,17 @@ __device__ __forceinline__ void tma_prefetch_desc(const void* tmap)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
+// Copy `bytes` contiguous bytes (a multiple of 16; both addresses 16-byte
+// aligned) from global to shared memory; completion counted on bar in bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Gather four rows (r0..r3) of a 2-D tensor map, columns [x, x + box width),
 // into four consecutive box rows at dst; completion counted on bar in bytes.
 __device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int32_t x, int32_t r0,
@@ -367,12 +378,14 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     return d;
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B and an fp32
-// accumulator; a_mn / b_mn select MN-major operands.
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n, bool a_mn, bool b_mn)
+// Instruction descriptor for kind::f8f6f4 with e4m3 A, e4m3 (or e5m2) B and an
+// fp32 accumulator; a_mn / b_mn select MN-major operands.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n, bool a_mn, bool b_mn,
+                                                  bool b_e5m2 = false)
 {
     return (1u << 4)                          // D format: f32
-           | (0u << 7) | (0u << 10)           // A, B format: e4m3
+           | (0u << 7)                        // A format: e4m3
+           | ((b_e5m2 ? 1u : 0u) << 10)       // B format: e4m3 or e5m2
            | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
            | ((n >> 3) << 17) | ((m >> 4) << 24);
 }

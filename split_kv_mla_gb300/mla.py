@@ -57,6 +57,14 @@ class mla_plan_t(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class mla_prefix_plan_t(ctypes.Structure):
+    _fields_ = [
+        ("tiles", ctypes.c_int32), ("ctas", ctypes.c_int32), ("parts", ctypes.c_int32),
+        ("sm_count", ctypes.c_int32), ("workspace_bytes", ctypes.c_int64),
+        ("prefix_cap", ctypes.c_int64), ("own", mla_plan_t),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -113,6 +121,11 @@ def load(build_if_missing: bool = True, path: Optional[str] = None):
             "mla_decode_dcp_splits": (ctypes.c_int, [P, vp, vp, vp, i64, vp, vp, vp, i32, i32,
                                                      i32, f32, f32, vp, i32, i32, i32, vp, vp,
                                                      vp, i64, vp]),
+            "mla_prefix_decode_plan": (ctypes.c_int, [i32, i32, i32, i64, i64, i32,
+                                                      ctypes.POINTER(mla_prefix_plan_t)]),
+            "mla_prefix_decode": (ctypes.c_int, [ctypes.POINTER(mla_prefix_plan_t), vp, vp, vp,
+                                                 i64, vp, vp, vp, vp, vp, i32, i32, i32, f32, f32,
+                                                 vp, vp, vp, i64, vp]),
             "mla_cache_append": (ctypes.c_int, [vp, i64, vp, i32, vp, vp, i64, i32, f32, vp, i64,
                                                 i64, vp, i32, i32, vp, vp, vp, vp, i64, i32, f32,
                                                 i32, i32, vp, i64, vp]),
@@ -481,6 +494,60 @@ def mla_decode_noalloc(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices
         _stream_ptr(stream))
     _check(rc, "mla_decode_noalloc")
     return o_lat, lse
+
+
+# ---- decode over a shared prefix -----------------------------------------------------
+
+def mla_prefix_decode_plan(batch: int, q_len: int, num_heads: int, prefix_cap: int,
+                           total_keys: int, sm_count: int) -> mla_prefix_plan_t:
+    """Plan of mla_prefix_decode: prefix_cap entries of prefix_indices and
+    total_keys of kv_indices (shapes)."""
+    p = mla_prefix_plan_t()
+    _check(load().mla_prefix_decode_plan(batch, q_len, num_heads, prefix_cap, total_keys,
+                                         sm_count, ctypes.byref(p)), "mla_prefix_decode_plan")
+    return p
+
+
+def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices, seq_lens,
+                      kv_indices, kv_indptr, scale: float, kv_scale: float, prefix_len=None,
+                      o=None, lse=None, workspace_t=None, stream=None, return_lse: bool = True):
+    """Dense decode of requests that share the prefix's slots and continue with
+    their own (seq_lens, kv_indices, kv_indptr); returns (o, lse).  prefix_len
+    int32 [1] on the device: how many of prefix_indices are in use (None: all)."""
+    _same_device(q_lat, q_pe=q_pe, pool=pool, prefix_indices=prefix_indices, seq_lens=seq_lens,
+                 kv_indices=kv_indices, kv_indptr=kv_indptr, prefix_len=prefix_len, o=o, lse=lse,
+                 workspace=workspace_t)
+    R, H = q_lat.shape[0], q_lat.shape[1]
+    batch = seq_lens.shape[0]
+    q_len = R // batch if batch else plan.own.q_len
+    p = _pool_2d(pool)
+    if (R != batch * q_len or q_lat.shape[2:] != (512,) or q_pe.shape != (R, H, 64) or
+            p.shape[-1] != 576 or kv_indptr.numel() != batch + 1):
+        raise ValueError("q_lat [B * q_len, H, 512], q_pe [B * q_len, H, 64], pool [N, 576] and "
+                         "kv_indptr [B + 1] must agree")
+    if prefix_indices.numel() != plan.prefix_cap or kv_indices.numel() < plan.own.total_keys:
+        raise ValueError("prefix_indices and kv_indices must have the plan's entries")
+    if o is None:
+        o = torch.empty_like(q_lat)
+    elif o.shape != q_lat.shape:
+        raise ValueError("o must have q_lat's shape")
+    if lse is None and return_lse:
+        lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
+    elif lse is not None and lse.numel() != R * H:
+        raise ValueError("lse must be [B * q_len, H]")
+    if workspace_t is None:
+        workspace_t = workspace(plan, q_lat.device)
+    i32 = torch.int32
+    _check(load().mla_prefix_decode(
+        ctypes.byref(plan), _dev_ptr(q_lat, "q_lat", torch.bfloat16),
+        _dev_ptr(q_pe, "q_pe", torch.bfloat16), p.data_ptr(), p.shape[0],
+        _dev_ptr(prefix_indices, "prefix_indices", i32), _dev_ptr(prefix_len, "prefix_len", i32),
+        _dev_ptr(seq_lens, "seq_lens", i32), _dev_ptr(kv_indices, "kv_indices", i32),
+        _dev_ptr(kv_indptr, "kv_indptr", i32), batch, q_len, H, float(scale), float(kv_scale),
+        _dev_ptr(o, "o", torch.bfloat16), _dev_ptr(lse, "lse", torch.float32),
+        _dev_ptr(workspace_t, "workspace"), workspace_t.numel(), _stream_ptr(stream)),
+        "mla_prefix_decode")
+    return o, lse
 
 
 # ---- the cache: append, fork, compact ------------------------------------------------

@@ -1,0 +1,327 @@
+"""GPU: decode over a shared prefix against the fp64 oracle on the joined page
+tables, with the framework's parity bar (gpu_util.compare).
+
+The bar holds by the number formats: a probability is an e4m3 term plus an e5m2
+term, off by at most 2^-4 2^-3 = 2^-7 of itself and 0.0014 in the mean square,
+normalised by the sum of what was fed, on top of the output's own bf16 rounding
+(2^-8 at most, 0.0017 in the mean square): about 0.0022 relative RMS against a
+bar of 0.005.  Logits carry the bf16 queries to 2^-23 of a row's largest element.
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import oracle
+from split_kv_mla_gb300 import inputs as gen
+from split_kv_mla_gb300 import mla
+
+from gpu_util import compare
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    oracle.build()
+    mla.load()
+
+
+@dataclasses.dataclass
+class Shared:
+    own: gen.DenseInputs        # the requests' own keys
+    joined: gen.DenseInputs     # the same requests with the prefix in front
+    prefix: torch.Tensor        # int32 [P]
+
+
+def join(own, prefix):
+    P = prefix.numel()
+    lens, at, parts = own.seq_lens.long(), own.kv_indptr.long(), []
+    for b in range(own.batch):
+        parts += [prefix, own.kv_indices[at[b]:at[b] + lens[b]]]
+    ptr = torch.zeros(own.batch + 1, dtype=torch.int64)
+    ptr[1:] = torch.cumsum(lens + P, 0)
+    return Shared(own, dataclasses.replace(
+        own, seq_lens=(lens + P).int(), kv_indices=torch.cat(parts).int(), kv_indptr=ptr.int()),
+        prefix.int())
+
+
+def make(q_len, heads, P, lens, seed, **kw):
+    own = gen.dense_inputs(len(lens), q_len, heads, lens, seed, extra_slots=P + 37, **kw)
+    free = np.setdiff1d(np.arange(own.pool.shape[0]), own.kv_indices.numpy())
+    pick = np.random.default_rng(seed).permutation(free)[:P]
+    return join(own, torch.from_numpy(pick.astype(np.int32)))
+
+
+def to_cuda(s):
+    o = s.own
+    return dict(q_lat=o.q_lat.cuda(), q_pe=o.q_pe.cuda(), pool=o.pool.cuda(),
+                prefix_indices=s.prefix.cuda(), seq_lens=o.seq_lens.cuda(),
+                kv_indices=o.kv_indices.cuda(), kv_indptr=o.kv_indptr.cuda())
+
+
+def plan_of(s, cap=None, sms=None):
+    o = s.own
+    return mla.mla_prefix_decode_plan(o.batch, o.q_len, o.num_heads,
+                                      s.prefix.numel() if cap is None else cap, o.total_keys,
+                                      sms or mla.sm_count())
+
+
+def run(s, plan=None, ws=None, d=None, **kw):
+    d = d or to_cuda(s)
+    plan = plan or plan_of(s)
+    ws = mla.workspace(plan) if ws is None else ws
+    out = mla.mla_prefix_decode(plan, **d, scale=s.own.scale, kv_scale=s.own.kv_scale,
+                                workspace_t=ws, **kw)
+    torch.cuda.synchronize()
+    return out, ws
+
+
+def check(s, what="", errors=0, **kw):
+    (o, lse), ws = run(s, **kw)
+    ro, rl = oracle.dense_decode(s.joined)
+    compare(o, lse, ro, rl, what)
+    assert mla.mla_read_device_error(ws) == errors
+    return o, lse
+
+
+@pytest.mark.parametrize("q_len,heads,P,lens", [
+    (1, 1, 1, [0]), (1, 1, 1, [1]), (1, 16, 128, [3]), (1, 16, 127, [1, 0, 5]),
+    (1, 16, 129, [200, 1]), (1, 64, 256, [0, 0]), (1, 128, 640, [7, 130]),
+    (1, 5, 1000, [33, 0, 1, 129, 64]), (2, 16, 300, [2, 9]), (4, 16, 2001, [4, 70, 500]),
+    (7, 3, 131, [7, 8]), (1, 16, 5000, [600] * 9), (1, 128, 4096, [17, 400, 3, 90]),
+    (1, 33, 8192, [50] * 20), (8, 128, 700, [11, 40])])
+def test_prefix(q_len, heads, P, lens):
+    check(make(q_len, heads, P, lens, seed=P + heads), f"q{q_len} H{heads} P{P}")
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 7, 37, 152])
+def test_any_split_of_the_prefix(sms):
+    # runs that end inside tiles, several tiles per CTA, CTAs of one block
+    s = make(1, 24, 1500, [5, 0, 300, 17, 64, 9, 1, 80, 33, 2, 140], seed=sms)
+    check(s, f"{sms} SMs", plan=plan_of(s, sms=sms))
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 4, 5, 6, 11, 24, 60, 148])
+def test_forced_cta_counts(ctas):
+    s = make(1, 24, 1500, [5, 0, 300, 17, 64, 9, 1, 80, 33, 2, 140], seed=3)
+    plan = plan_of(s, sms=152)
+    assert plan.tiles == 5
+    parts = ctas // 5 if ctas % 5 == 0 else -(-ctas // 5) + 1
+    rows = 11 * 24
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    plan.workspace_bytes += sum(up(rows * parts * n) - up(rows * plan.parts * n) for n in (2048, 4))
+    plan.ctas, plan.parts = ctas, parts
+    check(s, f"{ctas} CTAs", plan=plan)
+
+
+def test_no_prefix_and_no_keys_at_all():
+    s = make(1, 16, 0, [40, 0, 7], seed=1)
+    o, lse = check(s, "no prefix")
+    assert bool((o[1] == 0).all()) and bool((lse[1] == -float("inf")).all())
+    (o, lse), _ = run(make(1, 16, 0, [0, 0], seed=2))   # (the oracle wants one key at least)
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
+    s = make(1, 16, 200, [0, 0], seed=2)
+    check(s, "only the prefix")
+
+
+def test_length_on_the_device():
+    # one plan and one captured graph serve every length up to the capacity
+    s = make(2, 16, 1400, [30, 2, 250], seed=8)
+    d, plan = to_cuda(s), plan_of(s)
+    ws = mla.workspace(plan)
+    n = torch.tensor([1400], dtype=torch.int32, device="cuda")
+    run(s, plan, ws, d, prefix_len=n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = mla.mla_prefix_decode(plan, **d, scale=s.own.scale, kv_scale=s.own.kv_scale,
+                                       prefix_len=n, workspace_t=ws)
+    for length in (1400, 1, 0, 127, 128, 129, 777, 1399):
+        n.fill_(length)
+        graph.replay()
+        torch.cuda.synchronize()
+        cut = join(s.own, s.prefix[:length])
+        ro, rl = oracle.dense_decode(cut.joined)
+        compare(o, lse, ro, rl, f"length {length}")
+    assert mla.mla_read_device_error(ws) == 0
+    for length, same in ((1500, 1400), (-3, 0)):
+        n.fill_(length)
+        graph.replay()
+        assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_LENGTH
+        mla.mla_workspace_reset(ws)
+        cut = join(s.own, s.prefix[:same])
+        ro, rl = oracle.dense_decode(cut.joined)
+        compare(o, lse, ro, rl, f"clamped {length}")
+
+
+def test_drafts_that_reach_back_into_the_prefix():
+    # fewer own keys than draft rows: the first rows do not see the prefix's end
+    s = make(4, 16, 300, [0, 1, 2, 3, 4], seed=9)
+    check(s, "window in the prefix")
+    s = make(6, 8, 3, [0, 1, 2], seed=10)   # rows that see nothing at all
+    o, lse = check(s, "empty rows")
+    assert bool((lse[0] == -float("inf")).all()) and bool((o[0] == 0).all())
+
+
+def test_same_slots_twice_and_joined_decode():
+    # a slot named by the prefix and by requests; the plain decode agrees
+    s = make(1, 16, 700, [90, 10], seed=11)
+    s.own.kv_indices[:20] = s.prefix[100:120]
+    s.prefix[5:9] = s.prefix[5]
+    s = join(s.own, s.prefix)
+    o, lse = check(s, "repeated slots")
+    j = s.joined
+    plan = mla.mla_decode_plan(j.batch, 1, 16, j.total_keys, mla.sm_count())
+    o2, lse2 = mla.mla_decode(plan, j.q_lat.cuda(), j.q_pe.cuda(), j.pool.cuda(),
+                              j.seq_lens.cuda(), j.kv_indices.cuda(), j.kv_indptr.cuda(), j.scale,
+                              j.kv_scale)
+    assert float((lse - lse2).abs().max()) <= 1e-3
+    assert float((o.float() - o2.float()).abs().max()) <= 2e-2
+
+
+@pytest.mark.parametrize("edge", ["lat 2^8", "lat 2^12", "pe 2^10", "pe x32", "lat tiny",
+                                  "sharp", "tied", "dominant", "tiny queries"])
+def test_number_format_edges(edge):
+    s = make(1, 16, 900, [60, 3], seed=12)
+    own = s.own
+    if edge.startswith("lat 2"):
+        gen.plant_query_outliers(own, 2.0 ** int(edge.split("^")[1]), 5)
+    elif edge.startswith("pe 2"):
+        gen.plant_query_outliers(own, 2.0 ** 10, 5, "pe")
+    elif edge == "pe x32":
+        gen.scale_query_parts(own, pe=32.0)
+    elif edge == "lat tiny":
+        gen.scale_query_parts(own, lat=2.0 ** -10)
+    elif edge == "sharp":
+        gen.scale_query_parts(own, lat=30.0, pe=30.0)
+    elif edge == "tied":
+        gen.near_tied_pool(own, 6)
+    elif edge == "tiny queries":
+        gen.scale_query_parts(own, lat=2.0 ** -60, pe=2.0 ** -60)
+    else:
+        gen.share_query_across_heads(own)
+        joined = join(own, s.prefix).joined
+        own.pool = gen.plant_dominant_key(joined, 0.8, 7).pool
+    check(join(own, s.prefix), edge)
+
+
+@pytest.mark.parametrize("gap", [6.0, 10.0, 13.0])
+def test_one_sink_key_over_many_weak_ones(gap):
+    # a key `gap` nats above 20,000 others: their weights sit 9 to 19 bits below it
+    s = make(1, 4, 20000, [1], seed=13)
+    own = s.own
+    gen.share_query_across_heads(own)
+    q = torch.cat([own.q_lat[0, 0].float(), own.q_pe[0, 0].float()])
+    pool = (torch.randn(own.pool.shape[0], 576, generator=torch.Generator().manual_seed(1)) * 8)
+    row = q * gap / (float(q @ q) * own.scale * own.kv_scale)
+    pool[int(s.prefix[777])] += row
+    own.pool = pool.to(torch.float8_e4m3fn).view(torch.uint8).view(own.pool.shape)
+    check(join(own, s.prefix), f"gap {gap}")
+
+
+def test_masked_rows_are_never_read_and_bad_slots_are_reported():
+    s = make(1, 16, 500, [40, 9], seed=14)
+    want, _ = run(s)
+    own = s.own
+    nan = own.pool.clone()
+    used = torch.cat([s.prefix, own.kv_indices]).long()
+    idle = torch.ones(nan.shape[0], dtype=torch.bool)
+    idle[used] = False
+    nan[idle] = 0x7F   # NaN codes in every row that no table names
+    got, _ = run(Shared(dataclasses.replace(own, pool=nan), s.joined, s.prefix))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # a bad slot is skipped and reported
+    for bad in (-1, own.pool.shape[0], 2 ** 31 - 1, -2 ** 31):
+        p = s.prefix.clone()
+        p[130] = bad
+        (o, lse), ws = run(Shared(own, s.joined, p))
+        assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_SLOT
+        keep = torch.cat([s.prefix[:130], s.prefix[131:]])
+        ro, rl = oracle.dense_decode(join(own, keep).joined)
+        compare(o, lse, ro, rl, "bad slot")
+
+
+def test_a_query_with_nan_or_inf_stays_in_its_row():
+    s = make(1, 16, 400, [30, 5, 60, 2, 9], seed=15)
+    want, _ = run(s)
+    q = s.own.q_lat.clone()
+    q[1, 3, 7] = float("nan")
+    q[2, 0, 500] = float("inf")
+    got, _ = run(Shared(dataclasses.replace(s.own, q_lat=q), s.joined, s.prefix))
+    same = torch.ones(5, 16, dtype=torch.bool)
+    same[1, 3] = same[2, 0] = False
+    assert torch.equal(got[0][same.cuda()], want[0][same.cuda()])
+    assert torch.equal(got[1][same.cuda()], want[1][same.cuda()])
+
+
+def test_repeat_permuted_pool_and_given_outputs():
+    s = make(1, 48, 3000, [100, 3, 250, 8], seed=16)
+    d, plan = to_cuda(s), plan_of(s)
+    ws = mla.workspace(plan)
+    (o, lse), _ = run(s, plan, ws, d)
+    o2 = torch.empty_like(o)
+    (got, none), _ = run(s, plan, ws, d, o=o2, return_lse=False)
+    assert got is o2 and none is None and torch.equal(o, o2)
+    dirty = torch.full_like(ws, 255)   # whatever the scratch held before
+    dirty[:mla.MLA_WORKSPACE_HEADER_BYTES] = 0
+    (o3, lse3), _ = run(s, plan, dirty, d)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+    perm = torch.randperm(s.own.pool.shape[0], generator=torch.Generator().manual_seed(3))
+    inv = torch.argsort(perm).int()
+    moved = dict(d, pool=s.own.pool[perm].cuda(), prefix_indices=inv[s.prefix.long()].cuda(),
+                 kv_indices=inv[s.own.kv_indices.long()].cuda())
+    (o4, lse4), _ = run(s, plan, ws, moved)
+    assert torch.equal(o, o4) and torch.equal(lse, lse4)
+
+
+def test_another_stream_and_calls_back_to_back():
+    a, b = make(1, 16, 900, [30, 5], seed=17), make(1, 64, 300, [3, 80, 9], seed=18)
+    da, db, pa, pb = to_cuda(a), to_cuda(b), plan_of(a), plan_of(b)
+    wa, wb = mla.workspace(pa), mla.workspace(pb)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(5):   # two streams, a workspace each
+        with torch.cuda.stream(side):
+            oa = mla.mla_prefix_decode(pa, **da, scale=a.own.scale, kv_scale=a.own.kv_scale,
+                                       workspace_t=wa)
+        ob = mla.mla_prefix_decode(pb, **db, scale=b.own.scale, kv_scale=b.own.kv_scale,
+                                   workspace_t=wb)
+        outs.append((oa, ob))
+    torch.cuda.synchronize()
+    for s, k in ((a, 0), (b, 1)):
+        ro, rl = oracle.dense_decode(s.joined)
+        for pair in outs:
+            compare(*pair[k], ro, rl)
+            assert torch.equal(pair[k][0], outs[0][k][0])
+
+
+def test_pool_past_four_gigabytes():
+    rows = 8_000_000
+    s = make(1, 16, 300, [20, 4], seed=19)
+    own = s.own
+    small = own.pool.shape[0]
+    spread = (torch.arange(small, dtype=torch.int64) * ((rows - 1) // (small - 1)))
+    pool = torch.zeros(rows, 576, dtype=torch.uint8, device="cuda")
+    pool[spread.cuda()] = own.pool.view(small, 576).cuda()
+    d = to_cuda(s)
+    d.update(pool=pool, prefix_indices=spread[s.prefix.long()].int().cuda(),
+             kv_indices=spread[own.kv_indices.long()].int().cuda())
+    want, _ = run(s)
+    got, _ = run(s, d=d)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_wait_that_runs_out_ends_the_call():
+    s = make(1, 64, 1000, [30, 5], seed=20)
+    plan = plan_of(s)
+    ws = mla.workspace(plan)
+    mla.mla_debug_wait_limit(300)
+    try:
+        run(s, plan, ws)
+    finally:
+        mla.mla_debug_wait_limit(0)
+    assert mla.mla_read_device_error(ws) & mla.MLA_DEVERR_TIMEOUT
+    mla.mla_workspace_reset(ws)
+    check(s, "after a timeout", plan=plan, ws=ws)

@@ -257,6 +257,7 @@ struct PrefixShared {
     int abort;
     alignas(16) float cq[kRows];
     alignas(16) int win[kRows];
+    alignas(16) float scale[kRows];   // epilogue: 1 / the sum of what the MMA consumed
     float red[kSoftmaxWarps][32];
     float redt[kSoftmaxWarps][32];
 };
@@ -633,30 +634,41 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
 
     // ---- epilogue: sums over the keys, then the rows out of TMEM, normalised by
     // what the MMA consumed (lt), and the LSE from the exact p (l) -------------------------
-    red[quad * 32 + lane] = warp_transpose_reduce<R, false>(l, lane);
-    redt[quad * 32 + lane] = warp_transpose_reduce<R, false>(lt, lane);
+    {
+        const float sum = warp_transpose_reduce<R, false>(l, lane);
+        const float fed = warp_transpose_reduce<R, false>(lt, lane);
+        red[quad * 32 + lane] = sum;
+        redt[quad * 32 + lane] = fed;
+    }
     const bool have = alive && warp_wait(&ms.pv_done, (uint32_t)(r.j0 + n - 1) & 1, abort_flag, 0,
                                          a.wait_limit);
     if (have) tc_fence_after();
     softmax_bar(bar_id);
+    if (ti < R) {
+        const float fed = (redt[ti] + redt[32 + ti]) + (redt[64 + ti] + redt[96 + ti]);
+        ms.scale[r0 + ti] = have && fed != 0.f ? 1.f / fed : 0.f;   // NaN stays NaN
+    }
+    softmax_bar(bar_id);
     float* stage = reinterpret_cast<float*>(smem);   // fp32 [64][512]
+    float scl[R];
+#pragma unroll
+    for (int g = 0; g < R / 4; ++g) {
+        const float4 s = reinterpret_cast<const float4*>(ms.scale + r0)[g];
+        scl[4 * g] = s.x;
+        scl[4 * g + 1] = s.y;
+        scl[4 * g + 2] = s.z;
+        scl[4 * g + 3] = s.w;
+    }
+    // (without `have` the columns may hold anything: the rows are zero then)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
-        if (have) {
-            tmem_ld32(lanes + kColO + c * kRows + r0, o);
-            tmem_wait_ld();
-            reg_fence(o);
-        } else {
+        tmem_ld32(lanes + kColO + c * kRows + r0, o);
+        tmem_wait_ld();
+        reg_fence(o);
 #pragma unroll
-            for (int k = 0; k < R; ++k) o[k] = 0u;
-        }
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const float t = (redt[k] + redt[32 + k]) + (redt[64 + k] + redt[96 + k]);
-            stage[(r0 + k) * kDv + c * 128 + ti] =
-                t > 0.f ? __uint_as_float(o[k]) * rcp_approx(t) : 0.f;
-        }
+        for (int k = 0; k < R; ++k)
+            stage[(r0 + k) * kDv + c * 128 + ti] = scl[k] != 0.f ? __uint_as_float(o[k]) * scl[k] : 0.f;
     }
     tc_fence_before();
     fence_proxy_async_smem();
@@ -670,7 +682,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
             for (int k = 0; k < R; ++k)
                 if (k == ti) m = nm[k];
             const int64_t at = item * a.parts + r.part;
-            a.lse_part[at] = sum > 0.f ? log2f(sum) - m : -CUDART_INF_F;
+            a.lse_part[at] = sum != 0.f ? log2f(sum) - m : -CUDART_INF_F;
             bulk_store(a.o_part + at * kDv, stage + (r0 + ti) * kDv, kDv * 4);
             bulk_commit();
             bulk_wait_read();
@@ -829,7 +841,7 @@ prefix_merge_kernel(const PrefixArgs a)
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
             sum_s = sum;
-            if (a.lse != nullptr) a.lse[item] = sum > 0.f ? m + log2f(sum) : -CUDART_INF_F;
+            if (a.lse != nullptr) a.lse[item] = sum != 0.f ? m + log2f(sum) : -CUDART_INF_F;
         }
     }
     __syncthreads();
@@ -847,7 +859,7 @@ prefix_merge_kernel(const PrefixArgs a)
         if (i < n) add(w_s[i], v[i]);
     for (int i = kMergeAhead; i < n; ++i)
         add(w_s[i], __ldcg(reinterpret_cast<const float4*>(row_of(i) + c)));
-    const float f = sum_s > 0.f ? 1.f / sum_s : 0.f;
+    const float f = sum_s != 0.f ? 1.f / sum_s : 0.f;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
     *reinterpret_cast<uint2*>(a.o + item * kDv + c) =

@@ -172,8 +172,8 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str, dtype=None) -> Optional[int]:
 
 
 def _stream_ptr(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -496,6 +496,33 @@ def mla_decode_noalloc(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices
     return o_lat, lse
 
 
+# ---- arguments of the entry points below: checked once, in one place -----------------
+
+def _device(t: torch.Tensor) -> int:
+    """The CUDA device of a call's first tensor, which must be the current one
+    (the library launches on the current device)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor of the dtype on device dev, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 # ---- decode over a shared prefix -----------------------------------------------------
 
 def mla_prefix_decode_plan(batch: int, q_len: int, num_heads: int, prefix_cap: int,
@@ -514,13 +541,11 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
     """Dense decode of requests that share the prefix's slots and continue with
     their own (seq_lens, kv_indices, kv_indptr); returns (o, lse).  prefix_len
     int32 [1] on the device: how many of prefix_indices are in use (None: all)."""
-    _same_device(q_lat, q_pe=q_pe, pool=pool, prefix_indices=prefix_indices, seq_lens=seq_lens,
-                 kv_indices=kv_indices, kv_indptr=kv_indptr, prefix_len=prefix_len, o=o, lse=lse,
-                 workspace=workspace_t)
+    dev = _device(q_lat)
     R, H = q_lat.shape[0], q_lat.shape[1]
     batch = seq_lens.shape[0]
     q_len = R // batch if batch else plan.own.q_len
-    p = _pool_2d(pool)
+    p = _pool_2d(pool, dev)
     if (R != batch * q_len or q_lat.shape[2:] != (512,) or q_pe.shape != (R, H, 64) or
             p.shape[-1] != 576 or kv_indptr.numel() != batch + 1):
         raise ValueError("q_lat [B * q_len, H, 512], q_pe [B * q_len, H, 64], pool [N, 576] and "
@@ -537,34 +562,19 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
         raise ValueError("lse must be [B * q_len, H]")
     if workspace_t is None:
         workspace_t = workspace(plan, q_lat.device)
-    i32 = torch.int32
-    _check(load().mla_prefix_decode(
-        ctypes.byref(plan), _dev_ptr(q_lat, "q_lat", torch.bfloat16),
-        _dev_ptr(q_pe, "q_pe", torch.bfloat16), p.data_ptr(), p.shape[0],
-        _dev_ptr(prefix_indices, "prefix_indices", i32), _dev_ptr(prefix_len, "prefix_len", i32),
-        _dev_ptr(seq_lens, "seq_lens", i32), _dev_ptr(kv_indices, "kv_indices", i32),
-        _dev_ptr(kv_indptr, "kv_indptr", i32), batch, q_len, H, float(scale), float(kv_scale),
-        _dev_ptr(o, "o", torch.bfloat16), _dev_ptr(lse, "lse", torch.float32),
-        _dev_ptr(workspace_t, "workspace"), workspace_t.numel(), _stream_ptr(stream)),
-        "mla_prefix_decode")
+    i32, bf16 = torch.int32, torch.bfloat16
+    _check((_lib or load()).mla_prefix_decode(
+        ctypes.byref(plan), _ptr(q_lat, "q_lat", bf16, dev), _ptr(q_pe, "q_pe", bf16, dev),
+        p.data_ptr(), p.shape[0], _ptr(prefix_indices, "prefix_indices", i32, dev),
+        _ptr(prefix_len, "prefix_len", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev),
+        _ptr(kv_indices, "kv_indices", i32, dev), _ptr(kv_indptr, "kv_indptr", i32, dev), batch,
+        q_len, H, scale, kv_scale, _ptr(o, "o", bf16, dev), _ptr(lse, "lse", torch.float32, dev),
+        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
+        _stream_ptr(stream)), "mla_prefix_decode")
     return o, lse
 
 
 # ---- the cache: append, fork, compact ------------------------------------------------
-
-def _same_device(first: torch.Tensor, **tensors) -> None:
-    """All given tensors on `first`'s CUDA device, and that device current (the
-    library launches on the current device)."""
-    dev = first.device
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-
 
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
     """t as [..., columns] whose last dimension is contiguous."""
@@ -575,11 +585,13 @@ def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _pool_2d(pool: torch.Tensor) -> torch.Tensor:
-    """The pool as [rows, row_bytes]: 2-D, or a [rows, 1, row_bytes] cache."""
+def _pool_2d(pool: torch.Tensor, dev: int) -> torch.Tensor:
+    """The pool: [rows, row_bytes], or a [rows, 1, row_bytes] cache, of bytes."""
     if pool.element_size() != 1 or pool.dim() not in (2, 3) or (pool.dim() == 3 and
                                                                pool.shape[1] != 1):
         raise ValueError("pool must hold one byte per element, [rows, row_bytes]")
+    if pool.get_device() != dev:
+        raise ValueError(f"pool must be on cuda:{dev}, got {pool.device}")
     if not pool.is_contiguous():
         raise ValueError("pool must be contiguous")
     return pool
@@ -610,21 +622,19 @@ def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0,
     first = kv if kv is not None else q
     if first is None:
         raise ValueError("kv or q must be given")
-    _same_device(first, slots=slots, pool=pool, positions=positions, cos_sin=cos_sin, q=q,
-                 kv_weight=kv_weight, q_weight=q_weight, q_nope=q_nope, q_pe=q_pe,
-                 workspace=workspace_t)
+    dev = _device(first)
     T = first.shape[0]
     kv_ptr = kv_stride = pool_rows = width = 0
     if kv is not None:
         if slots is None or pool is None:
             raise ValueError("slots and pool must be given with kv")
-        p = _pool_2d(pool)
+        p = _pool_2d(pool, dev)
         pool_rows, width = p.shape[0], p.shape[-1]
         if _rows(kv, "kv").dim() != 2 or kv.shape[1] != width:
             raise ValueError(f"kv must be [T, {width}], the pool's row width")
         if slots.numel() != T:
             raise ValueError("slots must have one entry per token")
-        if kv_weight is not None and kv_weight.numel() != kv_norm_cols:
+        if kv_weight is not None and kv_weight.numel() != int(kv_norm_cols):
             raise ValueError("kv_weight must have kv_norm_cols entries")
         kv_ptr, kv_stride = kv.data_ptr(), kv.stride(0)
     if positions.numel() != T:
@@ -633,8 +643,8 @@ def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0,
         raise ValueError("cos_sin must be [max_positions, 64]")
     H = cols = q_ptr = qts = qhs = 0
     if q is not None:
-        if _rows(q, "q").dim() != 3 or q.shape[0] != T:
-            raise ValueError("q must be [T, H, q_cols]")
+        if _rows(q, "q").dim() != 3 or q.shape[0] != T or q.get_device() != dev:
+            raise ValueError(f"q must be [T, H, q_cols] on cuda:{dev}")
         H, cols = q.shape[1], q.shape[2]
         if q_weight is not None and q_weight.numel() != cols:
             raise ValueError("q_weight must have q_cols entries")
@@ -647,15 +657,15 @@ def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0,
             raise ValueError("q_nope and q_pe must be [T, H, q_cols - 64] and [T, H, 64]")
     if workspace_t is None:
         workspace_t = cache_workspace(device=first.device)
-    _check(load().mla_cache_append(
-        kv_ptr or None, kv_stride, _dev_ptr(kv_weight, "kv_weight", torch.bfloat16),
-        int(kv_norm_cols), _dev_ptr(slots, "slots", torch.int32),
-        pool.data_ptr() if kv is not None else None, pool_rows, width, float(kv_scale),
-        q_ptr or None, qts, qhs, _dev_ptr(q_weight, "q_weight", torch.bfloat16),
-        1 if q_norm else 0, cols, _dev_ptr(q_nope, "q_nope", torch.bfloat16),
-        _dev_ptr(q_pe, "q_pe", torch.bfloat16), _dev_ptr(positions, "positions", torch.int32),
-        _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], 1 if half_split else 0,
-        float(eps), T, H, _dev_ptr(workspace_t, "workspace"), workspace_t.numel(),
+    i32, bf16 = torch.int32, torch.bfloat16
+    _check((_lib or load()).mla_cache_append(
+        kv_ptr or None, kv_stride, _ptr(kv_weight, "kv_weight", bf16, dev), kv_norm_cols,
+        _ptr(slots, "slots", i32, dev), pool.data_ptr() if kv is not None else None, pool_rows,
+        width, kv_scale, q_ptr or None, qts, qhs, _ptr(q_weight, "q_weight", bf16, dev),
+        1 if q_norm else 0, cols, _ptr(q_nope, "q_nope", bf16, dev), _ptr(q_pe, "q_pe", bf16, dev),
+        _ptr(positions, "positions", i32, dev), _ptr(cos_sin, "cos_sin", torch.float32, dev),
+        cos_sin.shape[0], 1 if half_split else 0, eps, T, H,
+        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
         _stream_ptr(stream)), "mla_cache_append")
     return q_nope, q_pe
 
@@ -665,10 +675,8 @@ def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, tot
     """Page tables of requests that continue `parents`, sharing their first
     keep[f] slots and copying the other rows to fresh slots; returns the
     children's kv_indices int32 [total] (their kv_indptr is child_indptr)."""
-    p = _pool_2d(pool)
-    _same_device(pool, kv_indices=kv_indices, kv_indptr=kv_indptr, parents=parents, keep=keep,
-                 child_indptr=child_indptr, fresh=fresh, fresh_indptr=fresh_indptr, table=table,
-                 workspace=workspace_t)
+    dev = _device(pool)
+    p = _pool_2d(pool, dev)
     F = parents.numel()
     if keep.numel() != F or child_indptr.numel() != F + 1 or fresh_indptr.numel() != F + 1:
         raise ValueError("keep, child_indptr and fresh_indptr must match parents")
@@ -679,14 +687,15 @@ def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, tot
     if workspace_t is None:
         workspace_t = cache_workspace(device=pool.device)
     i32 = torch.int32
-    _check(load().mla_cache_fork(
-        p.data_ptr(), p.shape[0], p.shape[-1], _dev_ptr(kv_indices, "kv_indices", i32),
-        kv_indices.numel(), _dev_ptr(kv_indptr, "kv_indptr", i32), max(0, kv_indptr.numel() - 1),
-        _dev_ptr(parents, "parents", i32), _dev_ptr(keep, "keep", i32),
-        _dev_ptr(child_indptr, "child_indptr", i32), F, _dev_ptr(fresh, "fresh", i32),
-        fresh.numel(), _dev_ptr(fresh_indptr, "fresh_indptr", i32),
-        _dev_ptr(table, "table", i32), int(total), _dev_ptr(workspace_t, "workspace"),
-        workspace_t.numel(), _stream_ptr(stream)), "mla_cache_fork")
+    _check((_lib or load()).mla_cache_fork(
+        p.data_ptr(), p.shape[0], p.shape[-1], _ptr(kv_indices, "kv_indices", i32, dev),
+        kv_indices.numel(), _ptr(kv_indptr, "kv_indptr", i32, dev),
+        max(0, kv_indptr.numel() - 1), _ptr(parents, "parents", i32, dev),
+        _ptr(keep, "keep", i32, dev), _ptr(child_indptr, "child_indptr", i32, dev), F,
+        _ptr(fresh, "fresh", i32, dev), fresh.numel(),
+        _ptr(fresh_indptr, "fresh_indptr", i32, dev), _ptr(table, "table", i32, dev), total,
+        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
+        _stream_ptr(stream)), "mla_cache_fork")
     return table
 
 
@@ -695,9 +704,8 @@ def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t
     """Move the rows that kv_indices names to the front of the pool, in place;
     returns (new_indices, live): the rewritten table and the live row count
     int32 [1] (rows from there on are free).  new_indices may be kv_indices."""
-    p = _pool_2d(pool)
-    _same_device(pool, kv_indices=kv_indices, new_indices=new_indices, live=live,
-                 workspace=workspace_t)
+    dev = _device(pool)
+    p = _pool_2d(pool, dev)
     if new_indices is None:
         new_indices = torch.empty_like(kv_indices)
     elif new_indices.numel() != kv_indices.numel():
@@ -706,9 +714,10 @@ def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t
         live = torch.empty(1, dtype=torch.int32, device=pool.device)
     if workspace_t is None:
         workspace_t = cache_workspace(p.shape[0], device=pool.device)
-    _check(load().mla_cache_compact(
-        p.data_ptr(), p.shape[0], p.shape[-1], _dev_ptr(kv_indices, "kv_indices", torch.int32),
-        kv_indices.numel(), _dev_ptr(new_indices, "new_indices", torch.int32),
-        _dev_ptr(live, "live", torch.int32), _dev_ptr(workspace_t, "workspace"),
+    i32 = torch.int32
+    _check((_lib or load()).mla_cache_compact(
+        p.data_ptr(), p.shape[0], p.shape[-1], _ptr(kv_indices, "kv_indices", i32, dev),
+        kv_indices.numel(), _ptr(new_indices, "new_indices", i32, dev),
+        _ptr(live, "live", i32, dev), _ptr(workspace_t, "workspace", torch.uint8, dev),
         workspace_t.numel(), _stream_ptr(stream)), "mla_cache_compact")
     return new_indices, live

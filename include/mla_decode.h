@@ -412,10 +412,15 @@ int mla_decode_noalloc(const mla_plan_t* plan, const void* q_lat, const void* q_
  */
 typedef struct {
     int32_t tiles;           /* 64-row tiles of the batch * q_len * num_heads query rows */
-    int32_t ctas;            /* CTAs that share the (tile, 128-key block) pairs of the prefix */
-    int32_t parts;           /* most CTAs that one tile's blocks fall to (partials per row);
-                                0 when prefix_cap is 0 */
+    int32_t ctas;            /* CTAs of the prefix kernel; 0 when prefix_cap is 0 */
+    int32_t splits;          /* CTAs per tile, each an equal part of its 128-key blocks;
+                                or 0: the sequence of all tiles' blocks is cut into
+                                equal runs, one per CTA (at most MLA_MAX_SPLITS) */
+    int32_t joined;          /* 1: a tile's blocks are the prefix's and then its requests'
+                                own; 0: the requests' own keys go through the kernel of
+                                mla_decode.  Results agree with the oracle either way */
     int32_t sm_count;
+    int32_t reserved;        /* 0 */
     int64_t workspace_bytes; /* bytes of device workspace the call needs */
     int64_t prefix_cap;      /* entries of prefix_indices */
     mla_plan_t own;          /* the plan of the requests' own keys (mla_decode_plan) */

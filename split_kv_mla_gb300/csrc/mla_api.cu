@@ -646,29 +646,31 @@ int mla_sparse_decode_splits(const mla_plan_t* plan, const void* q_nope, const v
 
 namespace {
 
-constexpr double kPrefixBlockUs = 1.6;   // a 128-key block of one 64-row tile
-constexpr double kPrefixRunUs = 6.0;     // a run's start (query tile, first block) and epilogue
-
-inline int64_t prefix_blocks(int64_t cap) { return ceil_div(cap, kPrefixKeys); }
-
-// Most partials of one tile when `tiles` tiles are dealt out to `ctas` CTAs in
-// equal runs: run borders fall at multiples of tiles / ctas tiles.
-int32_t prefix_parts(int64_t tiles, int64_t ctas)
-{
-    if (ctas % tiles == 0) return (int32_t)(ctas / tiles);
-    return (int32_t)(ceil_div(ctas, tiles) + 1);
-}
+constexpr double kPrefixBlockUs = 1.9;   // a 128-key block of one 64-row tile
+constexpr double kPrefixRunUs = 9.0;     // a run's start (query tile, first block) and epilogue
+constexpr double kOwnCallUs = 3.0;       // one more kernel in the call
+constexpr int64_t kMaxJoinedKeys = 1 << 24;
 
 struct PrefixLayout {   // byte offsets in the workspace
-    int64_t own_o, own_lse, o_part, lse_part, k_image, k_valid, q_image, q_scale, q_window, end;
+    int64_t own_o, own_lse, o_part, lse_part, k_image, k_valid, q_image, q_scale, q_window,
+        tile_start, end;
 };
+
+// Slots for the partial rows of every run of the prefix kernel.
+inline int64_t prefix_slots(const mla_prefix_plan_t* p)
+{
+    if (p->ctas == 0) return 0;
+    return p->splits > 0 ? p->ctas : (int64_t)p->ctas + p->tiles;
+}
 
 // The requests' own partials first, where the split kernel's plan has them.
 PrefixLayout prefix_layout(const mla_prefix_plan_t* p)
 {
     const int64_t rows = (int64_t)p->own.batch * p->own.q_len * p->own.num_heads;
-    const int64_t blocks = prefix_blocks(p->prefix_cap);
-    const int64_t tiles = p->parts > 0 ? p->tiles : 0;
+    const int64_t own_rows = p->joined || p->own.total_keys == 0 ? 0 : rows * p->own.num_splits;
+    const int64_t tiles = p->ctas > 0 ? p->tiles : 0;
+    const int64_t blocks = prefix_blocks(p->prefix_cap) +
+                           (p->joined ? prefix_own_blocks(p->own.total_keys, p->own.batch) : 0);
     int64_t at = MLA_WORKSPACE_HEADER_BYTES;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -676,15 +678,16 @@ PrefixLayout prefix_layout(const mla_prefix_plan_t* p)
         return here;
     };
     PrefixLayout l;
-    l.own_o = take(rows * p->own.num_splits * kDenseDv * 4);
-    l.own_lse = take(rows * p->own.num_splits * 4);
-    l.o_part = take(rows * p->parts * kDenseDv * 4);
-    l.lse_part = take(rows * p->parts * 4);
+    l.own_o = take(own_rows * kDenseDv * 4);
+    l.own_lse = take(own_rows * 4);
+    l.o_part = take(prefix_slots(p) * kPrefixRows * kDenseDv * 4);
+    l.lse_part = take(prefix_slots(p) * kPrefixRows * 4);
     l.k_image = take(blocks * kPrefixImage);
     l.k_valid = take(blocks * 16);
     l.q_image = take(tiles * kPrefixImage);
     l.q_scale = take(tiles * kPrefixRows * 4);
     l.q_window = take(tiles * kPrefixRows * 4);
+    l.tile_start = take(tiles > 0 ? (tiles + 1) * 8 : 0);
     l.end = at;
     return l;
 }
@@ -699,10 +702,15 @@ bool prefix_plan_ok(const mla_prefix_plan_t* p)
         return false;
     if (p->prefix_cap < 0 || p->prefix_cap > (1LL << 30)) return false;
     if (p->tiles != ceil_div(rows, kPrefixRows)) return false;
-    if (p->prefix_cap == 0 ? p->parts != 0
-                           : p->ctas < 1 || p->parts != prefix_parts(p->tiles, p->ctas) ||
-                                 p->parts > MLA_MAX_SPLITS)
-        return false;
+    if (p->prefix_cap == 0) {
+        if (p->ctas != 0 || p->splits != 0 || p->joined != 0) return false;
+    } else {
+        // a tile's partials are at most MLA_MAX_SPLITS (one per CTA without splits)
+        if (p->ctas < 1 || p->splits < 0 || p->splits > MLA_MAX_SPLITS) return false;
+        if (p->splits > 0 ? p->ctas != (int64_t)p->tiles * p->splits : p->ctas > MLA_MAX_SPLITS)
+            return false;
+        if (p->joined != 0 && (p->joined != 1 || p->own.total_keys > kMaxJoinedKeys)) return false;
+    }
     return p->workspace_bytes == prefix_layout(p).end;
 }
 
@@ -724,27 +732,54 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
     out->tiles = (int32_t)ceil_div(rows, kPrefixRows);
     const int64_t tiles = out->tiles, blocks = prefix_blocks(prefix_cap);
     if (tiles > 0 && blocks > 0) {
-        // Either every tile is cut into ns equal runs, one per CTA, or all SMs get
-        // an equal run of the tile-major sequence, which ends and starts inside
-        // tiles: the first has no second run in a CTA, the second no idle SM.
-        const int64_t U = tiles * blocks;
+        // Two choices by the model's time.  Whether a tile takes its requests' own
+        // keys after the prefix (their rows are copied and a block is multiplied for
+        // all 64 rows) or the split kernel does them in a launch of its own; and
+        // whether every tile is cut into equal parts, one per CTA, or the whole
+        // sequence into equal runs, which end and start inside tiles: the first has
+        // one run per CTA, the second no idle SM.
+        const int64_t per = (int64_t)q_len * num_heads;
+        const double own_blocks = (double)ceil_div(ceil_div(total_keys, batch), kPrefixKeys) *
+                                  (per >= kPrefixRows ? 1.0 : (double)kPrefixRows / per);
+        const int64_t own_keys = ceil_div(total_keys, batch);
+        const int32_t rpc = out->own.rows_per_cta;
+        const double own_us =
+            total_keys == 0 ? 0.0
+                            : kOwnCallUs + gb300_splits(ceil_div(per, rpc) * batch, own_keys, rows,
+                                                        kDenseDv, kDenseDv + kDenseDr, sm_count,
+                                                        rpc).us;
         double best = 0.0;
-        auto consider = [&](int64_t ctas) {
-            const int64_t per = ceil_div(U, ctas);
-            const int64_t runs = ctas % tiles == 0 ? 1 : (per - 2 + blocks) / blocks + 1;
-            const int64_t parts = prefix_parts(tiles, ctas);
-            if (parts > MLA_MAX_SPLITS) return;
-            const double us = (double)per * kPrefixBlockUs + (double)runs * kPrefixRunUs +
-                              (double)rows * parts * kDenseDv * 8.0 / kBytesPerUs;
+        auto consider = [&](bool joined, int64_t splits) {
+            const double nb = (double)blocks + (joined ? own_blocks : 0.0);
+            double ctas, at_most, runs;
+            if (splits > 0) {
+                ctas = (double)(tiles * splits);
+                at_most = std::ceil(nb / (double)splits);
+                runs = 1.0;
+            } else {
+                const double U = nb * (double)tiles;
+                const int64_t most = sm_count < MLA_MAX_SPLITS ? sm_count : MLA_MAX_SPLITS;
+                ctas = U < (double)most ? U : (double)most;
+                at_most = std::ceil(U / ctas);
+                runs = 1.0 + std::ceil((at_most - 1.0) / nb);
+            }
+            const double parts = splits > 0 ? (double)splits : ctas / (double)tiles + 2.0;
+            const double us = at_most * kPrefixBlockUs + runs * kPrefixRunUs +
+                              (double)rows * parts * kDenseDv * 8.0 / kBytesPerUs +
+                              (joined ? (double)total_keys * 1152.0 / kBytesPerUs : own_us);
             if (out->ctas == 0 || us < best) {
                 best = us;
                 out->ctas = (int32_t)ctas;
-                out->parts = (int32_t)parts;
+                out->splits = (int32_t)splits;
+                out->joined = joined ? 1 : 0;
             }
         };
-        for (int64_t ns = 1; ns <= blocks && ns * tiles <= sm_count; ++ns) consider(ns * tiles);
-        consider(U < sm_count ? U : sm_count);
-        if (out->ctas == 0) return MLA_ERR_UNSUPPORTED_SHAPE;
+        for (int joined = 0; joined <= (total_keys > 0 && total_keys <= kMaxJoinedKeys ? 1 : 0);
+             ++joined) {
+            consider(joined != 0, 0);
+            for (int64_t s = 1; s <= blocks && s <= MLA_MAX_SPLITS && s * tiles <= sm_count; ++s)
+                consider(joined != 0, s);
+        }
     }
     out->workspace_bytes = prefix_layout(out).end;
     return MLA_OK;
@@ -783,8 +818,9 @@ int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const vo
     a.pool_rows = pool_rows;
     a.prefix_indices = prefix_indices;
     a.prefix_len = plan->prefix_cap > 0 ? prefix_len : nullptr;
-    a.prefix_cap = plan->prefix_cap;
+    a.prefix_cap = (int32_t)plan->prefix_cap;
     a.seq_lens = seq_lens;
+    a.kv_indices = kv_indices;
     a.kv_indptr = kv_indptr;
     a.batch = batch;
     a.q_len = q_len;
@@ -792,7 +828,9 @@ int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const vo
     a.rows = (int64_t)batch * q_len * num_heads;
     a.tiles = plan->tiles;
     a.ctas = plan->ctas;
-    a.parts = plan->parts;
+    a.splits = plan->splits;
+    a.joined = plan->joined;
+    a.total_keys = plan->joined ? (int32_t)plan->own.total_keys : 0;
     a.logit_scale = scale * kv_scale * kLog2e;
     a.kv_scale = kv_scale;
     a.err = reinterpret_cast<uint32_t*>(ws);
@@ -801,19 +839,20 @@ int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const vo
     a.q_image = reinterpret_cast<uint8_t*>(ws + l.q_image);
     a.q_scale = reinterpret_cast<float*>(ws + l.q_scale);
     a.q_window = reinterpret_cast<int32_t*>(ws + l.q_window);
+    a.tile_start = reinterpret_cast<int64_t*>(ws + l.tile_start);
     a.o_part = reinterpret_cast<float*>(ws + l.o_part);
     a.lse_part = reinterpret_cast<float*>(ws + l.lse_part);
     a.o_own = reinterpret_cast<const float*>(ws + l.own_o);
     a.lse_own = reinterpret_cast<const float*>(ws + l.own_lse);
     // one split writes final rows (kv_scale applied), several leave raw partials
-    a.own_splits = plan->own.total_keys > 0 ? plan->own.num_splits : 0;
+    a.own_splits = plan->own.total_keys > 0 && !plan->joined ? plan->own.num_splits : 0;
     a.own_scale = plan->own.num_splits == 1 ? 1.f : kv_scale;
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
     a.wait_limit = pipeline_wait_limit();
     a.stall_probe = stall_probe_armed() ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (plan->parts > 0 && launch_prefix_split(a, s) != cudaSuccess) return MLA_ERR_LAUNCH_FAILED;
+    if (plan->ctas > 0 && launch_prefix_split(a, s) != cudaSuccess) return MLA_ERR_LAUNCH_FAILED;
     if (a.own_splits > 0) {
         rc = dense_call(&plan->own, q_lat, q_pe, pool, pool_rows, seq_lens, kv_indices, kv_indptr,
                         batch, q_len, num_heads, scale, kv_scale, ws + l.own_o,

@@ -151,35 +151,47 @@ struct PrefixArgs {
     int64_t pool_rows;
     const int32_t* prefix_indices;
     const int32_t* prefix_len;   // device length, or NULL: prefix_cap
-    int64_t prefix_cap;          // entries of prefix_indices
+    int32_t prefix_cap;          // entries of prefix_indices
     const int32_t* seq_lens;     // the requests' own keys
+    const int32_t* kv_indices;
     const int32_t* kv_indptr;
+    int32_t total_keys;          // entries of kv_indices that joined tiles may read
     int32_t batch, q_len, num_heads;
     int64_t rows;                // batch * q_len * num_heads
     int32_t tiles;               // ceil(rows / kPrefixRows)
     int32_t ctas;                // CTAs of the prefix kernel
-    int32_t parts;               // partial rows per output row from the prefix
+    int32_t splits;              // CTAs per tile, or 0: equal runs of the tiles' sequence
+    int32_t joined;              // a tile's blocks are the prefix's and its requests' own
     float logit_scale;           // scale * kv_scale * log2(e)
     float kv_scale;
     // workspace
     uint32_t* err;
-    uint8_t* k_image;            // [blocks][kPrefixImage]: keys as the MMA reads them
+    uint8_t* k_image;            // [prefix blocks, then own blocks][kPrefixImage]
     uint32_t* k_valid;           // [blocks][4]: bit per key
     uint8_t* q_image;            // [tiles][kPrefixImage]: e4m3 terms of the queries
     float* q_scale;              // [tiles * 64] raw dot -> base-2 logit
-    int32_t* q_window;           // [tiles * 64] prefix positions the row sees
-    float* o_part;               // [rows, parts, 512], normalised
-    float* lse_part;             // [rows, parts]
-    // the requests' own keys: partial rows of the split kernel
+    int32_t* q_window;           // [tiles * 64] positions the row sees
+    int64_t* tile_start;         // [tiles + 1] blocks before the tile
+    float* o_part;               // [slots][64][512], normalised
+    float* lse_part;             // [slots][64]
+    // without joined tiles: the requests' own keys as partial rows of the split kernel
     const float* o_own;          // [rows, own_splits, 512]
     const float* lse_own;        // [rows, own_splits]
-    int32_t own_splits;          // 0: no request has keys of its own
+    int32_t own_splits;          // 0: none
     float own_scale;             // o_own's units -> output units
     uint16_t* o;                 // bf16 [rows, 512]
     float* lse;                  // fp32 [rows] or NULL
     long long wait_limit;
     int32_t stall_probe;
 };
+
+// Blocks of the prefix, and room for the requests' own: request b's start at
+// block kv_indptr[b] / 128 + b.
+inline int64_t prefix_blocks(int64_t cap) { return (cap + kPrefixKeys - 1) / kPrefixKeys; }
+inline int64_t prefix_own_blocks(int64_t total_keys, int64_t batch)
+{
+    return total_keys / kPrefixKeys + batch;
+}
 
 // The operand images of the prefix and the queries, and the prefix's partials.
 cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream);

@@ -3,15 +3,19 @@
 // per tile, instead of once per request.  See mla_prefix_decode in
 // include/mla_decode.h for the contract.
 //
-// Three kernels here (the requests' own keys go through the split kernel):
+// Three kernels:
 //
-// * prepare: gathers the prefix's rows through its slot list into 128-key
+// * prepare: gathers the keys' rows through their slot lists into 128-key
 //   blocks laid out exactly as the MMA reads them (mla_layout.cuh), and splits
 //   each query row into two e4m3 terms the same way.  Both are then fetched with
 //   plain bulk copies of whole 16 KB chunks: a row gather cannot feed 64-row
-//   tiles (160 tile::gather4 copies of a block take ~3,800 cycles, a block's
-//   MMAs 2,700), and every tile reads the same blocks.
-// * prefix_split: per CTA a range of (tile, block) pairs.
+//   tiles (160 tile::gather4 copies of a block take ~3,800 cycles, as long as
+//   all its MMAs), and every tile reads the same prefix blocks.
+// * prefix_split: a tile's blocks are the prefix's, then those of the requests
+//   that have rows in the tile (their own keys, masked for the other requests'
+//   rows); or, where the requests' own keys are long, the prefix's alone and
+//   the split kernel (mla_split_kernel.cuh) does the others.  Per CTA runs of
+//   (tile, block) pairs; per block
 //     S^T[128 keys x 128] = K[128 x 576] . [q_hi | q_lo]^T      one MMA chain
 //     p = 2^(s - m),  O^T[512 x 64] += V^T[512 x 128] . (p_hi + p_lo)
 //   with K and V e4m3 as they are stored.  A query row, scaled to max |q| in
@@ -25,12 +29,14 @@
 //   below the row's reference, where bf16 carries eight.
 // * prefix_merge: joins a row's partials by their base-2 LSEs.
 //
-// What bounds the split kernel: an MMA with N = 64 waits for its A operand from
-// shared memory (4 KB a K-step of 32 at 128 bytes a cycle, and 2 KB of B: 48
-// cycles for 32 cycles of multiplying).  QK stacks both terms along N (128
-// columns, 64 cycles, A read once); P.V cannot.  A block of 128 keys and 64 rows
-// so costs 18 x 64 + 32 x 48 = 2,688 cycles of the tensor pipe against 2,176 at
-// the bf16 rate.
+// What bounds the split kernel: shared memory's 128 bytes a cycle.  A block of
+// 128 keys and 64 rows reads 18 x 8 KB for QK (both terms stacked along N, so K
+// is read once) and 32 x 6 KB for P.V (V once per term), the bulk copies write
+// 72 KB and the softmax 16 KB: 435 KB, 3,400 cycles, against 2,176 of
+// multiplying at the bf16 rate.  It takes 3,670 (1.9 us; the MMAs alone, back
+// to back: 18 x 73 + 32 x 58 = 3,170).  More rows per tile would read less per
+// row, but O^T and the S^T buffers fill TMEM and the stages, queries and P fill
+// shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -75,20 +81,50 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int sme
 
 // The prefix's length: the device value clamped to its list (prepare reports one
 // outside), or the list's own length.
-__device__ __forceinline__ int64_t prefix_length(const PrefixArgs& a)
+__device__ __forceinline__ int prefix_length(const PrefixArgs& a)
 {
     if (a.prefix_len == nullptr) return a.prefix_cap;
-    const int64_t n = __ldcg(a.prefix_len);
-    return n < 0 ? 0 : n > a.prefix_cap ? a.prefix_cap : n;
+    return min(max(__ldcg(a.prefix_len), 0), a.prefix_cap);
 }
 
-// The (tile, block) pairs, tile-major, are dealt out in equal runs: CTA g takes
-// pairs [g U / G, (g + 1) U / G) of U on G <= U CTAs.  With G a multiple of the
-// tile count the runs end at tile borders.  The CTA of pair u:
+// The own blocks' images follow those that the longest prefix takes.
+__device__ __forceinline__ int prefix_image_blocks(const PrefixArgs& a)
+{
+    return (a.prefix_cap + kKeys - 1) / kKeys;
+}
+
+// Request b's own keys: how many are in use, and where its table starts.  A
+// length outside its table is clamped (the caller reports it), as is a table
+// that reaches past the plan's entries.
+__device__ __forceinline__ int own_length(const PrefixArgs& a, int b, int& first)
+{
+    first = __ldg(a.kv_indptr + b);
+    const int cap = __ldg(a.kv_indptr + b + 1) - first;
+    const int len = min(max(__ldg(a.seq_lens + b), 0), max(cap, 0));
+    return first < 0 || first > a.total_keys ? 0 : min(len, a.total_keys - first);
+}
+
+// The block of the own images where request b's keys start.
+__device__ __forceinline__ int own_block0(int first, int b) { return first / kKeys + b; }
+
+// Requests that have rows in tile t: [first, last].
+__device__ __forceinline__ void tile_requests(const PrefixArgs& a, int64_t t, int& b0, int& b1)
+{
+    const int64_t per = (int64_t)a.q_len * a.num_heads;
+    b0 = (int)(t * kRows / per);
+    b1 = (int)((min(t * kRows + kRows, a.rows) - 1) / per);
+}
+
+// How a tile's blocks are dealt out.  With `splits`, CTA t * splits + s takes the
+// s-th of equal parts of tile t; else the tile-major sequence of all U blocks is
+// cut into equal runs, CTA g taking blocks [g U / G, (g + 1) U / G), G <= U.
+// Then the CTA of block u is:
 __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t U, int64_t G)
 {
     return ((u + 1) * G - 1) / U;
 }
+// A run of CTA g in tile t leaves its partial rows in slot g with `splits`, in
+// slot g + t without (runs follow one another by a step of g or of t).
 
 // ---- prepare ----------------------------------------------------------------------------------
 
@@ -96,36 +132,33 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepKeys = 32;     // keys per CTA
 constexpr int kPrepRows = kPrepThreads / 32;   // query rows per CTA, one per warp
 
-// Keys 32 c .. 32 c + 31 of the prefix into their block's image.
-__device__ void prepare_keys(const PrefixArgs& a, int64_t c)
+// Keys [k0, k0 + 32) of a list of `len` into rows k0 % 128 .. of block k0 / 128 of
+// `image`, as zero rows past the list's end and for bad slots.  The whole CTA.
+__device__ __forceinline__ void prepare_keys(const PrefixArgs& a, const int32_t* list, int k0,
+                                             int len, uint8_t* image, uint32_t* valid)
 {
     __shared__ int32_t slots[kPrepKeys];
     const int tid = threadIdx.x;
-    const int64_t len = prefix_length(a);
-    const int64_t k0 = c * kPrepKeys;
-    if (c == 0 && tid == 0 && a.prefix_len != nullptr && __ldcg(a.prefix_len) != len)
-        atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
-    if (k0 >= (len + kKeys - 1) / kKeys * kKeys) return;   // past the last block
     if (tid < kPrepKeys) {
-        int32_t s = k0 + tid < len ? __ldg(a.prefix_indices + k0 + tid) : -1;
+        int32_t s = k0 + tid < len ? __ldg(list + k0 + tid) : -1;
         if (k0 + tid < len && (s < 0 || s >= a.pool_rows)) {
             atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
             s = -1;
         }
         slots[tid] = s;
-        const uint32_t valid = __ballot_sync(0xffffffffu, s >= 0);
-        if (tid == 0) a.k_valid[c] = valid;
+        const uint32_t bits = __ballot_sync(0xffffffffu, s >= 0);
+        if (tid == 0) valid[k0 / kPrepKeys] = bits;
     }
     __syncthreads();
-    uint8_t* image = a.k_image + k0 / kKeys * kPrefixImage;
-    const int row0 = (int)(k0 % kKeys);
+    image += k0 / kKeys * kPrefixImage;
+    const int row0 = k0 % kKeys;
     constexpr int kPieces = kWidth / 16;
     constexpr int kPer = (kPrepKeys * kPieces + kPrepThreads - 1) / kPrepThreads;
     uint4 v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int p = tid + i * kPrepThreads, row = p / kPieces;
-        v[i] = make_uint4(0, 0, 0, 0);   // keys that are masked become zero rows
+        v[i] = make_uint4(0, 0, 0, 0);
         if (p < kPrepKeys * kPieces && slots[row] >= 0)
             v[i] = __ldg(reinterpret_cast<const uint4*>(a.pool + (int64_t)slots[row] * kWidth) +
                          p % kPieces);
@@ -137,6 +170,72 @@ __device__ void prepare_keys(const PrefixArgs& a, int64_t c)
             *reinterpret_cast<uint4*>(image + tile_offset(row0 + row, p % kPieces * 16, kKeys)) =
                 v[i];
     }
+}
+
+// Quarter c % 4 of own block c / 4, if a request's keys reach it.
+__device__ void prepare_own(const PrefixArgs& a, int c)
+{
+    const int block = c / 4, lane = threadIdx.x & 31;
+    // the last request whose first block is at most `block`: 32 probes a step
+    int lo = 0, n = a.batch;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int b = lo + lane * step;
+        const bool le = lane * step < n && (lane == 0 || own_block0(__ldg(a.kv_indptr + b), b) <= block);
+        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, le));
+        lo += hit * step;
+        n = min(step, n - hit * step);
+    }
+    int first;
+    const int len = own_length(a, lo, first);
+    const int k0 = (block - own_block0(first, lo)) * kKeys + c % 4 * kPrepKeys;
+    if (k0 < 0 || k0 >= (len + kKeys - 1) / kKeys * kKeys) return;
+    const int64_t at = prefix_image_blocks(a) + own_block0(first, lo);
+    prepare_keys(a, a.kv_indices + first, k0, len, a.k_image + at * kPrefixImage, a.k_valid + at * 4);
+}
+
+// Blocks before each tile, by one CTA; it also reports bad lengths.
+__device__ void prepare_tiles(const PrefixArgs& a)
+{
+    __shared__ int64_t part[kPrepThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int len = prefix_length(a);
+    if (tid == 0 && a.prefix_len != nullptr && __ldcg(a.prefix_len) != len)
+        atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
+    int64_t before = 0;
+    for (int64_t t0 = 0; t0 < a.tiles; t0 += kPrepThreads) {
+        const int64_t t = t0 + tid;
+        int64_t mine = 0;
+        if (t < a.tiles) {
+            mine = (len + kKeys - 1) / kKeys;
+            if (a.joined) {
+                int b0, b1;
+                tile_requests(a, t, b0, b1);
+                for (int b = b0; b <= b1; ++b) {
+                    int first;
+                    const int n = own_length(a, b, first);
+                    if (n != __ldg(a.seq_lens + b)) atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
+                    mine += (n + kKeys - 1) / kKeys;
+                }
+            }
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = incl;
+        __syncthreads();
+        int64_t base = before;
+        for (int w = 0; w < kPrepThreads / 32; ++w) {
+            if (w < warp) base += part[w];
+            before += part[w];
+        }
+        if (t < a.tiles) a.tile_start[t] = base + incl - mine;
+    }
+    if (tid == 0) a.tile_start[a.tiles] = before;
 }
 
 // Query row `item` (one warp) into its tile's image, rows 0..63 the high terms
@@ -187,35 +286,48 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
     if (lane == 0) {
         int64_t win = 0;
         if (on) {
-            // draft row t sees positions <= P + S_b - q_len + t: all of the
-            // prefix unless the request's own keys are fewer than the drafts
+            // draft row t sees positions <= P + S_b - q_len + t, the prefix's first
             const int64_t r = item / a.num_heads;
             const int b = (int)(r / a.q_len), t = (int)(r % a.q_len);
             const int cap = __ldg(a.kv_indptr + b + 1) - __ldg(a.kv_indptr + b);
             const int len = min(max(__ldg(a.seq_lens + b), 0), max(cap, 0));
             const int64_t P = prefix_length(a);
-            win = min(P, max((int64_t)0, P + len - a.q_len + t + 1));
+            win = max((int64_t)0, P + len - a.q_len + t + 1);
+            win = min(win, a.joined ? (int64_t)INT32_MAX : P);
         }
         a.q_scale[item] = on ? mul_pow2(a.logit_scale, -sh) : 0.f;
         a.q_window[item] = (int32_t)win;
     }
 }
 
+// CTA 0 ranks the tiles, then key_ctas CTAs of prefix keys, own_ctas of own keys
+// and the rest of queries.
 __global__ void __launch_bounds__(kPrepThreads)
-prefix_prepare_kernel(const PrefixArgs a, uint32_t key_ctas)
+prefix_prepare_kernel(const PrefixArgs a, int key_ctas, int own_ctas)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    if (blockIdx.x < key_ctas) prepare_keys(a, blockIdx.x);
-    else prepare_query(a, (int64_t)(blockIdx.x - key_ctas) * kPrepRows + (threadIdx.x >> 5));
+    int64_t c = blockIdx.x;
+    if (c == 0) {
+        prepare_tiles(a);
+    } else if ((c -= 1) < key_ctas) {
+        const int len = prefix_length(a);
+        if (c * kPrepKeys < (len + kKeys - 1) / kKeys * kKeys)
+            prepare_keys(a, a.prefix_indices, (int)c * kPrepKeys, len, a.k_image, a.k_valid);
+    } else if ((c -= key_ctas) < own_ctas) {
+        prepare_own(a, (int)c);
+    } else {
+        prepare_query(a, (c - own_ctas) * kPrepRows + (threadIdx.x >> 5));
+    }
 }
 
 // ---- prefix_split -----------------------------------------------------------------------------
 //
-// Warp 0 loads, warp 1 issues the MMAs, warps 4-11 are two softmax sets of four
+// Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests,
+// warps 4-11 are two softmax sets of four
 // warps; set s owns query rows 32 s .. 32 s + 31, warp w % 4 of a set the TMEM
 // lanes (keys) 32 (w % 4) .. + 31, one key per thread, as in the split kernel.
-// Warps 2-3 complete their warpgroup.
+// Warp 3 completes its warpgroup.
 //
 // A stage's four latent chunks are released one by one, as the P.V MMAs of that
 // chunk finish, so the next block's chunks stream in behind them; the RoPE
@@ -223,7 +335,7 @@ prefix_prepare_kernel(const PrefixArgs a, uint32_t key_ctas)
 // softmax works on block j, and P.V of block j - 1 before it.
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 0, kMmaWarp = 1, kSoftmaxWarp0 = 4;
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kTileWarp = 2, kSoftmaxWarp0 = 4;
 constexpr int kSets = 2, kSetRows = kRows / kSets;
 constexpr int kSoftmaxWarps = 4 * kSets;
 // 168 registers a thread at launch (384 x 168 <= 65536); the first warpgroup
@@ -259,7 +371,10 @@ struct PrefixShared {
     alignas(16) int win[kRows];
     alignas(16) float scale[kRows];   // epilogue: 1 / the sum of what the MMA consumed
     float red[kSoftmaxWarps][32];
-    float redt[kSoftmaxWarps][32];
+    // the tile's requests: own blocks before each, where its images start
+    uint64_t own_full;
+    int own_before[kRows + 1];
+    int own_image[kRows];
 };
 constexpr int kSmemBytes = kOffMisc + (int)sizeof(PrefixShared);
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's dynamic shared memory limit");
@@ -280,21 +395,64 @@ __device__ __forceinline__ float2 split_p(float a, float b, uint16_t& hi, uint16
     return __half22float2(*reinterpret_cast<const __half2*>(&sum));
 }
 
-// One run of blocks [b0, b1) of tile `tile`; `j0` blocks went before in this CTA
-// (the pipeline's phases go on counting).  Roles as above.  False after an abort.
+// A run: blocks [x0, x1) of a tile's list, the prefix's `shared` blocks and then its
+// requests' own.  `j0` blocks went before in this CTA (the pipeline's phases go
+// on counting), `run` runs.
 struct Run {
     int64_t tile;
-    int b0, b1;
-    int part;      // which of the tile's partials this run is
+    int x0, x1;
+    int shared;
+    int64_t slot;   // where its partial rows go
     int64_t j0;
-    int run;       // index of the run in this CTA
+    int run;
 };
+
+// The image of block x of the tile's list; for an own block k becomes its
+// request's number in the tile (x only grows from call to call).
+__device__ __forceinline__ int64_t image_of(const PrefixArgs& a, const PrefixShared& ms,
+                                            const Run& r, int x, int& k)
+{
+    if (x < r.shared) return x;
+    const int y = x - r.shared;
+    while (y >= ms.own_before[k + 1]) ++k;
+    return (int64_t)ms.own_image[k] + (y - ms.own_before[k]);
+}
+
+// Warp 2: the run's tile's requests into shared memory.
+__device__ __forceinline__ void tile_role(const PrefixArgs& a, PrefixShared& ms, const Run& r,
+                                          int lane)
+{
+    int b0 = 0, b1 = -1, before = 0;
+    if (r.x1 > r.shared) tile_requests(a, r.tile, b0, b1);
+    for (int k0 = 0; b0 + k0 <= b1; k0 += 32) {   // at most 64: a request has a row or more
+        const int b = b0 + k0 + lane;
+        int n = 0;
+        if (b <= b1) {
+            int first;
+            n = (own_length(a, b, first) + kKeys - 1) / kKeys;
+            ms.own_image[k0 + lane] = prefix_image_blocks(a) + own_block0(first, b);
+        }
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (b <= b1) ms.own_before[k0 + lane] = before + incl - n;
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) ms.own_before[b1 - b0 + 1] = before;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms.own_full);
+}
 
 __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, PrefixShared& ms,
                                           const Run& r, int lane)
 {
     volatile int* abort_flag = &ms.abort;
-    const int n = r.b1 - r.b0;
+    const int n = r.x1 - r.x0;
+    int k = 0;
+    bool own = false;   // the tile's requests have been looked up
     int64_t issued = 0, ropes = 0;   // latent chunks and RoPE chunks of this run
     if (lane == 0) {
         mbar_arrive_expect_tx(&ms.q_full, (uint32_t)kPrefixImage);
@@ -305,7 +463,11 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
     for (int j = 0; j < n && ok; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
-        const uint8_t* src = a.k_image + (int64_t)(r.b0 + j) * kPrefixImage;
+        if (!own && r.x0 + j >= r.shared) {
+            ok = own = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+            if (!ok) break;
+        }
+        const uint8_t* src = a.k_image + image_of(a, ms, r, r.x0 + j, k) * kPrefixImage;
         for (int c = 0; c < 4 && ok; ++c) {
             if (jj >= 2)
                 ok = warp_wait(&ms.k_empty[st][c], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
@@ -344,7 +506,7 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
                                          PrefixShared& ms, const Run& r)
 {
     volatile int* abort_flag = &ms.abort;
-    const int n = r.b1 - r.b0;
+    const int n = r.x1 - r.x0;
     constexpr uint32_t id_qk = idesc_e4m3(128, 2 * kRows, false, false);
     constexpr uint32_t id_hi = idesc_e4m3(128, kRows, true, true);
     constexpr uint32_t id_lo = idesc_e4m3(128, kRows, true, true, true);
@@ -452,8 +614,8 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     const int ti = quad * 32 + lane;                  // key within a block == TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     float* red = &ms.red[set * 4][0];
-    float* redt = &ms.redt[set * 4][0];
-    const int n = r.b1 - r.b0;
+    float* redt = reinterpret_cast<float*>(smem + kOffP) + set * 128;   // epilogue: P is idle
+    const int n = r.x1 - r.x0;
 
     // the rows' logit scales and windows (every set its own rows)
     if (ti < R) {
@@ -474,12 +636,25 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     for (int k = 0; k < R; ++k) nm[k] = l[k] = lt[k] = 0.f;
     bool alive = true;
     if (a.stall_probe) warp_wait(&ms.never, 0, abort_flag, 0, a.wait_limit);
-    uint32_t vnext = __ldcg(a.k_valid + (int64_t)r.b0 * 4 + quad);
+    // the requests of the tile, for the blocks of their own keys
+    const int P = prefix_length(a);
+    const int per = a.q_len * a.num_heads;
+    int k_next = 0, b0 = 0, b1;
+    bool own = false;
+    if (r.x1 > r.shared) tile_requests(a, r.tile, b0, b1);
+    auto valid_of = [&](int xb) -> uint32_t {   // of block xb, whose request k_next becomes
+        if (!own && xb >= r.shared)
+            own = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+        if (xb >= r.shared && !own) return 0;
+        return __ldcg(a.k_valid + image_of(a, ms, r, xb, k_next) * 4 + quad);
+    };
+    uint32_t vnext = valid_of(r.x0);
     for (int j = 0; j < n; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
+        const int xb = r.x0 + j, k_now = k_next;
         const uint32_t valid = vnext;
-        if (j + 1 < n) vnext = __ldcg(a.k_valid + (int64_t)(r.b0 + j + 1) * 4 + quad);
+        if (j + 1 < n) vnext = valid_of(xb + 1);
         const bool ok = warp_wait(&ms.s_full[st], (uint32_t)(jj >> 1) & 1, abort_flag, 0,
                                   a.wait_limit);
         float x[R];
@@ -516,18 +691,27 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
             x[4 * g + 2] = fmaf(x[4 * g + 2], c.z, nm[4 * g + 2]);
             x[4 * g + 3] = fmaf(x[4 * g + 3], c.w, nm[4 * g + 3]);
         }
-        // masked: keys past the prefix or with a bad slot, and in the blocks past
-        // the shortest row's window the positions that a row does not see
-        const int pos = (r.b0 + j) * kKeys + ti;
-        if (valid != 0xffffffffu || (r.b0 + j + 1) * kKeys > win_min) {
+        // masked: keys past their list or with a bad slot, positions that a row does
+        // not see, and own keys of another request than the row's
+        if (xb >= r.shared || valid != 0xffffffffu || (xb + 1) * kKeys > win_min) {
             const bool kval = (valid >> lane) & 1u;
+            int pos = xb * kKeys + ti;
+            uint32_t rows = 0xffffffffu;
+            if (xb >= r.shared) {
+                pos = P + (xb - r.shared - (own ? ms.own_before[k_now] : 0)) * kKeys + ti;
+                // rows of request b0 + k_now, as bits of this set's 32
+                const int64_t first = (int64_t)(b0 + k_now) * per - r.tile * kRows - r0;
+                const int lo = (int)max(first, (int64_t)0), hi = (int)min(first + per, (int64_t)R);
+                rows = hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
+            }
 #pragma unroll
             for (int g = 0; g < R / 4; ++g) {
                 const int4 w = reinterpret_cast<const int4*>(ms.win + r0)[g];
-                x[4 * g] = kval && pos < w.x ? x[4 * g] : -CUDART_INF_F;
-                x[4 * g + 1] = kval && pos < w.y ? x[4 * g + 1] : -CUDART_INF_F;
-                x[4 * g + 2] = kval && pos < w.z ? x[4 * g + 2] : -CUDART_INF_F;
-                x[4 * g + 3] = kval && pos < w.w ? x[4 * g + 3] : -CUDART_INF_F;
+                const int wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    x[4 * g + u] = kval && ((rows >> (4 * g + u)) & 1u) && pos < wv[u]
+                                       ? x[4 * g + u] : -CUDART_INF_F;
             }
         }
         float top = x[0];
@@ -634,15 +818,16 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
 
     // ---- epilogue: sums over the keys, then the rows out of TMEM, normalised by
     // what the MMA consumed (lt), and the LSE from the exact p (l) -------------------------
+    bool have;
     {
         const float sum = warp_transpose_reduce<R, false>(l, lane);
         const float fed = warp_transpose_reduce<R, false>(lt, lane);
         red[quad * 32 + lane] = sum;
+        have = alive && warp_wait(&ms.pv_done, (uint32_t)(r.j0 + n - 1) & 1, abort_flag, 0,
+                                  a.wait_limit);
+        if (have) tc_fence_after();
         redt[quad * 32 + lane] = fed;
     }
-    const bool have = alive && warp_wait(&ms.pv_done, (uint32_t)(r.j0 + n - 1) & 1, abort_flag, 0,
-                                         a.wait_limit);
-    if (have) tc_fence_after();
     softmax_bar(bar_id);
     if (ti < R) {
         const float fed = (redt[ti] + redt[32 + ti]) + (redt[64 + ti] + redt[96 + ti]);
@@ -681,7 +866,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
 #pragma unroll
             for (int k = 0; k < R; ++k)
                 if (k == ti) m = nm[k];
-            const int64_t at = item * a.parts + r.part;
+            const int64_t at = r.slot * kRows + r0 + ti;
             a.lse_part[at] = sum != 0.f ? log2f(sum) - m : -CUDART_INF_F;
             bulk_store(a.o_part + at * kDv, stage + (r0 + ti) * kDv, kDv * 4);
             bulk_commit();
@@ -713,6 +898,7 @@ prefix_split_kernel(const PrefixArgs a)
         mbar_init(&ms.p_full, kSoftmaxWarps);
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.mma_drain, 1);
+        mbar_init(&ms.own_full, 1);
         mbar_init(&ms.never, 1);
         ms.abort = 0;
         fence_mbar_init();
@@ -729,52 +915,83 @@ prefix_split_kernel(const PrefixArgs a)
     const uint32_t tmem = ms.tmem_base;
     const uint32_t smem_base = smem_u32(smem);
 
-    const int64_t blocks = (prefix_length(a) + kKeys - 1) / kKeys;
-    const int64_t U = blocks * a.tiles, G = min((int64_t)gridDim.x, U), g = blockIdx.x;
-    const int64_t u_begin = g < G ? g * U / G : 0, u_end = g < G ? (g + 1) * U / G : 0;
-    auto run_at = [&](int64_t u, int64_t j0, int idx) {
-        Run r;
-        r.tile = u / blocks;
-        r.b0 = (int)(u % blocks);
-        r.b1 = (int)min(blocks, r.b0 + (u_end - u));
-        r.part = (int)(g - cta_of(r.tile * blocks, U, G));
-        r.j0 = j0;
-        r.run = idx;
-        return r;
+    // this CTA's share: `left` blocks from block x of `tile` on
+    const int64_t g = blockIdx.x;
+    int64_t tile = 0, left = 0;
+    int x = 0;
+    if (a.splits > 0) {
+        tile = g / a.splits;
+        const int s = (int)(g % a.splits);
+        const int64_t nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
+        x = (int)(nb * s / a.splits);
+        left = nb * (s + 1) / a.splits - x;
+    } else {
+        const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)gridDim.x, U);
+        if (g < G) {
+            const int64_t u = g * U / G;
+            left = (g + 1) * U / G - u;
+            // the last tile that starts at or before u: 32 probes a step
+            int64_t n = a.tiles;
+            while (n > 1) {
+                const int64_t step = (n + 31) / 32;
+                const bool le = lane * step < n && __ldcg(a.tile_start + tile + lane * step) <= u;
+                const int hit = 31 - __clz(__ballot_sync(0xffffffffu, le));
+                tile += hit * step;
+                n = min(step, n - hit * step);
+            }
+            x = (int)(u - __ldcg(a.tile_start + tile));
+        }
+    }
+    const int shared = (prefix_length(a) + kKeys - 1) / kKeys;
+    int64_t j0 = 0;
+    int idx = 0;
+    // the next run, past tiles without blocks; false at the end
+    Run r;
+    auto next_run = [&]() -> bool {
+        while (left > 0) {
+            const int64_t nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
+            if (nb > x) {
+                r.tile = tile;
+                r.x0 = x;
+                r.x1 = (int)min(nb, x + left);
+                r.shared = shared;
+                r.slot = a.splits > 0 ? g : g + tile;
+                r.j0 = j0;
+                r.run = idx;
+                left -= r.x1 - r.x0;
+                j0 += r.x1 - r.x0;
+                ++idx;
+                ++tile;
+                x = 0;
+                return true;
+            }
+            ++tile;
+            x = 0;
+        }
+        return false;
     };
     // Registers move from the first warpgroup to the softmax warpgroups; each
     // branch below holds all of its warpgroups' remaining code.  Every thread
     // meets at the barrier that ends a run.
     if (warp < kSoftmaxWarp0) {
         regs_lower<kRegsLow>();
-        int64_t j0 = 0;
-        int idx = 0;
-        for (int64_t u = u_begin; u < u_end;) {
-            const Run r = run_at(u, j0, idx);
+        while (next_run()) {
             if (warp == kLoadWarp) load_role(a, smem, ms, r, lane);
             else if (warp == kMmaWarp) mma_role(a, smem_base, tmem, ms, r);
+            else if (warp == kTileWarp) tile_role(a, ms, r, lane);
             tc_fence_before();
             const bool stop = __syncthreads_or(ms.abort);
             tc_fence_after();
             if (stop) break;
-            u += r.b1 - r.b0;
-            j0 += r.b1 - r.b0;
-            ++idx;
         }
     } else {
         regs_raise<kRegsHigh>();
-        int64_t j0 = 0;
-        int idx = 0;
-        for (int64_t u = u_begin; u < u_end;) {
-            const Run r = run_at(u, j0, idx);
+        while (next_run()) {
             softmax_role(a, smem, tmem, ms, r, warp, lane);
             tc_fence_before();
             const bool stop = __syncthreads_or(ms.abort);
             tc_fence_after();
             if (stop) break;
-            u += r.b1 - r.b0;
-            j0 += r.b1 - r.b0;
-            ++idx;
         }
     }
     if (tid == 0 && ms.abort) atomicOr(a.err, MLA_DEVERR_TIMEOUT);
@@ -788,13 +1005,13 @@ prefix_split_kernel(const PrefixArgs a)
 
 // ---- prefix_merge -----------------------------------------------------------------------------
 //
-// One CTA per output row, four columns per thread.  The row's partials are the
-// prefix's (as many as CTAs took part of its tile) and the requests' own (one
-// per split): M = max lse, w = 2^(lse - M), o = sum w o_s / sum w, summed in
-// increasing order, lse = M + log2 sum w.  A partial of weight 0 is not read.
+// One CTA per output row, four columns per thread.  The row's partials are those
+// of the runs of its tile and, without joined tiles, the split kernel's:
+// M = max lse, w = 2^(lse - M), o = sum w o_s / sum w, summed in increasing
+// order, lse = M + log2 sum w.  A partial of weight 0 is not added.
 
 constexpr int kMergeThreads = 128;
-constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;
+constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;   // partials of one tile or one request: 256 each
 constexpr int kMergeAhead = 4;   // partials loaded before the weights are known
 
 __global__ void __launch_bounds__(kMergeThreads)
@@ -806,17 +1023,34 @@ prefix_merge_kernel(const PrefixArgs a)
     asm volatile("griddepcontrol.launch_dependents;");
     const int64_t item = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31;
-    int np = 0;
-    const int64_t blocks = (prefix_length(a) + kKeys - 1) / kKeys;
-    if (blocks > 0 && a.parts > 0) {
-        const int64_t U = blocks * a.tiles, G = min((int64_t)a.ctas, U), tile = item / kRows;
-        np = (int)(cta_of((tile + 1) * blocks - 1, U, G) - cta_of(tile * blocks, U, G)) + 1;
+    const int64_t tile = item / kRows;
+    // the tile's runs: slots [s0, s0 + np); a run without blocks has left nothing
+    int64_t s0 = 0;
+    int np = 0, nb = 0;
+    if (a.ctas > 0) {
+        const int64_t u0 = __ldcg(a.tile_start + tile), u1 = __ldcg(a.tile_start + tile + 1);
+        nb = (int)(u1 - u0);
+        if (a.splits > 0) {
+            s0 = tile * a.splits;
+            np = nb > 0 ? a.splits : 0;
+        } else if (nb > 0) {
+            const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)a.ctas, U);
+            const int64_t g0 = cta_of(u0, U, G);
+            s0 = g0 + tile;
+            np = (int)(cta_of(u1 - 1, U, G) - g0) + 1;
+        }
     }
+    auto left_out = [&](int i) {   // equal parts of few blocks: some are empty
+        return a.splits > nb && (int64_t)nb * i / a.splits == (int64_t)nb * (i + 1) / a.splits;
+    };
     const int n = np + a.own_splits;
     const float* own = a.o_own + item * a.own_splits * kDv;
-    const float* part = a.o_part + item * a.parts * kDv;
+    const float* part = a.o_part + (s0 * kRows + item % kRows) * kDv;
+    const float* lse_part = a.lse_part + s0 * kRows + item % kRows;
     const int c = tid * 4;
-    auto row_of = [&](int i) { return i < np ? part + (int64_t)i * kDv : own + (int64_t)(i - np) * kDv; };
+    auto row_of = [&](int i) {
+        return i < np ? part + (int64_t)i * (kRows * kDv) : own + (int64_t)(i - np) * kDv;
+    };
     float4 v[kMergeAhead];
 #pragma unroll
     for (int i = 0; i < kMergeAhead; ++i)
@@ -824,8 +1058,9 @@ prefix_merge_kernel(const PrefixArgs a)
     if (tid < 32) {
         float m = -CUDART_INF_F;
         for (int i = lane; i < n; i += 32) {
-            const float l = i < np ? __ldcg(a.lse_part + item * a.parts + i)
-                                   : __ldcg(a.lse_own + item * a.own_splits + (i - np));
+            float l = -CUDART_INF_F;
+            if (i >= np) l = __ldcg(a.lse_own + item * a.own_splits + (i - np));
+            else if (!left_out(i)) l = __ldcg(lse_part + i * kRows);
             w_s[i] = l;
             m = fmaxf(m, l);
         }
@@ -876,10 +1111,12 @@ cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream)
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (a.prefix_cap + kKeys - 1) / kKeys;
-    const uint32_t key_ctas = (uint32_t)(blocks * (kKeys / kPrepKeys));
-    const int64_t ctas = key_ctas + (int64_t)a.tiles * (kRows / kPrepRows);
-    e = launch_pdl(prefix_prepare_kernel, dim3((unsigned)ctas), kPrepThreads, 0, stream, a, key_ctas);
+    const int64_t key_ctas = prefix_blocks(a.prefix_cap) * (kKeys / kPrepKeys);
+    const int64_t own_ctas =
+        a.joined ? prefix_own_blocks(a.total_keys, a.batch) * (kKeys / kPrepKeys) : 0;
+    const int64_t ctas = 1 + key_ctas + own_ctas + (int64_t)a.tiles * (kRows / kPrepRows);
+    e = launch_pdl(prefix_prepare_kernel, dim3((unsigned)ctas), kPrepThreads, 0, stream, a,
+                   (int)key_ctas, (int)own_ctas);
     if (e != cudaSuccess) return e;
     return launch_pdl(prefix_split_kernel, dim3((unsigned)a.ctas), kThreads, kSmemBytes, stream, a);
 }

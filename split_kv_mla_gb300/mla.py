@@ -59,8 +59,9 @@ class mla_plan_t(ctypes.Structure):
 
 class mla_prefix_plan_t(ctypes.Structure):
     _fields_ = [
-        ("tiles", ctypes.c_int32), ("ctas", ctypes.c_int32), ("parts", ctypes.c_int32),
-        ("sm_count", ctypes.c_int32), ("workspace_bytes", ctypes.c_int64),
+        ("tiles", ctypes.c_int32), ("ctas", ctypes.c_int32), ("splits", ctypes.c_int32),
+        ("joined", ctypes.c_int32), ("sm_count", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("workspace_bytes", ctypes.c_int64),
         ("prefix_cap", ctypes.c_int64), ("own", mla_plan_t),
     ]
 

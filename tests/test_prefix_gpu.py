@@ -18,6 +18,7 @@ from split_kv_mla_gb300 import inputs as gen
 from split_kv_mla_gb300 import mla
 
 from gpu_util import compare
+from test_prefix_host import workspace_bytes
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +69,21 @@ def plan_of(s, cap=None, sms=None):
                                       sms or mla.sm_count())
 
 
+def variant(plan, **fields):
+    """The plan with other launch choices."""
+    p = mla.mla_prefix_plan_t.from_buffer_copy(plan)
+    for k, v in fields.items():
+        setattr(p, k, v)
+    p.workspace_bytes = workspace_bytes(p)
+    return p
+
+
+def both(s):
+    """The plan with the requests' own keys in the tiles, and in the split kernel."""
+    plan = plan_of(s)
+    return [variant(plan, joined=j) for j in ((0, 1) if s.own.total_keys and plan.ctas else (0,))]
+
+
 def run(s, plan=None, ws=None, d=None, **kw):
     d = d or to_cuda(s)
     plan = plan or plan_of(s)
@@ -93,27 +109,62 @@ def check(s, what="", errors=0, **kw):
     (7, 3, 131, [7, 8]), (1, 16, 5000, [600] * 9), (1, 128, 4096, [17, 400, 3, 90]),
     (1, 33, 8192, [50] * 20), (8, 128, 700, [11, 40])])
 def test_prefix(q_len, heads, P, lens):
-    check(make(q_len, heads, P, lens, seed=P + heads), f"q{q_len} H{heads} P{P}")
+    s = make(q_len, heads, P, lens, seed=P + heads)
+    for plan in both(s):
+        check(s, f"q{q_len} H{heads} P{P} joined {plan.joined}", plan=plan)
 
 
-@pytest.mark.parametrize("sms", [1, 2, 3, 7, 37, 152])
-def test_any_split_of_the_prefix(sms):
-    # runs that end inside tiles, several tiles per CTA, CTAs of one block
-    s = make(1, 24, 1500, [5, 0, 300, 17, 64, 9, 1, 80, 33, 2, 140], seed=sms)
-    check(s, f"{sms} SMs", plan=plan_of(s, sms=sms))
+@pytest.mark.parametrize("heads,lens", [
+    (1, [3, 0, 0, 200, 1, 0, 129] * 11), (2, [5] * 33), (24, [5, 300, 17, 64, 9, 1, 80, 33, 2]),
+    (24, [0, 0, 0, 0, 0]), (128, [1, 128, 129, 0, 700]), (65, [50, 60, 70]), (96, [300, 2])])
+@pytest.mark.parametrize("ctas,splits", [(1, 0), (2, 0), (3, 0), (5, 0), (11, 0), (37, 0),
+                                         (152, 0), (None, 1), (None, 2), (None, 13)])
+def test_any_cut_of_the_blocks(heads, lens, ctas, splits):
+    # runs that end inside tiles, several tiles per CTA, CTAs of one block or none,
+    # tiles of many requests and requests of several tiles
+    s = make(1, heads, 500, lens, seed=heads)
+    plan = plan_of(s)
+    ctas = ctas or plan.tiles * splits
+    for joined in (0, 1) if s.own.total_keys else (0,):
+        check(s, f"{ctas} CTAs, {splits} splits, joined {joined}",
+              plan=variant(plan, ctas=ctas, splits=splits, joined=joined))
 
 
-@pytest.mark.parametrize("ctas", [1, 2, 4, 5, 6, 11, 24, 60, 148])
-def test_forced_cta_counts(ctas):
-    s = make(1, 24, 1500, [5, 0, 300, 17, 64, 9, 1, 80, 33, 2, 140], seed=3)
-    plan = plan_of(s, sms=152)
-    assert plan.tiles == 5
-    parts = ctas // 5 if ctas % 5 == 0 else -(-ctas // 5) + 1
-    rows = 11 * 24
-    up = lambda x: -(-x // 256) * 256  # noqa: E731
-    plan.workspace_bytes += sum(up(rows * parts * n) - up(rows * plan.parts * n) for n in (2048, 4))
-    plan.ctas, plan.parts = ctas, parts
-    check(s, f"{ctas} CTAs", plan=plan)
+def test_one_request_far_longer_than_the_others():
+    s = make(1, 16, 600, [3, 5000, 0, 40, 7, 1, 1, 900], seed=21)
+    for plan in both(s):
+        check(s, f"skewed, joined {plan.joined}", plan=plan)
+        check(s, f"skewed, joined {plan.joined}", plan=variant(plan, ctas=152, splits=0))
+
+
+def test_tables_with_room_to_spare():
+    # a table longer than its request's length, starting past entry 0
+    s = make(2, 16, 300, [30, 0, 150], seed=22)
+    own = s.own
+    lens, ptr = own.seq_lens, own.kv_indptr
+    new_ptr = torch.tensor([7, 7 + 200, 7 + 203, 7 + 203 + 150]).int()
+    idx = torch.full((int(new_ptr[-1]),), 2 ** 30, dtype=torch.int32)
+    for b in range(3):
+        idx[int(new_ptr[b]):int(new_ptr[b]) + int(lens[b])] = \
+            own.kv_indices[int(ptr[b]):int(ptr[b]) + int(lens[b])]
+    d = to_cuda(s)
+    d.update(kv_indices=idx.cuda(), kv_indptr=new_ptr.cuda())
+    base = mla.mla_prefix_decode_plan(3, 2, 16, 300, idx.numel(), mla.sm_count())
+    for joined in (0, 1):
+        check(s, f"spare, joined {joined}", plan=variant(base, joined=joined), d=d)
+
+
+def test_bad_lengths_are_clamped_and_reported():
+    s = make(1, 16, 300, [30, 20, 150], seed=23)
+    for joined in (0, 1):
+        plan = variant(plan_of(s), joined=joined)
+        d = to_cuda(s)
+        d["seq_lens"] = torch.tensor([30, 21, -4], dtype=torch.int32, device="cuda")
+        (o, lse), ws = run(s, plan, d=d)
+        assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_LENGTH
+        cut = dataclasses.replace(s.own, seq_lens=torch.tensor([30, 20, 0]).int())
+        ro, rl = oracle.dense_decode(join(cut, s.prefix).joined)
+        compare(o, lse, ro, rl, f"joined {joined}")
 
 
 def test_no_prefix_and_no_keys_at_all():
@@ -129,7 +180,13 @@ def test_no_prefix_and_no_keys_at_all():
 def test_length_on_the_device():
     # one plan and one captured graph serve every length up to the capacity
     s = make(2, 16, 1400, [30, 2, 250], seed=8)
-    d, plan = to_cuda(s), plan_of(s)
+    for plan in both(s):
+        lengths_on_the_device(s, plan)
+    lengths_on_the_device(s, variant(plan_of(s), ctas=40, splits=0))
+
+
+def lengths_on_the_device(s, plan):
+    d = to_cuda(s)
     ws = mla.workspace(plan)
     n = torch.tensor([1400], dtype=torch.int32, device="cuda")
     run(s, plan, ws, d, prefix_len=n)
@@ -158,10 +215,12 @@ def test_length_on_the_device():
 def test_drafts_that_reach_back_into_the_prefix():
     # fewer own keys than draft rows: the first rows do not see the prefix's end
     s = make(4, 16, 300, [0, 1, 2, 3, 4], seed=9)
-    check(s, "window in the prefix")
+    for plan in both(s):
+        check(s, "window in the prefix", plan=plan)
     s = make(6, 8, 3, [0, 1, 2], seed=10)   # rows that see nothing at all
-    o, lse = check(s, "empty rows")
-    assert bool((lse[0] == -float("inf")).all()) and bool((o[0] == 0).all())
+    for plan in both(s):
+        o, lse = check(s, "empty rows", plan=plan)
+        assert bool((lse[0] == -float("inf")).all()) and bool((o[0] == 0).all())
 
 
 def test_same_slots_twice_and_joined_decode():
@@ -170,7 +229,8 @@ def test_same_slots_twice_and_joined_decode():
     s.own.kv_indices[:20] = s.prefix[100:120]
     s.prefix[5:9] = s.prefix[5]
     s = join(s.own, s.prefix)
-    o, lse = check(s, "repeated slots")
+    for plan in both(s):
+        o, lse = check(s, "repeated slots", plan=plan)
     j = s.joined
     plan = mla.mla_decode_plan(j.batch, 1, 16, j.total_keys, mla.sm_count())
     o2, lse2 = mla.mla_decode(plan, j.q_lat.cuda(), j.q_pe.cuda(), j.pool.cuda(),
@@ -203,7 +263,9 @@ def test_number_format_edges(edge):
         gen.share_query_across_heads(own)
         joined = join(own, s.prefix).joined
         own.pool = gen.plant_dominant_key(joined, 0.8, 7).pool
-    check(join(own, s.prefix), edge)
+    s = join(own, s.prefix)
+    for plan in both(s):
+        check(s, edge, plan=plan)
 
 
 @pytest.mark.parametrize("gap", [6.0, 10.0, 13.0])
@@ -222,29 +284,45 @@ def test_one_sink_key_over_many_weak_ones(gap):
 
 def test_masked_rows_are_never_read_and_bad_slots_are_reported():
     s = make(1, 16, 500, [40, 9], seed=14)
-    want, _ = run(s)
+    for plan in both(s):
+        masked_rows(s, plan)
+
+
+def masked_rows(s, plan):
+    want, _ = run(s, plan)
     own = s.own
     nan = own.pool.clone()
     used = torch.cat([s.prefix, own.kv_indices]).long()
     idle = torch.ones(nan.shape[0], dtype=torch.bool)
     idle[used] = False
     nan[idle] = 0x7F   # NaN codes in every row that no table names
-    got, _ = run(Shared(dataclasses.replace(own, pool=nan), s.joined, s.prefix))
+    got, _ = run(Shared(dataclasses.replace(own, pool=nan), s.joined, s.prefix), plan)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     # a bad slot is skipped and reported
     for bad in (-1, own.pool.shape[0], 2 ** 31 - 1, -2 ** 31):
         p = s.prefix.clone()
         p[130] = bad
-        (o, lse), ws = run(Shared(own, s.joined, p))
+        (o, lse), ws = run(Shared(own, s.joined, p), plan)
         assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_SLOT
         keep = torch.cat([s.prefix[:130], s.prefix[131:]])
         ro, rl = oracle.dense_decode(join(own, keep).joined)
         compare(o, lse, ro, rl, "bad slot")
+        idx = own.kv_indices.clone()
+        idx[44] = bad   # the fifth of the second request's nine
+        (o, lse), ws = run(Shared(dataclasses.replace(own, kv_indices=idx), s.joined, s.prefix),
+                           plan)
+        assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_SLOT
+        short = dataclasses.replace(
+            own, kv_indices=torch.cat([own.kv_indices[:44], own.kv_indices[45:]]),
+            seq_lens=torch.tensor([40, 8]).int(), kv_indptr=torch.tensor([0, 40, 48]).int())
+        ro, rl = oracle.dense_decode(join(short, s.prefix).joined)
+        compare(o, lse, ro, rl, "bad own slot")
 
 
 def test_a_query_with_nan_or_inf_stays_in_its_row():
     s = make(1, 16, 400, [30, 5, 60, 2, 9], seed=15)
     want, _ = run(s)
+    assert plan_of(s).joined == 1
     q = s.own.q_lat.clone()
     q[1, 3, 7] = float("nan")
     q[2, 0, 500] = float("inf")
@@ -253,6 +331,7 @@ def test_a_query_with_nan_or_inf_stays_in_its_row():
     same[1, 3] = same[2, 0] = False
     assert torch.equal(got[0][same.cuda()], want[0][same.cuda()])
     assert torch.equal(got[1][same.cuda()], want[1][same.cuda()])
+    assert bool(torch.isnan(got[0][1, 3]).all()) and bool(torch.isnan(got[1][1, 3]))
 
 
 def test_repeat_permuted_pool_and_given_outputs():
@@ -315,7 +394,11 @@ def test_pool_past_four_gigabytes():
 
 def test_a_wait_that_runs_out_ends_the_call():
     s = make(1, 64, 1000, [30, 5], seed=20)
-    plan = plan_of(s)
+    for plan in both(s) + [variant(plan_of(s), ctas=2, splits=0, joined=1)]:
+        wait_runs_out(s, plan)
+
+
+def wait_runs_out(s, plan):
     ws = mla.workspace(plan)
     mla.mla_debug_wait_limit(300)
     try:

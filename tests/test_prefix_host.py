@@ -30,50 +30,101 @@ SHAPES = [(1, 1, 1, 1, 0), (1, 1, 16, 127, 5), (4, 1, 16, 1024, 130), (64, 1, 16
           (0, 1, 16, 100, 0), (65535, 1, 1, 300, 65535)]
 
 
+def workspace_bytes(p):
+    """The plan's workspace from its other fields."""
+    def up(x):
+        return -(-x // 256) * 256
+    rows = p.own.batch * p.own.q_len * p.own.num_heads
+    blocks = -(-p.prefix_cap // 128)
+    own = 0 if p.joined or p.own.total_keys == 0 else rows * p.own.num_splits
+    if p.joined:
+        blocks += p.own.total_keys // 128 + p.own.batch
+    slots = 0 if p.ctas == 0 else p.ctas if p.splits else p.ctas + p.tiles
+    tiles = p.tiles if p.ctas else 0
+    return mla.MLA_WORKSPACE_HEADER_BYTES + sum(map(up, (
+        own * 2048, own * 4, slots * 64 * 2048, slots * 64 * 4, blocks * 73728, blocks * 16,
+        tiles * 73728, tiles * 256, tiles * 256, (tiles + 1) * 8 if tiles else 0)))
+
+
 @pytest.mark.parametrize("batch,q_len,heads,cap,total", SHAPES)
 @pytest.mark.parametrize("sms", [1, 20, 152])
 def test_plan_invariants(lib, batch, q_len, heads, cap, total, sms):
     p = mla.mla_prefix_decode_plan(batch, q_len, heads, cap, total, sms)
     rows = batch * q_len * heads
-    blocks = -(-cap // 128)
     assert p.tiles == -(-rows // 64)
     assert (p.prefix_cap, p.sm_count) == (cap, sms)
     assert p.own.as_dict() == mla.mla_decode_plan(batch, q_len, heads, total, sms).as_dict()
     if cap == 0 or rows == 0:
-        assert (p.ctas, p.parts) == (0, 0)
+        assert (p.ctas, p.splits, p.joined) == (0, 0, 0)
     else:
-        assert 1 <= p.ctas <= sms and p.ctas <= p.tiles * blocks and 1 <= p.parts <= 256
-    def up(x):
-        return -(-x // 256) * 256
-    ns, tiles = p.own.num_splits, p.tiles if p.parts else 0
-    want = mla.MLA_WORKSPACE_HEADER_BYTES + sum(map(up, (
-        rows * ns * 2048, rows * ns * 4, rows * p.parts * 2048, rows * p.parts * 4,
-        blocks * 73728, blocks * 16, tiles * 73728, tiles * 256, tiles * 256)))
-    assert p.workspace_bytes == want
+        assert 1 <= p.ctas <= sms and p.ctas == (p.tiles * p.splits or p.ctas)
+        assert p.joined in (0, 1) and not (p.joined and total == 0)
+    assert p.workspace_bytes == workspace_bytes(p)
     q = mla.mla_prefix_decode_plan(batch, q_len, heads, cap, total, sms)
     assert bytes(p) == bytes(q)
 
 
-@pytest.mark.parametrize("batch,q_len,heads,cap,total", SHAPES)
-def test_every_length_fits_the_planned_partials(lib, batch, q_len, heads, cap, total):
-    # runs of (tile, block) pairs as the kernel deals them out: every pair once, a
-    # tile's runs numbered 0, 1, ... below parts, whatever the length in use
-    p = mla.mla_prefix_decode_plan(batch, q_len, heads, cap, total, 152)
-    if p.parts == 0:
-        return
-    T = min(p.tiles, 300)
-    most = -(-cap // 128)
-    for blocks in sorted({1, 2, 3, 7, most // 3 + 1, most - 1, most} & set(range(1, most + 1))):
-        U = p.tiles * blocks
-        G = min(p.ctas, U)
-        def first(u):
-            return ((u + 1) * G - 1) // U
-        for t in range(T):
-            cut = [g * U // G for g in range(first(t * blocks), first((t + 1) * blocks - 1) + 2)]
-            assert cut[0] <= t * blocks < cut[1]
-            assert cut[-2] < (t + 1) * blocks <= cut[-1]
-            assert len(cut) - 1 <= p.parts
-            assert all(b > a for a, b in zip(cut, cut[1:]))
+def test_plan_choices(lib):
+    # short own keys join the tiles, long ones go through the split kernel (measured);
+    # many tiles are cut into equal runs, few into equal parts
+    def of(*a):
+        p = mla.mla_prefix_decode_plan(*a, 152)
+        return p.ctas, p.splits, p.joined
+    assert of(64, 1, 16, 8192, 64 * 264) == (144, 9, 1)
+    assert of(64, 1, 16, 8192, 64 * 8192)[2] == 0
+    assert of(64, 1, 128, 32768, 64 * 512) == (152, 0, 1)
+    assert of(8, 4, 16, 32001, 8 * 150) == (152, 19, 1)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_runs_cover_every_block_once(seed):
+    # blocks of tiles (some empty) as the kernel deals them out: each once, in order,
+    # and no two runs share a slot
+    import random
+    rng = random.Random(seed)
+    tiles = rng.choice([1, 2, 5, 16, 130, 700])
+    nb = [rng.choice([0, 1, 3, 64, rng.randrange(300)]) for _ in range(tiles)]
+    start = [0]
+    for n in nb:
+        start.append(start[-1] + n)
+    seen, slots = [], set()
+    splits = rng.choice([0, 1, 7, 19])
+    ctas = tiles * splits or rng.choice([1, 2, 37, 152])
+    U = start[-1]
+    G = min(ctas, U)
+    runs_of = [[] for _ in range(tiles)]
+    for g in range(ctas):
+        if splits:
+            t, s = divmod(g, splits)
+            x0, x1 = nb[t] * s // splits, nb[t] * (s + 1) // splits
+            runs = [(t, x0, x1, g)] if x1 > x0 else []
+        else:
+            runs = []
+            u, end = (g * U // G, (g + 1) * U // G) if g < G else (0, 0)
+            while u < end:
+                t = max(i for i in range(tiles) if start[i] <= u and nb[i] > 0)
+                x0 = u - start[t]
+                x1 = min(nb[t], x0 + end - u)
+                runs.append((t, x0, x1, g + t))
+                u += x1 - x0
+        for t, x0, x1, slot in runs:
+            seen += [(t, x) for x in range(x0, x1)]
+            assert slot not in slots
+            slots.add(slot)
+            runs_of[t].append(slot)
+    assert sorted(seen) == [(t, x) for t in range(tiles) for x in range(nb[t])]
+    for t in range(tiles):   # where the merge looks
+        if nb[t] == 0:
+            assert runs_of[t] == []
+        elif splits:
+            want = [t * splits + s for s in range(splits)
+                    if nb[t] * s // splits < nb[t] * (s + 1) // splits]
+            assert runs_of[t] == want
+        else:
+            g0 = ((start[t] + 1) * G - 1) // U
+            g1 = (start[t + 1] * G - 1) // U
+            assert runs_of[t] == list(range(g0 + t, g1 + t + 1))
+            assert max(runs_of[t]) < ctas + tiles
 
 
 def test_plan_refusals(lib):
@@ -113,12 +164,14 @@ def test_call_refusals(lib, want, kw):
 def test_tampered_plans_are_refused(lib):
     good = mla.mla_prefix_decode_plan(2, 1, 16, 1000, 100, 152)
     assert call(lib, None) == INVALID
-    for field, value in [("tiles", 2), ("ctas", 0), ("ctas", -3), ("parts", 0), ("parts", 300),
-                         ("workspace_bytes", 1 << 20), ("prefix_cap", 5000), ("prefix_cap", -1),
-                         ("prefix_cap", 0)]:
+    for field, value in [("tiles", 2), ("ctas", 0), ("ctas", -3), ("ctas", 300), ("splits", -1),
+                         ("splits", 300), ("splits", good.splits + 1), ("joined", 2),
+                         ("joined", 1 - good.joined), ("workspace_bytes", 1 << 20),
+                         ("prefix_cap", 5000), ("prefix_cap", -1), ("prefix_cap", 0)]:
         p = mla.mla_prefix_plan_t.from_buffer_copy(good)
         setattr(p, field, value)
-        assert call(lib, p) == INVALID, field
+        if (p.ctas, p.splits) == (good.ctas, good.splits) or not good.splits:
+            assert call(lib, p) == INVALID, field
     for field, value in [("num_splits", 3), ("grid_x", 9), ("variant", 1), ("merge_cluster", 2),
                          ("workspace_bytes", 4), ("d_v", 448), ("total_keys", -1)]:
         p = mla.mla_prefix_plan_t.from_buffer_copy(good)

@@ -168,37 +168,39 @@ __device__ __forceinline__ float row_sum(float v)
     return v;
 }
 
-// One row of 64 K columns per eight lanes, normed over its first `norm_cols`.
+// 1 / rms over the row's first `norm_cols` columns (1 without a norm).  The whole
+// warp calls it.
 template <int K>
-__device__ __forceinline__ void norm_row(const uint4 (&v)[K], int norm_cols,
-                                         const uint16_t* weight, float eps, int l,
-                                         float (&x)[K][8])
+__device__ __forceinline__ float inv_rms(const uint4 (&v)[K], int norm_cols, float eps)
 {
-#pragma unroll
-    for (int k = 0; k < K; ++k) unpack8(v[k], x[k]);
-    if (norm_cols == 0) return;
+    if (norm_cols == 0) return 1.f;
     const int n = norm_cols / 64;   // pieces of this lane that take part
     float sq = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
         if (k < n) {
+            float x[8];
+            unpack8(v[k], x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(x[k][j], x[k][j], sq);
+            for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
         }
-    const float r = 1.f / sqrtf(row_sum(sq) / (float)norm_cols + eps);
+    return 1.f / sqrtf(row_sum(sq) / (float)norm_cols + eps);
+}
+
+// Piece k of a row, normed: x_j r w_j (w = 1 without weights).
+__device__ __forceinline__ void norm_piece(uint4 v, int k, float r, const uint16_t* weight, int l,
+                                           float (&x)[8])
+{
+    unpack8(v, x);
+    if (weight != nullptr) {
+        float w[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 64 * k + 8 * l)), w);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (k < n) {
-            float w[8];
-            if (weight != nullptr) {
-                unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 64 * k + 8 * l)), w);
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+    } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * r * w[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] *= r;
-            }
-        }
+        for (int j = 0; j < 8; ++j) x[j] *= r;
+    }
 }
 
 // The position of token t, or -1 (reported by the caller's lane 0) if it is
@@ -226,65 +228,74 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int64_t t, int l
     for (int k = 0; k < K; ++k)
         v[k] = write ? load_once(a.kv + t * a.kv_stride + 64 * k + 8 * l) : make_uint4(0, 0, 0, 0);
     const Turn turn = load_turn(a.cos_sin + (write ? pos : 0) * 64, l, a.half_split != 0);
-    float x[K][8];
-    norm_row<K>(v, a.kv_norm_cols, a.kv_weight, a.eps, l, x);
-    rotate(x[K - 1], turn, a.half_split != 0);
-    if (!write) return;
-    uint8_t* row = a.pool + (int64_t)slot * (64 * K) + 8 * l;
+    const float r = inv_rms<K>(v, a.kv_norm_cols, a.eps);
+    uint8_t* row = a.pool + (int64_t)(write ? slot : 0) * (64 * K) + 8 * l;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+        float x[8];
+        if (64 * k < a.kv_norm_cols) norm_piece(v[k], k, r, a.kv_weight, l, x);
+        else unpack8(v[k], x);
+        if (k == K - 1) rotate(x, turn, a.half_split != 0);
         uint32_t w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            w[i] = (uint32_t)f32x2_to_e4m3x2(x[k][4 * i] * a.inv_scale, x[k][4 * i + 1] * a.inv_scale) |
-                   ((uint32_t)f32x2_to_e4m3x2(x[k][4 * i + 2] * a.inv_scale,
-                                              x[k][4 * i + 3] * a.inv_scale) << 16);
-        *reinterpret_cast<uint2*>(row + 64 * k) = make_uint2(w[0], w[1]);
+            w[i] = (uint32_t)f32x2_to_e4m3x2(x[4 * i] * a.inv_scale, x[4 * i + 1] * a.inv_scale) |
+                   ((uint32_t)f32x2_to_e4m3x2(x[4 * i + 2] * a.inv_scale,
+                                              x[4 * i + 3] * a.inv_scale) << 16);
+        if (write) *reinterpret_cast<uint2*>(row + 64 * k) = make_uint2(w[0], w[1]);
     }
 }
 
 // U heads of one token per eight lanes, their loads in flight together and the
 // angles loaded once.
 template <int K, int U>
-__device__ __forceinline__ void query_rows(const AppendArgs& a, int64_t group, int l)
+__device__ __forceinline__ void query_rows(const AppendArgs& a, int64_t first, int g, int l)
 {
-    const int per = (a.heads + U - 1) / U;
-    const int64_t t = group / per;
-    const int h0 = (int)(group % per) * U;
+    // group `first` + g: the CTA's first one is found once, the others from it
+    const uint32_t per = (uint32_t)(a.heads + U - 1) / U;
+    const uint32_t off = (uint32_t)(first % per) + g;
+    const int64_t t = first / per + off / per;
+    const int h0 = (int)(off % per) * U;
     const bool on = t < a.tokens;
     const int64_t pos = on ? position_of(a, (int)t) : -1;
     if (on && pos < 0 && l == 0 && h0 == 0) atomicOr(a.err, MLA_DEVERR_BAD_POSITION);
     const bool half = a.half_split != 0;
+    const uint16_t* q = a.q + (on ? t : 0) * a.q_token_stride + 8 * l;
     uint4 v[U][K];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            v[u][k] = pos >= 0 && h0 + u < a.heads
-                ? load_once(a.q + t * a.q_token_stride + (h0 + u) * a.q_head_stride + 64 * k + 8 * l)
-                : make_uint4(0, 0, 0, 0);
+            v[u][k] = on && h0 + u < a.heads ? load_once(q + (h0 + u) * a.q_head_stride + 64 * k)
+                                             : make_uint4(0, 0, 0, 0);
     const Turn turn = load_turn(a.cos_sin + (pos >= 0 ? pos : 0) * 64, l, half);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float x[K][8];
-        norm_row<K>(v[u], a.q_norm ? 64 * K : 0, a.q_weight, a.eps, l, x);
-        rotate(x[K - 1], turn, half);
-        if (pos < 0 || h0 + u >= a.heads) continue;
+        const bool write = pos >= 0 && h0 + u < a.heads;
         const int64_t row = t * a.heads + h0 + u;
+        const float r = inv_rms<K>(v[u], a.q_norm ? 64 * K : 0, a.eps);
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-            __stcs(reinterpret_cast<uint4*>(a.q_nope + row * (64 * (K - 1)) + 64 * k + 8 * l),
-                   pack8(x[k]));
-        __stcs(reinterpret_cast<uint4*>(a.q_pe + row * 64 + 8 * l), pack8(x[K - 1]));
+        for (int k = 0; k < K; ++k) {
+            uint4 y = v[u][k];   // without a norm the other columns pass through
+            if (a.q_norm || k == K - 1) {
+                float x[8];
+                if (a.q_norm) norm_piece(y, k, r, a.q_weight, l, x);
+                else unpack8(y, x);
+                if (k == K - 1) rotate(x, turn, half);
+                y = pack8(x);
+            }
+            uint16_t* to = k < K - 1 ? a.q_nope + row * (64 * (K - 1)) + 64 * k : a.q_pe + row * 64;
+            if (write) __stcs(reinterpret_cast<uint4*>(to + 8 * l), y);
+        }
     }
 }
 
-// Heads per eight lanes: about four 16-byte loads of queries in flight a lane.
+// Heads per eight lanes: about six 16-byte loads of queries in flight a lane.
 template <int K>
-constexpr int kHeads = K == 1 ? 4 : K == 2 ? 2 : 1;
+constexpr int kHeads = K == 1 ? 4 : K <= 3 ? 2 : 1;
 
 template <int KKV, int KQ>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 4)
 append_kernel(const AppendArgs a)
 {
     wait_for_predecessor();
@@ -293,8 +304,7 @@ append_kernel(const AppendArgs a)
     if (blockIdx.x < a.kv_ctas)
         append_row<KKV>(a, (int64_t)blockIdx.x * kAppendRows + g, l);
     else
-        query_rows<KQ, kHeads<KQ>>(
-            a, (int64_t)(blockIdx.x - a.kv_ctas) * kAppendRows + g, l);
+        query_rows<KQ, kHeads<KQ>>(a, (int64_t)(blockIdx.x - a.kv_ctas) * kAppendRows, g, l);
 }
 
 template <int KKV, int KQ>
@@ -334,31 +344,33 @@ cudaError_t launch_append_q(const AppendArgs& a, bool kv, int kq, cudaStream_t s
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 8;
 
-// Lane i < kCopyRows of the warp holds row i's source and destination slot
-// (dst < 0: none).  The whole warp calls it.
+// Lane first + i, i < kCopyRows, of the warp holds row i's source and destination
+// slot (dst < 0: none).  The whole warp calls it.
 template <int WIDTH>
-__device__ __forceinline__ void copy_rows(uint8_t* pool, int32_t src, int32_t dst, int lane)
+__device__ __forceinline__ void copy_rows(uint8_t* pool, int32_t src, int32_t dst, int lane,
+                                          int first = 0)
 {
     constexpr int kPieces = WIDTH / 16;
     constexpr int kPer = kCopyRows * kPieces / 32;
     static_assert(kCopyRows * kPieces % 32 == 0, "pieces deal out evenly");
     uint4 v[kPer];
-    int32_t to[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int i = lane + 32 * k, row = i / kPieces, piece = i % kPieces;
-        const int32_t from = __shfl_sync(0xffffffffu, src, row);
-        to[k] = __shfl_sync(0xffffffffu, dst, row);
-        if (to[k] >= 0)
+        const int32_t from = __shfl_sync(0xffffffffu, src, first + row);
+        const int32_t to = __shfl_sync(0xffffffffu, dst, first + row);
+        if (to >= 0)
             v[k] = __ldcs(reinterpret_cast<const uint4*>(pool + (int64_t)from * WIDTH) + piece);
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        const int piece = (lane + 32 * k) % kPieces;
-        if (to[k] >= 0)
-            reinterpret_cast<uint4*>(pool + (int64_t)to[k] * WIDTH)[piece] = v[k];
+        const int i = lane + 32 * k, row = i / kPieces, piece = i % kPieces;
+        const int32_t to = __shfl_sync(0xffffffffu, dst, first + row);
+        if (to >= 0) __stcs(reinterpret_cast<uint4*>(pool + (int64_t)to * WIDTH) + piece, v[k]);
     }
 }
+
+constexpr int64_t kForkManyEntries = 1 << 17;
 
 struct ForkArgs {
     uint8_t* pool;
@@ -434,7 +446,9 @@ __device__ __forceinline__ void fork_entry(const ForkArgs& a, int64_t i, int32_t
     a.table[i] = entry;
 }
 
-template <int WIDTH>
+// A warp takes B * kCopyRows table entries, one per lane, and copies their rows in
+// B turns.
+template <int WIDTH, int B>
 __global__ void __launch_bounds__(kCopyThreads)
 fork_kernel(const ForkArgs a)
 {
@@ -443,8 +457,12 @@ fork_kernel(const ForkArgs a)
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
     int32_t src = -1, dst = -1;
-    if (lane < kCopyRows) fork_entry(a, warp * kCopyRows + lane, src, dst);
-    if (__any_sync(0xffffffffu, dst >= 0)) copy_rows<WIDTH>(a.pool, src, dst, lane);
+    if (lane < B * kCopyRows) fork_entry(a, warp * (B * kCopyRows) + lane, src, dst);
+    const uint32_t any = __ballot_sync(0xffffffffu, dst >= 0);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+        if ((any >> (b * kCopyRows)) & ((1u << kCopyRows) - 1u))
+            copy_rows<WIDTH>(a.pool, src, dst, lane, b * kCopyRows);
 }
 
 // ---- compaction -------------------------------------------------------------------------------
@@ -458,6 +476,8 @@ fork_kernel(const ForkArgs a)
 //   count   the live slots of each chunk of 8192;
 //   place   ranks: u at every bitmap word, the lists of holes and of tail rows;
 //   move    copies the tail rows and rewrites the table.
+// A small pool's mark, count and place are one CTA's work on a bitmap in shared
+// memory (rank_kernel).
 
 constexpr int kPlaceThreads = 256;                       // one bitmap word each
 constexpr int64_t kChunkSlots = kPlaceThreads * 32;
@@ -504,6 +524,23 @@ __device__ __forceinline__ int block_sum(int v, int* part)
 #pragma unroll
     for (int w = 0; w < kPlaceThreads / 32; ++w) s += part[w];
     return s;
+}
+
+// A warp's 32 bitmap words from `word` on, one per lane with u at its first slot:
+// their holes and tail rows into the lists, a word at a time, a slot per lane.
+__device__ __forceinline__ void list_slots(const CompactArgs& a, uint32_t bits, int u, int64_t word,
+                                           int L, int U)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t lower = (1u << lane) - 1u;
+    for (int w = 0; w < 32; ++w) {
+        const uint32_t b = __shfl_sync(0xffffffffu, bits, w);
+        const int un = __shfl_sync(0xffffffffu, u, w) + __popc(b & lower);   // u at this slot
+        const int64_t s = (word + w) * 32 + lane;
+        const bool live = (b >> lane) & 1u;
+        if (live && s >= L) a.tail[un - U] = (int32_t)s;
+        if (!live && s < L) a.holes[s - un] = (int32_t)s;
+    }
 }
 
 __global__ void __launch_bounds__(kPlaceThreads)
@@ -566,22 +603,90 @@ place_kernel(const CompactArgs a)
     int u = before + incl - mine;
     for (int w = 0; w < warp; ++w) u += part[w];
     a.below[word] = u;
-    const int64_t s0 = word * 32;
-    const int64_t under_l = L - s0;   // slots of this word below L
-    uint32_t hole_bits = ~bits, tail_bits = bits;
-    if (under_l <= 0) hole_bits = 0;
-    else if (under_l < 32) hole_bits &= (1u << under_l) - 1u;
-    if (under_l >= 32) tail_bits = 0;
-    else if (under_l > 0) tail_bits &= ~((1u << under_l) - 1u);
-    // the first hole of this word is number s0 - u(s0)
-    for (int64_t k = s0 - u; hole_bits != 0; ++k) {
-        a.holes[k] = (int32_t)(s0 + __ffs(hole_bits) - 1);
-        hole_bits &= hole_bits - 1;
+    list_slots(a, bits, u, word - lane, L, U);
+}
+
+// Pools of at most kSmallRows rows whose tables have at most kSmallEntries
+// entries: bitmap, ranks and lists by one CTA, one launch instead of a clear and
+// three kernels.
+constexpr int kRankThreads = 1024;
+constexpr int kRankWords = 4;   // bitmap words per thread
+constexpr int64_t kSmallRows = 32 * kRankThreads * kRankWords;
+constexpr int64_t kSmallEntries = 1 << 17;
+
+__global__ void __launch_bounds__(kRankThreads)
+rank_kernel(const CompactArgs a)
+{
+    __shared__ uint32_t map[kRankThreads * kRankWords];
+    __shared__ int part[kRankThreads / 32];
+    __shared__ int under_s;
+    wait_for_predecessor();
+    allow_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int i = 0; i < kRankWords; ++i) map[tid + i * kRankThreads] = 0;
+    if (tid == 0) under_s = 0;
+    __syncthreads();
+    constexpr int kAhead = 8;
+    for (int64_t i0 = tid; i0 < a.num_indices; i0 += kAhead * kRankThreads) {
+        int32_t s[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            s[k] = i0 + k * kRankThreads < a.num_indices ? __ldg(a.kv_indices + i0 + k * kRankThreads) : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s[k] < 0) continue;
+            if (s[k] < a.pool_rows) atomicOr(map + (s[k] >> 5), 1u << (s[k] & 31));
+            else atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
+        }
     }
-    // the first tail row of this word is number u(max(s0, L)) - U
-    for (int64_t k = (under_l > 0 ? U : u) - U; tail_bits != 0; ++k) {
-        a.tail[k] = (int32_t)(s0 + __ffs(tail_bits) - 1);
-        tail_bits &= tail_bits - 1;
+    __syncthreads();
+    // ranks: a warp takes 32 kRankWords neighbouring words, 32 at a time
+    uint32_t bits[kRankWords];
+    int u[kRankWords], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRankWords; ++i) {
+        bits[i] = map[(warp * kRankWords + i) * 32 + lane];
+        int incl = __popc(bits[i]);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        u[i] = sum + incl - __popc(bits[i]);
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    int before = 0, L = 0;
+    for (int w = 0; w < kRankThreads / 32; ++w) {
+        const int n = part[w];
+        before += w < warp ? n : 0;
+        L += n;
+    }
+    int under = 0;   // live slots below L
+#pragma unroll
+    for (int i = 0; i < kRankWords; ++i) {
+        const int n = L - ((warp * kRankWords + i) * 32 + lane) * 32;
+        under += n <= 0 ? 0 : __popc(n >= 32 ? bits[i] : bits[i] & ((1u << n) - 1u));
+    }
+    under = __reduce_add_sync(0xffffffffu, under);
+    if (lane == 0) atomicAdd(&under_s, under);
+    __syncthreads();
+    const int U = under_s;
+    if (tid == 0) {
+        a.totals[0] = L;
+        a.totals[1] = U;
+        a.live[0] = L;
+    }
+    const int words = a.chunks * kPlaceThreads;
+#pragma unroll
+    for (int i = 0; i < kRankWords; ++i) {
+        const int first = (warp * kRankWords + i) * 32;
+        if (first >= words) break;   // whole warps: words come in multiples of 256
+        a.bits[first + lane] = bits[i];
+        a.below[first + lane] = before + u[i];
+        list_slots(a, bits[i], before + u[i], first, L, U);
     }
 }
 
@@ -596,13 +701,17 @@ move_kernel(const CompactArgs a)
     const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
     const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
     const int64_t moves = L - U;
-    for (int64_t k0 = thread / 32 * kCopyRows; k0 < moves; k0 += threads / 32 * kCopyRows) {
+    // 32 moves a turn of the warp: their slots one per lane, then four row copies
+    for (int64_t k0 = thread & ~31ll; k0 < moves; k0 += threads) {
         int32_t src = -1, dst = -1;
-        if (lane < kCopyRows && k0 + lane < moves) {
+        if (k0 + lane < moves) {
             src = __ldcg(a.tail + k0 + lane);
             dst = __ldcg(a.holes + k0 + lane);
         }
-        copy_rows<WIDTH>(a.pool, src, dst, lane);
+#pragma unroll 1
+        for (int b = 0; b < 32 / kCopyRows; ++b)
+            if (k0 + b * kCopyRows < moves)
+                copy_rows<WIDTH>(a.pool, src, dst, lane, b * kCopyRows);
     }
     for (int64_t i = thread; i < a.num_indices; i += threads) {
         const int32_t s = __ldcg(a.kv_indices + i);
@@ -729,11 +838,15 @@ int mla_cache_fork(void* pool, int64_t pool_rows, int32_t row_bytes, const int32
     const ForkArgs a{static_cast<uint8_t*>(pool), pool_rows, kv_indices, num_indices, kv_indptr,
                      num_parents, parents, keep, child_indptr, num_children, fresh, num_fresh,
                      fresh_indptr, table, total, static_cast<uint32_t*>(workspace)};
-    const int64_t per = kCopyThreads / 32 * kCopyRows;
+    // Four turns a warp amortise the look-up of its entries once every SM has
+    // work without that.
+    const bool many = total > kForkManyEntries;
+    const int64_t per = kCopyThreads / 32 * kCopyRows * (many ? 4 : 1);
     const dim3 grid((unsigned)((total + per - 1) / per));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(launch_dependent(row_bytes == 576 ? fork_kernel<576> : fork_kernel<512>, grid,
-                                      kCopyThreads, s, true, a));
+    auto* kernel = row_bytes == 576 ? (many ? fork_kernel<576, 4> : fork_kernel<576, 1>)
+                                    : (many ? fork_kernel<512, 4> : fork_kernel<512, 1>);
+    return status_of(launch_dependent(kernel, grid, kCopyThreads, s, true, a));
 }
 
 int64_t mla_cache_compact_workspace_bytes(int64_t pool_rows)
@@ -784,20 +897,25 @@ int mla_cache_compact(void* pool, int64_t pool_rows, int32_t row_bytes,
     a.tail = reinterpret_cast<int32_t*>(p + align256((pool_rows / 2 + 1) * 4));
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(a.bits, 0, (size_t)a.chunks * kPlaceThreads * 4, s);
-    if (e == cudaSuccess && num_indices > 0)
-        e = launch_dependent(mark_kernel,
-                             dim3((unsigned)((num_indices + kCopyThreads - 1) / kCopyThreads)),
-                             kCopyThreads, s, false, a);
-    if (e == cudaSuccess)
-        e = launch_dependent(count_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s,
-                             num_indices > 0, a);
-    if (e == cudaSuccess)
-        e = launch_dependent(place_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s, true, a);
+    cudaError_t e;
+    if (pool_rows <= kSmallRows && num_indices <= kSmallEntries) {
+        e = launch_dependent(rank_kernel, dim3(1), kRankThreads, s, true, a);
+    } else {
+        e = cudaMemsetAsync(a.bits, 0, (size_t)a.chunks * kPlaceThreads * 4, s);
+        if (e == cudaSuccess && num_indices > 0)
+            e = launch_dependent(mark_kernel,
+                                 dim3((unsigned)((num_indices + kCopyThreads - 1) / kCopyThreads)),
+                                 kCopyThreads, s, false, a);
+        if (e == cudaSuccess)
+            e = launch_dependent(count_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s,
+                                 num_indices > 0, a);
+        if (e == cudaSuccess)
+            e = launch_dependent(place_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s, true, a);
+    }
     if (e == cudaSuccess) {
         // enough CTAs for the worst case, at most eight a SM of a full GPU (a
         // CTA loops over the rest)
-        const int64_t most = pool_rows / 2 / (kCopyThreads / 32 * kCopyRows) + 1;
+        const int64_t most = pool_rows / 2 / kCopyThreads + 1;
         const int64_t remap = (num_indices + kCopyThreads - 1) / kCopyThreads;
         const int64_t want = most > remap ? most : remap;
         const dim3 grid((unsigned)(want < 8 * 152 ? want : 8 * 152));

@@ -370,7 +370,7 @@ struct PrefixShared {
     alignas(16) float cq[kRows];
     alignas(16) int win[kRows];
     alignas(16) float scale[kRows];   // epilogue: 1 / the sum of what the MMA consumed
-    float red[kSoftmaxWarps][32];
+    alignas(16) float red[kSoftmaxWarps][32];
     // the tile's requests: own blocks before each, where its images start
     uint64_t own_full;
     int own_before[kRows + 1];
@@ -395,35 +395,60 @@ __device__ __forceinline__ float2 split_p(float a, float b, uint16_t& hi, uint16
     return __half22float2(*reinterpret_cast<const __half2*>(&sum));
 }
 
-// A run: blocks [x0, x1) of a tile's list, the prefix's `shared` blocks and then its
-// requests' own.  `j0` blocks went before in this CTA (the pipeline's phases go
-// on counting), `run` runs.
+// A run: blocks [x0, x1) of a tile's nb, of which `shared` are the prefix's and the
+// others its requests' own.  The own blocks are spread evenly among the
+// prefix's, so that no run is made of own blocks alone: there every request's
+// first block would start its rows' softmax anew (measured, with the own blocks
+// behind the prefix's the CTAs that had them took 34 us, the others 24).  `j0`
+// blocks went before in this CTA (the pipeline's phases go on counting), `run`
+// runs.
 struct Run {
     int64_t tile;
-    int x0, x1;
+    int x0, x1, nb;
     int shared;
     int64_t slot;   // where its partial rows go
     int64_t j0;
     int run;
 };
 
-// The image of block x of the tile's list; for an own block k becomes its
-// request's number in the tile (x only grows from call to call).
-__device__ __forceinline__ int64_t image_of(const PrefixArgs& a, const PrefixShared& ms,
-                                            const Run& r, int x, int& k)
-{
-    if (x < r.shared) return x;
-    const int y = x - r.shared;
-    while (y >= ms.own_before[k + 1]) ++k;
-    return (int64_t)ms.own_image[k] + (y - ms.own_before[k]);
-}
+// Walks a run's blocks in order: block x is own if floor((x + 1) no / nb) is past
+// floor(x no / nb) = y, no the tile's own blocks, and then own block y; else block
+// x - y of the prefix.
+struct Walk {
+    int x, y, k;      // k: number in the tile of own block y's request (once looked up)
+    int64_t acc;      // x no mod nb
+    __device__ __forceinline__ explicit Walk(const Run& r) : x(r.x0), k(0)
+    {
+        const int64_t t = (int64_t)r.x0 * (r.nb - r.shared);
+        y = (int)(t / r.nb);
+        acc = t % r.nb;
+    }
+    __device__ __forceinline__ bool own(const Run& r) const
+    {
+        return acc + (r.nb - r.shared) >= r.nb;
+    }
+    __device__ __forceinline__ void next(const Run& r)
+    {
+        const bool o = own(r);
+        acc += (r.nb - r.shared) - (o ? r.nb : 0);
+        y += o ? 1 : 0;
+        ++x;
+    }
+    // The image of the block (an own one's request looked up by warp 2).
+    __device__ __forceinline__ int64_t image(const Run& r, const PrefixShared& ms)
+    {
+        if (!own(r)) return x - y;
+        while (y >= ms.own_before[k + 1]) ++k;
+        return (int64_t)ms.own_image[k] + (y - ms.own_before[k]);
+    }
+};
 
 // Warp 2: the run's tile's requests into shared memory.
 __device__ __forceinline__ void tile_role(const PrefixArgs& a, PrefixShared& ms, const Run& r,
                                           int lane)
 {
     int b0 = 0, b1 = -1, before = 0;
-    if (r.x1 > r.shared) tile_requests(a, r.tile, b0, b1);
+    if (r.nb > r.shared) tile_requests(a, r.tile, b0, b1);
     for (int k0 = 0; b0 + k0 <= b1; k0 += 32) {   // at most 64: a request has a row or more
         const int b = b0 + k0 + lane;
         int n = 0;
@@ -451,8 +476,8 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
 {
     volatile int* abort_flag = &ms.abort;
     const int n = r.x1 - r.x0;
-    int k = 0;
-    bool own = false;   // the tile's requests have been looked up
+    Walk walk(r);
+    bool looked = false;   // the tile's requests are known
     int64_t issued = 0, ropes = 0;   // latent chunks and RoPE chunks of this run
     if (lane == 0) {
         mbar_arrive_expect_tx(&ms.q_full, (uint32_t)kPrefixImage);
@@ -463,11 +488,12 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
     for (int j = 0; j < n && ok; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
-        if (!own && r.x0 + j >= r.shared) {
-            ok = own = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+        if (!looked && walk.own(r)) {
+            ok = looked = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
             if (!ok) break;
         }
-        const uint8_t* src = a.k_image + image_of(a, ms, r, r.x0 + j, k) * kPrefixImage;
+        const uint8_t* src = a.k_image + walk.image(r, ms) * kPrefixImage;
+        walk.next(r);
         for (int c = 0; c < 4 && ok; ++c) {
             if (jj >= 2)
                 ok = warp_wait(&ms.k_empty[st][c], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
@@ -639,22 +665,31 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     // the requests of the tile, for the blocks of their own keys
     const int P = prefix_length(a);
     const int per = a.q_len * a.num_heads;
-    int k_next = 0, b0 = 0, b1;
-    bool own = false;
-    if (r.x1 > r.shared) tile_requests(a, r.tile, b0, b1);
-    auto valid_of = [&](int xb) -> uint32_t {   // of block xb, whose request k_next becomes
-        if (!own && xb >= r.shared)
-            own = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
-        if (xb >= r.shared && !own) return 0;
-        return __ldcg(a.k_valid + image_of(a, ms, r, xb, k_next) * 4 + quad);
+    int b0 = 0, b1;
+    if (r.nb > r.shared) tile_requests(a, r.tile, b0, b1);
+    // one block ahead: its valid keys, and where its first key is and whose
+    Walk walk(r);
+    bool looked = false;
+    uint32_t valid_next;
+    int pos_next, k_next;   // k_next < 0: a prefix block
+    auto look_ahead = [&]() {
+        const bool own = walk.own(r);
+        if (own && !looked)
+            looked = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+        valid_next = 0;
+        if (!own || looked) valid_next = __ldcg(a.k_valid + walk.image(r, ms) * 4 + quad);
+        k_next = own ? walk.k : -1;
+        pos_next = own ? P + (walk.y - (looked ? ms.own_before[walk.k] : 0)) * kKeys
+                       : (walk.x - walk.y) * kKeys;
+        walk.next(r);
     };
-    uint32_t vnext = valid_of(r.x0);
+    look_ahead();
     for (int j = 0; j < n; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
-        const int xb = r.x0 + j, k_now = k_next;
-        const uint32_t valid = vnext;
-        if (j + 1 < n) vnext = valid_of(xb + 1);
+        const uint32_t valid = valid_next;
+        const int pos0 = pos_next, k_now = k_next;
+        if (j + 1 < n) look_ahead();
         const bool ok = warp_wait(&ms.s_full[st], (uint32_t)(jj >> 1) & 1, abort_flag, 0,
                                   a.wait_limit);
         float x[R];
@@ -693,12 +728,11 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
         }
         // masked: keys past their list or with a bad slot, positions that a row does
         // not see, and own keys of another request than the row's
-        if (xb >= r.shared || valid != 0xffffffffu || (xb + 1) * kKeys > win_min) {
+        if (k_now >= 0 || valid != 0xffffffffu || pos0 + kKeys > win_min) {
             const bool kval = (valid >> lane) & 1u;
-            int pos = xb * kKeys + ti;
+            const int pos = pos0 + ti;
             uint32_t rows = 0xffffffffu;
-            if (xb >= r.shared) {
-                pos = P + (xb - r.shared - (own ? ms.own_before[k_now] : 0)) * kKeys + ti;
+            if (k_now >= 0) {
                 // rows of request b0 + k_now, as bits of this set's 32
                 const int64_t first = (int64_t)(b0 + k_now) * per - r.tile * kRows - r0;
                 const int lo = (int)max(first, (int64_t)0), hi = (int)min(first + per, (int64_t)R);
@@ -736,21 +770,27 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
             uint32_t moved = 0;   // rows whose sums so far shrink
             float shrink[R];
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const float bm = fmaxf(fmaxf(red[k], red[32 + k]), fmaxf(red[64 + k], red[96 + k]));
-                const bool first = (unset >> k) & 1u;
-                shrink[k] = 1.f;
-                if (first ? bm > -CUDART_INF_F : bm > kTop) {
-                    const float delta = (kShift - kHeadroom) - bm;
+            for (int g = 0; g < R / 4; ++g) {
+                float4 m4[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) m4[w] = reinterpret_cast<const float4*>(red + 32 * w)[g];
+                const float top4[4] = {fmaxf(fmaxf(m4[0].x, m4[1].x), fmaxf(m4[2].x, m4[3].x)),
+                                       fmaxf(fmaxf(m4[0].y, m4[1].y), fmaxf(m4[2].y, m4[3].y)),
+                                       fmaxf(fmaxf(m4[0].z, m4[1].z), fmaxf(m4[2].z, m4[3].z)),
+                                       fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w))};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int k = 4 * g + u;
+                    const bool first = (unset >> k) & 1u;
+                    const bool move = top4[u] > (first ? -CUDART_INF_F : kTop);
+                    const float delta = move ? (kShift - kHeadroom) - top4[u] : 0.f;
                     nm[k] += delta;
                     x[k] += delta;
-                    unset &= ~(1u << k);
-                    if (!first) {
-                        shrink[k] = exp2f(delta);
-                        moved |= 1u << k;
-                        l[k] *= shrink[k];
-                        lt[k] *= shrink[k];
-                    }
+                    if (move) unset &= ~(1u << k);
+                    shrink[k] = move && !first ? ex2_approx(delta) : 1.f;
+                    if (move && !first) moved |= 1u << k;
+                    l[k] *= shrink[k];
+                    lt[k] *= shrink[k];
                 }
             }
             if (moved != 0 &&
@@ -917,14 +957,14 @@ prefix_split_kernel(const PrefixArgs a)
 
     // this CTA's share: `left` blocks from block x of `tile` on
     const int64_t g = blockIdx.x;
-    int64_t tile = 0, left = 0;
+    int64_t tile = 0, left = 0, tile_nb = -1;   // blocks of `tile`, -1: not read yet
     int x = 0;
     if (a.splits > 0) {
-        tile = g / a.splits;
-        const int s = (int)(g % a.splits);
-        const int64_t nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
-        x = (int)(nb * s / a.splits);
-        left = nb * (s + 1) / a.splits - x;
+        tile = (int)blockIdx.x / a.splits;
+        const int s = (int)blockIdx.x % a.splits;
+        tile_nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
+        x = (int)(tile_nb * s / a.splits);
+        left = tile_nb * (s + 1) / a.splits - x;
     } else {
         const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)gridDim.x, U);
         if (g < G) {
@@ -949,9 +989,12 @@ prefix_split_kernel(const PrefixArgs a)
     Run r;
     auto next_run = [&]() -> bool {
         while (left > 0) {
-            const int64_t nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
+            const int64_t nb = tile_nb >= 0 ? tile_nb
+                                            : __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
+            tile_nb = -1;
             if (nb > x) {
                 r.tile = tile;
+                r.nb = (int)nb;
                 r.x0 = x;
                 r.x1 = (int)min(nb, x + left);
                 r.shared = shared;
@@ -1005,25 +1048,36 @@ prefix_split_kernel(const PrefixArgs a)
 
 // ---- prefix_merge -----------------------------------------------------------------------------
 //
-// One CTA per output row, four columns per thread.  The row's partials are those
-// of the runs of its tile and, without joined tiles, the split kernel's:
-// M = max lse, w = 2^(lse - M), o = sum w o_s / sum w, summed in increasing
-// order, lse = M + log2 sum w.  A partial of weight 0 is not added.
+// W warps per output row (4 up to 512 rows, else 1), 16 / W columns per lane; a
+// CTA's rows are in one tile.  (Measured, 4 against 1: 64 rows of 12 partials 4.0
+// against 4.7 us, 512 of 19 6.9 against 7.9, 1024 of 9 6.8 against 4.7.)
+// The row's partials are those of the runs of its tile and, without joined
+// tiles, the split kernel's: M = max lse, w = 2^(lse - M), o = sum w o_s / sum w,
+// summed in increasing order, lse = M + log2 sum w.  A partial of weight 0 is
+// not added.  The first partials are loaded before the weights are known.
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 32 * kMergeWarps;
 constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;   // partials of one tile or one request: 256 each
-constexpr int kMergeAhead = 4;   // partials loaded before the weights are known
+constexpr int64_t kMergeFewRows = 512;
+static_assert(kRows % kMergeWarps == 0, "a CTA's rows are in one tile");
 
+template <int W>
 __global__ void __launch_bounds__(kMergeThreads)
 prefix_merge_kernel(const PrefixArgs a)
 {
-    __shared__ float w_s[kMergeMax];
-    __shared__ float sum_s;
+    constexpr int kQuads = 4 / W;        // groups of four columns per lane
+    constexpr int kAhead = 2 * W;        // partials in flight per lane
+    constexpr int kMergeRows = kMergeWarps / W;
+    __shared__ float weights[kMergeWarps][kMergeMax];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t item = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t tile = item / kRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * kMergeRows + warp / W;
+    const int col = warp % W * (128 * kQuads) + lane * 4;   // and every 128 columns on
+    const int64_t tile = (int64_t)blockIdx.x * kMergeRows / kRows;
+    if (item >= a.rows) return;   // whole warps, and no barrier follows
+    float* w_s = weights[warp];
     // the tile's runs: slots [s0, s0 + np); a run without blocks has left nothing
     int64_t s0 = 0;
     int np = 0, nb = 0;
@@ -1044,61 +1098,77 @@ prefix_merge_kernel(const PrefixArgs a)
         return a.splits > nb && (int64_t)nb * i / a.splits == (int64_t)nb * (i + 1) / a.splits;
     };
     const int n = np + a.own_splits;
-    const float* own = a.o_own + item * a.own_splits * kDv;
-    const float* part = a.o_part + (s0 * kRows + item % kRows) * kDv;
+    const float* own = a.o_own + item * a.own_splits * kDv + col;
+    const float* part = a.o_part + (s0 * kRows + item % kRows) * kDv + col;
     const float* lse_part = a.lse_part + s0 * kRows + item % kRows;
-    const int c = tid * 4;
-    auto row_of = [&](int i) {
-        return i < np ? part + (int64_t)i * (kRows * kDv) : own + (int64_t)(i - np) * kDv;
+    struct Cols {
+        float4 v[kQuads];   // columns col + 128 q .. + 3
     };
-    float4 v[kMergeAhead];
+    auto load = [&](int i) {
+        const float* row = i < np ? part + (int64_t)i * (kRows * kDv) : own + (int64_t)(i - np) * kDv;
+        Cols c;
 #pragma unroll
-    for (int i = 0; i < kMergeAhead; ++i)
-        if (i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(i) + c));
-    if (tid < 32) {
-        float m = -CUDART_INF_F;
-        for (int i = lane; i < n; i += 32) {
-            float l = -CUDART_INF_F;
-            if (i >= np) l = __ldcg(a.lse_own + item * a.own_splits + (i - np));
-            else if (!left_out(i)) l = __ldcg(lse_part + i * kRows);
-            w_s[i] = l;
-            m = fmaxf(m, l);
-        }
+        for (int q = 0; q < kQuads; ++q) c.v[q] = __ldcg(reinterpret_cast<const float4*>(row + 128 * q));
+        return c;
+    };
+    Cols ahead[kAhead];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        float sum = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const float w = w_s[i] == -CUDART_INF_F ? 0.f : exp2f(w_s[i] - m);
-            sum += w;
-            w_s[i] = w * (i < np ? a.kv_scale : a.own_scale);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) {
-            sum_s = sum;
-            if (a.lse != nullptr) a.lse[item] = sum != 0.f ? m + log2f(sum) : -CUDART_INF_F;
-        }
+    for (int i = 0; i < kAhead; ++i)
+        if (i < n) ahead[i] = load(i);
+    float m = -CUDART_INF_F;
+    for (int i = lane; i < n; i += 32) {
+        float l = -CUDART_INF_F;
+        if (i >= np) l = __ldcg(a.lse_own + item * a.own_splits + (i - np));
+        else if (!left_out(i)) l = __ldcg(lse_part + i * kRows);
+        w_s[i] = l;
+        m = fmaxf(m, l);
     }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float w, float4 x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float w = w_s[i] == -CUDART_INF_F ? 0.f : exp2f(w_s[i] - m);
+        sum += w;
+        w_s[i] = w * (i < np ? a.kv_scale : a.own_scale);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0 && warp % W == 0 && a.lse != nullptr)
+        a.lse[item] = sum != 0.f ? m + log2f(sum) : -CUDART_INF_F;
+    __syncwarp();
+    Cols acc;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) acc.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, const Cols& c) {
         if (w != 0.f) {
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) {
+                acc.v[q].x += w * c.v[q].x;
+                acc.v[q].y += w * c.v[q].y;
+                acc.v[q].z += w * c.v[q].z;
+                acc.v[q].w += w * c.v[q].w;
+            }
         }
     };
 #pragma unroll
-    for (int i = 0; i < kMergeAhead; ++i)
-        if (i < n) add(w_s[i], v[i]);
-    for (int i = kMergeAhead; i < n; ++i)
-        add(w_s[i], __ldcg(reinterpret_cast<const float4*>(row_of(i) + c)));
-    const float f = sum_s != 0.f ? 1.f / sum_s : 0.f;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    *reinterpret_cast<uint2*>(a.o + item * kDv + c) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    for (int i = 0; i < kAhead; ++i)
+        if (i < n) add(w_s[i], ahead[i]);
+    for (int i0 = kAhead; i0 < n; i0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < n) ahead[i] = load(i0 + i);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < n) add(w_s[i0 + i], ahead[i]);
+    }
+    const float f = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.v[q].x * f, acc.v[q].y * f);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.v[q].z * f, acc.v[q].w * f);
+        *reinterpret_cast<uint2*>(a.o + item * kDv + col + 128 * q) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
 }
 
 }  // namespace
@@ -1123,7 +1193,10 @@ cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream)
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream)
 {
-    return launch_pdl(prefix_merge_kernel, dim3((unsigned)a.rows), kMergeThreads, 0, stream, a);
+    const bool few = a.rows <= kMergeFewRows;
+    const int64_t rows = kMergeWarps / (few ? 4 : 1);
+    return launch_pdl(few ? prefix_merge_kernel<4> : prefix_merge_kernel<1>,
+                      dim3((unsigned)((a.rows + rows - 1) / rows)), kMergeThreads, 0, stream, a);
 }
 
 }  // namespace mla

@@ -341,6 +341,25 @@ def test_fork(lens, parents, keep, n, width):
     assert torch.equal(pool.cpu(), want_pool)
 
 
+def test_fork_of_many_entries():
+    # above 131072 entries a warp takes 32 of them, below 8
+    lens, F = [3001, 2999, 1], 60
+    parents = [f % 3 for f in range(F)]
+    n = [lens[p] for p in parents]
+    keep = [(f * 977) % 3100 for f in range(F)]
+    c = make_fork(lens, parents, keep, n, 130000, 512, seed=1)
+    small = make_fork(lens, parents[:40], keep[:40], n[:40], 130000, 576, seed=2)
+    assert sum(n[:40]) < 1 << 17 and sum(n) < 1 << 17
+    big = make_fork([30011], [0] * 5, [30000, 1, 15000, 29999, 12345], [30011] * 5, 130000, 576, 3)
+    assert int(big["child_indptr"][-1]) > 1 << 17
+    for case in (c, small, big):
+        table, pool, err = run_fork(case)
+        want_table, want_pool = reference_fork(case)
+        assert err == 0
+        assert torch.equal(table.cpu(), want_table)
+        assert torch.equal(pool.cpu(), want_pool)
+
+
 def test_fork_reports_and_skips_what_is_out_of_range():
     c = make_fork([50, 60], [0, 1, 0], [10, 60, 50], [50, 60, 50], 300, 576, seed=3)
     _, want_pool = reference_fork(c)
@@ -442,6 +461,16 @@ def test_compact_where_the_live_rows_lie(place):
            "middle": torch.arange(8000, 17000),
            "borders": torch.tensor([0, 31, 32, 8191, 8192, 16383, 16384, n - 1])}[place]
     assert check_compact(pool, idx.int().flip(0)) == 0
+
+
+@pytest.mark.parametrize("rows,entries", [(131072, 131072), (131073, 60000), (131072, 131073),
+                                          (500, 200000), (300000, 120000)])
+def test_compact_both_sides_of_the_small_pool_rule(rows, entries):
+    # up to 131072 rows and entries one CTA ranks the pool, above that three kernels
+    g = torch.Generator().manual_seed(rows)
+    pool = torch.randint(0, 256, (rows, 512), generator=g).to(torch.uint8)
+    slots = torch.randint(0, rows, (entries,), generator=g).int()
+    assert check_compact(pool, slots) == 0
 
 
 def test_compact_one_entry_many_times_and_out_of_range():

@@ -463,10 +463,10 @@ def test_compact_where_the_live_rows_lie(place):
     assert check_compact(pool, idx.int().flip(0)) == 0
 
 
-@pytest.mark.parametrize("rows,entries", [(131072, 131072), (131073, 60000), (131072, 131073),
-                                          (500, 200000), (300000, 120000)])
+@pytest.mark.parametrize("rows,entries", [(16384, 32768), (16385, 9000), (16384, 32769),
+                                          (500, 40000), (300000, 120000)])
 def test_compact_both_sides_of_the_small_pool_rule(rows, entries):
-    # up to 131072 rows and entries one CTA ranks the pool, above that three kernels
+    # up to 16384 rows and 32768 entries one CTA ranks the pool, above three kernels
     g = torch.Generator().manual_seed(rows)
     pool = torch.randint(0, 256, (rows, 512), generator=g).to(torch.uint8)
     slots = torch.randint(0, rows, (entries,), generator=g).int()

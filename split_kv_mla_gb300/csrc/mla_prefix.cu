@@ -369,7 +369,10 @@ struct PrefixShared {
     int abort;
     alignas(16) float cq[kRows];
     alignas(16) int win[kRows];
-    alignas(16) float scale[kRows];   // epilogue: 1 / the sum of what the MMA consumed
+    alignas(16) float delta[kRows];   // a reference's step
+    alignas(16) float scale[kRows];   // 2^step; epilogue: 1 / the sum of what the MMA consumed
+    uint32_t set_now[kSets], shrunk[kSets];   // rows that got a reference, that moved theirs
+    int stop[kSets];
     alignas(16) float red[kSoftmaxWarps][32];
     // the tile's requests: own blocks before each, where its images start
     uint64_t own_full;
@@ -650,14 +653,15 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     }
     softmax_bar(bar_id);
     int win_min = ms.win[r0 + lane];
+    // rows without a reference yet, as bits (the same in every thread of the set);
+    // a row that sees nothing never gets one
+    uint32_t unset = __ballot_sync(0xffffffffu, win_min > 0);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         win_min = min(win_min, __shfl_xor_sync(0xffffffffu, win_min, off));
 
-    // x = logit - m + kShift, nm = kShift - m; a row without a reference yet
-    // (bit of `unset`, the same in every thread of the set) has nm = 0
+    // x = logit - m + kShift, nm = kShift - m (0 while the row has no reference)
     float nm[R], l[R], lt[R];
-    uint32_t unset = 0xffffffffu;
 #pragma unroll
     for (int k = 0; k < R; ++k) nm[k] = l[k] = lt[k] = 0.f;
     bool alive = true;
@@ -665,8 +669,12 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     // the requests of the tile, for the blocks of their own keys
     const int P = prefix_length(a);
     const int per = a.q_len * a.num_heads;
-    int b0 = 0, b1;
-    if (r.nb > r.shared) tile_requests(a, r.tile, b0, b1);
+    int row0 = 0;   // row of the tile's first request's first row, among the set's
+    if (r.nb > r.shared) {
+        int b0, b1;
+        tile_requests(a, r.tile, b0, b1);
+        row0 = (int)((int64_t)b0 * per - r.tile * kRows) - r0;
+    }
     // one block ahead: its valid keys, and where its first key is and whose
     Walk walk(r);
     bool looked = false;
@@ -727,70 +735,91 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
             x[4 * g + 3] = fmaf(x[4 * g + 3], c.w, nm[4 * g + 3]);
         }
         // masked: keys past their list or with a bad slot, positions that a row does
-        // not see, and own keys of another request than the row's
+        // not see, and own keys of another request than the row's.  `vis` has a bit
+        // per row that sees this thread's key.  (The rolled loop keeps the code of
+        // this rare path short: unrolled, it cost 2,500 cycles, most of them
+        // fetching it.)
+        uint32_t vis = 0xffffffffu;
         if (k_now >= 0 || valid != 0xffffffffu || pos0 + kKeys > win_min) {
-            const bool kval = (valid >> lane) & 1u;
             const int pos = pos0 + ti;
-            uint32_t rows = 0xffffffffu;
-            if (k_now >= 0) {
-                // rows of request b0 + k_now, as bits of this set's 32
-                const int64_t first = (int64_t)(b0 + k_now) * per - r.tile * kRows - r0;
-                const int lo = (int)max(first, (int64_t)0), hi = (int)min(first + per, (int64_t)R);
-                rows = hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
+            vis = 0;
+            if ((valid >> lane) & 1u) {
+#pragma unroll 1
+                for (int g = 0; g < R / 4; ++g) {
+                    const int4 w = reinterpret_cast<const int4*>(ms.win + r0)[g];
+                    vis |= ((pos < w.x ? 1u : 0u) | (pos < w.y ? 2u : 0u) |
+                            (pos < w.z ? 4u : 0u) | (pos < w.w ? 8u : 0u)) << (4 * g);
+                }
+            }
+            if (k_now >= 0) {   // only the rows of the key's request
+                const int first = row0 + k_now * per;
+                const int lo = max(first, 0), hi = min(first + per, R);
+                vis &= hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
             }
 #pragma unroll
-            for (int g = 0; g < R / 4; ++g) {
-                const int4 w = reinterpret_cast<const int4*>(ms.win + r0)[g];
-                const int wv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    x[4 * g + u] = kval && ((rows >> (4 * g + u)) & 1u) && pos < wv[u]
-                                       ? x[4 * g + u] : -CUDART_INF_F;
-            }
+            for (int k = 0; k < R; ++k) x[k] = (vis >> k) & 1u ? x[k] : -CUDART_INF_F;
         }
         float top = x[0];
 #pragma unroll
         for (int k = 1; k < R; ++k) top = fmaxf(top, x[k]);
-        bool need = top > kTop || !ok;
-        if (unset != 0) {
-#pragma unroll
-            for (int k = 0; k < R; ++k) need |= ((unset >> k) & 1u) && x[k] > -CUDART_INF_F;
-        }
+        const bool need = top > kTop || (unset & vis) != 0 || !ok;
         if (softmax_bar_or(bar_id, need)) {
-            // (bar.red above also tells of a warp that gave up)
-            if (softmax_bar_or(bar_id, !ok || *abort_flag)) {
+            // block maxima per row, then one lane per row of the set's first warp
+            // decides on the row's new reference
+            {
+                float v[R];
+#pragma unroll
+                for (int k = 0; k < R; ++k) v[k] = x[k];
+                red[quad * 32 + lane] = warp_transpose_reduce<R, true>(v, lane);
+            }
+            softmax_bar(bar_id);
+            if (quad == 0) {
+                const float bm = fmaxf(fmaxf(red[lane], red[32 + lane]),
+                                       fmaxf(red[64 + lane], red[96 + lane]));
+                const bool first = (unset >> lane) & 1u;
+                const bool move = bm > (first ? -CUDART_INF_F : kTop);
+                const float delta = move ? (kShift - kHeadroom) - bm : 0.f;
+                ms.delta[r0 + lane] = delta;
+                ms.scale[r0 + lane] = move && !first ? ex2_approx(delta) : 1.f;
+                const uint32_t set_now = __ballot_sync(0xffffffffu, move && first);
+                const uint32_t shrunk = __ballot_sync(0xffffffffu, move && !first);
+                if (lane == 0) {
+                    ms.set_now[set] = set_now;
+                    ms.shrunk[set] = shrunk;
+                    ms.stop[set] = *abort_flag;   // a warp that gave up: all of the set stop
+                }
+            }
+            softmax_bar(bar_id);
+            if (ms.stop[set] != 0) {
                 alive = false;
                 break;
             }
-            float v[R];
-#pragma unroll
-            for (int k = 0; k < R; ++k) v[k] = x[k];
-            red[quad * 32 + lane] = warp_transpose_reduce<R, true>(v, lane);
-            softmax_bar(bar_id);
-            uint32_t moved = 0;   // rows whose sums so far shrink
-            float shrink[R];
+            unset &= ~ms.set_now[set];
+            uint32_t moved = ms.shrunk[set];
 #pragma unroll
             for (int g = 0; g < R / 4; ++g) {
-                float4 m4[4];
+                const float4 d = reinterpret_cast<const float4*>(ms.delta + r0)[g];
+                nm[4 * g] += d.x;
+                nm[4 * g + 1] += d.y;
+                nm[4 * g + 2] += d.z;
+                nm[4 * g + 3] += d.w;
+                x[4 * g] += d.x;
+                x[4 * g + 1] += d.y;
+                x[4 * g + 2] += d.z;
+                x[4 * g + 3] += d.w;
+            }
+            if (moved != 0) {   // sums and O so far shrink with the reference's step
 #pragma unroll
-                for (int w = 0; w < 4; ++w) m4[w] = reinterpret_cast<const float4*>(red + 32 * w)[g];
-                const float top4[4] = {fmaxf(fmaxf(m4[0].x, m4[1].x), fmaxf(m4[2].x, m4[3].x)),
-                                       fmaxf(fmaxf(m4[0].y, m4[1].y), fmaxf(m4[2].y, m4[3].y)),
-                                       fmaxf(fmaxf(m4[0].z, m4[1].z), fmaxf(m4[2].z, m4[3].z)),
-                                       fmaxf(fmaxf(m4[0].w, m4[1].w), fmaxf(m4[2].w, m4[3].w))};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int k = 4 * g + u;
-                    const bool first = (unset >> k) & 1u;
-                    const bool move = top4[u] > (first ? -CUDART_INF_F : kTop);
-                    const float delta = move ? (kShift - kHeadroom) - top4[u] : 0.f;
-                    nm[k] += delta;
-                    x[k] += delta;
-                    if (move) unset &= ~(1u << k);
-                    shrink[k] = move && !first ? ex2_approx(delta) : 1.f;
-                    if (move && !first) moved |= 1u << k;
-                    l[k] *= shrink[k];
-                    lt[k] *= shrink[k];
+                for (int g = 0; g < R / 4; ++g) {
+                    const float4 f = reinterpret_cast<const float4*>(ms.scale + r0)[g];
+                    l[4 * g] *= f.x;
+                    l[4 * g + 1] *= f.y;
+                    l[4 * g + 2] *= f.z;
+                    l[4 * g + 3] *= f.w;
+                    lt[4 * g] *= f.x;
+                    lt[4 * g + 1] *= f.y;
+                    lt[4 * g + 2] *= f.z;
+                    lt[4 * g + 3] *= f.w;
                 }
             }
             if (moved != 0 &&
@@ -801,10 +830,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
                 while (moved != 0) {
                     const int row = __ffs(moved) - 1;
                     moved &= moved - 1;
-                    float f = 1.f;
-#pragma unroll
-                    for (int k = 0; k < R; ++k)
-                        if (k == row) f = shrink[k];
+                    const float f = ms.scale[r0 + row];
                     uint32_t o[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[c] = tmem_ld1(lanes + kColO + c * kRows + r0 + row);
@@ -817,7 +843,6 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
                 }
                 tmem_wait_st();
             }
-            softmax_bar(bar_id);   // `red` is free again
         }
         // P^T is stored as 16-row columns of 128 keys x 16 bytes, e4m3 terms
         // then e5m2 terms

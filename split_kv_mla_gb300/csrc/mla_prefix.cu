@@ -123,6 +123,11 @@ __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t U, int64_t G)
 {
     return ((u + 1) * G - 1) / U;
 }
+// The first block of part s of `splits` equal parts of nb < 2^24 blocks.
+__device__ __forceinline__ uint32_t part_begin(uint32_t nb, int s, int splits)
+{
+    return nb * (uint32_t)s / (uint32_t)splits;
+}
 // A run of CTA g in tile t leaves its partial rows in slot g with `splits`, in
 // slot g + t without (runs follow one another by a step of g or of t).
 
@@ -300,24 +305,25 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
     }
 }
 
-// CTA 0 ranks the tiles, then key_ctas CTAs of prefix keys, own_ctas of own keys
-// and the rest of queries.
+// CTA 0 ranks the tiles, then own_ctas CTAs of own keys (the longest chain of
+// loads first), query_ctas of queries and the rest of prefix keys.
 __global__ void __launch_bounds__(kPrepThreads)
-prefix_prepare_kernel(const PrefixArgs a, int key_ctas, int own_ctas)
+prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    int64_t c = blockIdx.x;
-    if (c == 0) {
+    int c = (int)blockIdx.x - 1;
+    if (c < 0) {
         prepare_tiles(a);
-    } else if ((c -= 1) < key_ctas) {
+    } else if (c < own_ctas) {
+        prepare_own(a, c);
+    } else if ((c -= own_ctas) < query_ctas) {
+        prepare_query(a, (int64_t)c * kPrepRows + (threadIdx.x >> 5));
+    } else {
+        c -= query_ctas;
         const int len = prefix_length(a);
         if (c * kPrepKeys < (len + kKeys - 1) / kKeys * kKeys)
-            prepare_keys(a, a.prefix_indices, (int)c * kPrepKeys, len, a.k_image, a.k_valid);
-    } else if ((c -= key_ctas) < own_ctas) {
-        prepare_own(a, (int)c);
-    } else {
-        prepare_query(a, (c - own_ctas) * kPrepRows + (threadIdx.x >> 5));
+            prepare_keys(a, a.prefix_indices, c * kPrepKeys, len, a.k_image, a.k_valid);
     }
 }
 
@@ -422,9 +428,13 @@ struct Walk {
     int64_t acc;      // x no mod nb
     __device__ __forceinline__ explicit Walk(const Run& r) : x(r.x0), k(0)
     {
-        const int64_t t = (int64_t)r.x0 * (r.nb - r.shared);
-        y = (int)(t / r.nb);
-        acc = t % r.nb;
+        y = 0;
+        acc = 0;
+        if (r.nb > r.shared) {
+            const int64_t t = (int64_t)r.x0 * (r.nb - r.shared);
+            y = (int)(t / r.nb);
+            acc = t % r.nb;
+        }
     }
     __device__ __forceinline__ bool own(const Run& r) const
     {
@@ -988,8 +998,8 @@ prefix_split_kernel(const PrefixArgs a)
         tile = (int)blockIdx.x / a.splits;
         const int s = (int)blockIdx.x % a.splits;
         tile_nb = __ldcg(a.tile_start + tile + 1) - __ldcg(a.tile_start + tile);
-        x = (int)(tile_nb * s / a.splits);
-        left = tile_nb * (s + 1) / a.splits - x;
+        x = (int)part_begin((uint32_t)tile_nb, s, a.splits);
+        left = (int)part_begin((uint32_t)tile_nb, s + 1, a.splits) - x;
     } else {
         const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)gridDim.x, U);
         if (g < G) {
@@ -1073,9 +1083,12 @@ prefix_split_kernel(const PrefixArgs a)
 
 // ---- prefix_merge -----------------------------------------------------------------------------
 //
-// W warps per output row (4 up to 512 rows, else 1), 16 / W columns per lane; a
-// CTA's rows are in one tile.  (Measured, 4 against 1: 64 rows of 12 partials 4.0
-// against 4.7 us, 512 of 19 6.9 against 7.9, 1024 of 9 6.8 against 4.7.)
+// W warps per output row, 16 / W columns per lane; a CTA's rows are in one tile.
+// Few rows have few warps, so as many take a row as leave one wave of CTAs (two an
+// SM), each with up to 20 (10) of its partials' loads in flight; with many rows one
+// warp does, two partials at a time.  (Measured: 512 rows of 19 partials 5.0 us at
+// W = 4 against 7.9 at 1; 1024 of 9 4.4 at 2 against 7.6 at 1; 8192 of 2 to 3 9.6
+// at 1 against 16.4 at 2.)
 // The row's partials are those of the runs of its tile and, without joined
 // tiles, the split kernel's: M = max lse, w = 2^(lse - M), o = sum w o_s / sum w,
 // summed in increasing order, lse = M + log2 sum w.  A partial of weight 0 is
@@ -1084,7 +1097,7 @@ prefix_split_kernel(const PrefixArgs a)
 constexpr int kMergeWarps = 8;
 constexpr int kMergeThreads = 32 * kMergeWarps;
 constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;   // partials of one tile or one request: 256 each
-constexpr int64_t kMergeFewRows = 512;
+constexpr int64_t kMergeRows4 = 512, kMergeRows2 = 1024;   // rows up to which W is 4, 2
 static_assert(kRows % kMergeWarps == 0, "a CTA's rows are in one tile");
 
 template <int W>
@@ -1092,7 +1105,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 prefix_merge_kernel(const PrefixArgs a)
 {
     constexpr int kQuads = 4 / W;        // groups of four columns per lane
-    constexpr int kAhead = 2 * W;        // partials in flight per lane
+    constexpr int kAhead = W == 1 ? 2 : 5 * W;   // partials in flight per lane
     constexpr int kMergeRows = kMergeWarps / W;
     __shared__ float weights[kMergeWarps][kMergeMax];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1105,13 +1118,14 @@ prefix_merge_kernel(const PrefixArgs a)
     float* w_s = weights[warp];
     // the tile's runs: slots [s0, s0 + np); a run without blocks has left nothing
     int64_t s0 = 0;
-    int np = 0, nb = 0;
+    int np = 0;
+    uint32_t nb = 0;
     if (a.ctas > 0) {
         const int64_t u0 = __ldcg(a.tile_start + tile), u1 = __ldcg(a.tile_start + tile + 1);
-        nb = (int)(u1 - u0);
-        if (a.splits > 0) {
+        nb = (uint32_t)(u1 - u0);
+        if (a.splits > 0) {   // (the partials' loads need not wait for nb)
             s0 = tile * a.splits;
-            np = nb > 0 ? a.splits : 0;
+            np = a.splits;
         } else if (nb > 0) {
             const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)a.ctas, U);
             const int64_t g0 = cta_of(u0, U, G);
@@ -1120,7 +1134,7 @@ prefix_merge_kernel(const PrefixArgs a)
         }
     }
     auto left_out = [&](int i) {   // equal parts of few blocks: some are empty
-        return a.splits > nb && (int64_t)nb * i / a.splits == (int64_t)nb * (i + 1) / a.splits;
+        return a.splits > 0 && part_begin(nb, i, a.splits) == part_begin(nb, i + 1, a.splits);
     };
     const int n = np + a.own_splits;
     const float* own = a.o_own + item * a.own_splits * kDv + col;
@@ -1209,19 +1223,21 @@ cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream)
     const int64_t key_ctas = prefix_blocks(a.prefix_cap) * (kKeys / kPrepKeys);
     const int64_t own_ctas =
         a.joined ? prefix_own_blocks(a.total_keys, a.batch) * (kKeys / kPrepKeys) : 0;
-    const int64_t ctas = 1 + key_ctas + own_ctas + (int64_t)a.tiles * (kRows / kPrepRows);
-    e = launch_pdl(prefix_prepare_kernel, dim3((unsigned)ctas), kPrepThreads, 0, stream, a,
-                   (int)key_ctas, (int)own_ctas);
+    const int64_t query_ctas = (int64_t)a.tiles * (kRows / kPrepRows);
+    e = launch_pdl(prefix_prepare_kernel, dim3((unsigned)(1 + own_ctas + query_ctas + key_ctas)),
+                   kPrepThreads, 0, stream, a, (int)own_ctas, (int)query_ctas);
     if (e != cudaSuccess) return e;
     return launch_pdl(prefix_split_kernel, dim3((unsigned)a.ctas), kThreads, kSmemBytes, stream, a);
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream)
 {
-    const bool few = a.rows <= kMergeFewRows;
-    const int64_t rows = kMergeWarps / (few ? 4 : 1);
-    return launch_pdl(few ? prefix_merge_kernel<4> : prefix_merge_kernel<1>,
-                      dim3((unsigned)((a.rows + rows - 1) / rows)), kMergeThreads, 0, stream, a);
+    const int w = a.rows <= kMergeRows4 ? 4 : a.rows <= kMergeRows2 ? 2 : 1;
+    auto* kernel = w == 4 ? prefix_merge_kernel<4> : w == 2 ? prefix_merge_kernel<2>
+                                                            : prefix_merge_kernel<1>;
+    const int64_t rows = kMergeWarps / w;
+    return launch_pdl(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), kMergeThreads, 0,
+                      stream, a);
 }
 
 }  // namespace mla

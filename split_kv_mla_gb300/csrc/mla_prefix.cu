@@ -1083,39 +1083,45 @@ prefix_split_kernel(const PrefixArgs a)
 
 // ---- prefix_merge -----------------------------------------------------------------------------
 //
-// W warps per output row, 16 / W columns per lane; a CTA's rows are in one tile.
-// Few rows have few warps, so as many take a row as leave one wave of CTAs (two an
-// SM), each with up to 20 (10) of its partials' loads in flight; with many rows one
-// warp does, two partials at a time.  (Measured: 512 rows of 19 partials 5.0 us at
-// W = 4 against 7.9 at 1; 1024 of 9 4.4 at 2 against 7.6 at 1; 8192 of 2 to 3 9.6
-// at 1 against 16.4 at 2.)
+// A CTA's warps are rows x G groups of partials x W column parts: a lane has 16 / W
+// columns of every G-th partial (group g: g, g + G, ...), the groups' sums are
+// added in increasing g.  Few rows have few warps, so as many take a row as leave
+// one wave of CTAs (two an SM), each with up to 20 (10) partials' loads in flight;
+// with many rows one warp does, two partials at a time.  (Measured: 512 rows of 19
+// partials 5.0 us at W = 4 against 7.9 at 1; 1024 of 9 4.4 at 2 against 7.6 at 1;
+// 8192 of 2 to 3 9.6 at 1 against 16.4 at 2.)  Few rows of many partials are a small
+// batch on a long prefix: there four groups share them.
 // The row's partials are those of the runs of its tile and, without joined
 // tiles, the split kernel's: M = max lse, w = 2^(lse - M), o = sum w o_s / sum w,
 // summed in increasing order, lse = M + log2 sum w.  A partial of weight 0 is
 // not added.  The first partials are loaded before the weights are known.
 
-constexpr int kMergeWarps = 8;
-constexpr int kMergeThreads = 32 * kMergeWarps;
 constexpr int kMergeMax = 2 * MLA_MAX_SPLITS;   // partials of one tile or one request: 256 each
 constexpr int64_t kMergeRows4 = 512, kMergeRows2 = 1024;   // rows up to which W is 4, 2
-static_assert(kRows % kMergeWarps == 0, "a CTA's rows are in one tile");
+constexpr int kMergeManyParts = 20;   // partials above which four groups share a row's
 
-template <int W>
-__global__ void __launch_bounds__(kMergeThreads)
+template <int W, int G>
+__global__ void __launch_bounds__(32 * (G > 1 ? W * G : 8))
 prefix_merge_kernel(const PrefixArgs a)
 {
     constexpr int kQuads = 4 / W;        // groups of four columns per lane
     constexpr int kAhead = W == 1 ? 2 : 5 * W;   // partials in flight per lane
-    constexpr int kMergeRows = kMergeWarps / W;
-    __shared__ float weights[kMergeWarps][kMergeMax];
+    constexpr int kWarps = G > 1 ? W * G : 8;
+    constexpr int kMergeRows = kWarps / (W * G);
+    static_assert(kRows % kMergeRows == 0, "a CTA's rows are in one tile");
+    static_assert(G == 1 || kMergeRows == 1, "the groups of a row are a CTA");
+    __shared__ float weights[G > 1 ? 1 : kWarps][kMergeMax];
+    __shared__ float4 group_sum[G > 1 ? G - 1 : 1][G > 1 ? W : 1][32];
+    __shared__ float row_sum_s;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * kMergeRows + warp / W;
+    const int64_t item = (int64_t)blockIdx.x * kMergeRows + warp / (W * G);
+    const int group = G > 1 ? warp / W : 0;
     const int col = warp % W * (128 * kQuads) + lane * 4;   // and every 128 columns on
     const int64_t tile = (int64_t)blockIdx.x * kMergeRows / kRows;
     if (item >= a.rows) return;   // whole warps, and no barrier follows
-    float* w_s = weights[warp];
+    float* w_s = weights[G > 1 ? 0 : warp];
     // the tile's runs: slots [s0, s0 + np); a run without blocks has left nothing
     int64_t s0 = 0;
     int np = 0;
@@ -1153,28 +1159,36 @@ prefix_merge_kernel(const PrefixArgs a)
     Cols ahead[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (i < n) ahead[i] = load(i);
-    float m = -CUDART_INF_F;
-    for (int i = lane; i < n; i += 32) {
-        float l = -CUDART_INF_F;
-        if (i >= np) l = __ldcg(a.lse_own + item * a.own_splits + (i - np));
-        else if (!left_out(i)) l = __ldcg(lse_part + i * kRows);
-        w_s[i] = l;
-        m = fmaxf(m, l);
-    }
+        if (group + i * G < n) ahead[i] = load(group + i * G);
+    // the weights: by every warp for itself, or by the CTA's first for all
+    float m = -CUDART_INF_F, sum = 0.f;
+    if (G == 1 || warp == 0) {
+        for (int i = lane; i < n; i += 32) {
+            float l = -CUDART_INF_F;
+            if (i >= np) l = __ldcg(a.lse_own + item * a.own_splits + (i - np));
+            else if (!left_out(i)) l = __ldcg(lse_part + i * kRows);
+            w_s[i] = l;
+            m = fmaxf(m, l);
+        }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float sum = 0.f;
-    for (int i = lane; i < n; i += 32) {
-        const float w = w_s[i] == -CUDART_INF_F ? 0.f : exp2f(w_s[i] - m);
-        sum += w;
-        w_s[i] = w * (i < np ? a.kv_scale : a.own_scale);
-    }
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int i = lane; i < n; i += 32) {
+            const float w = w_s[i] == -CUDART_INF_F ? 0.f : exp2f(w_s[i] - m);
+            sum += w;
+            w_s[i] = w * (i < np ? a.kv_scale : a.own_scale);
+        }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0 && warp % W == 0 && a.lse != nullptr)
-        a.lse[item] = sum != 0.f ? m + log2f(sum) : -CUDART_INF_F;
-    __syncwarp();
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0 && warp % W == 0 && a.lse != nullptr)
+            a.lse[item] = sum != 0.f ? m + log2f(sum) : -CUDART_INF_F;
+        if (G > 1 && lane == 0) row_sum_s = sum;
+    }
+    if constexpr (G > 1) {
+        __syncthreads();
+        sum = row_sum_s;
+    } else {
+        __syncwarp();
+    }
     Cols acc;
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) acc.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1191,14 +1205,28 @@ prefix_merge_kernel(const PrefixArgs a)
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (i < n) add(w_s[i], ahead[i]);
-    for (int i0 = kAhead; i0 < n; i0 += kAhead) {
+        if (group + i * G < n) add(w_s[group + i * G], ahead[i]);
+    for (int i0 = group + kAhead * G; i0 < n; i0 += kAhead * G) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < n) ahead[i] = load(i0 + i);
+            if (i0 + i * G < n) ahead[i] = load(i0 + i * G);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < n) add(w_s[i0 + i], ahead[i]);
+            if (i0 + i * G < n) add(w_s[i0 + i * G], ahead[i]);
+    }
+    if constexpr (G > 1) {
+        static_assert(G == 1 || kQuads == 1, "one float4 per lane and group");
+        if (group > 0) group_sum[group - 1][warp % W][lane] = acc.v[0];
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 0; g < G - 1; ++g) {
+            const float4 x = group_sum[g][warp % W][lane];
+            acc.v[0].x += x.x;
+            acc.v[0].y += x.y;
+            acc.v[0].z += x.z;
+            acc.v[0].w += x.w;
+        }
     }
     const float f = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -1232,12 +1260,15 @@ cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t stream)
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream)
 {
-    const int w = a.rows <= kMergeRows4 ? 4 : a.rows <= kMergeRows2 ? 2 : 1;
-    auto* kernel = w == 4 ? prefix_merge_kernel<4> : w == 2 ? prefix_merge_kernel<2>
-                                                            : prefix_merge_kernel<1>;
-    const int64_t rows = kMergeWarps / w;
-    return launch_pdl(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), kMergeThreads, 0,
-                      stream, a);
+    auto launch = [&](auto* kernel, int rows, int threads) {
+        return launch_pdl(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), threads, 0, stream, a);
+    };
+    const int parts = (a.splits > 0 ? a.splits : a.ctas / a.tiles) + a.own_splits;
+    if (a.rows <= kMergeRows4 && parts > kMergeManyParts)
+        return launch(prefix_merge_kernel<4, 4>, 1, 512);
+    if (a.rows <= kMergeRows4) return launch(prefix_merge_kernel<4, 1>, 2, 256);
+    if (a.rows <= kMergeRows2) return launch(prefix_merge_kernel<2, 1>, 4, 256);
+    return launch(prefix_merge_kernel<1, 1>, 8, 256);
 }
 
 }  // namespace mla

@@ -473,11 +473,13 @@ fork_kernel(const ForkArgs a)
 // each, and tail row k moves into hole k.  Sources lie at or past L and
 // destinations below it, so the moves run in any order.
 //   mark    sets the bits;
-//   count   the live slots of each chunk of 8192;
+//   count   the live slots of each chunk of 8192 (only for large pools);
 //   place   ranks: u at every bitmap word, the lists of holes and of tail rows;
 //   move    copies the tail rows and rewrites the table.
-// A small pool's mark, count and place are one CTA's work on a bitmap in shared
-// memory (rank_kernel).
+// A small pool's mark and place are one CTA's work on a bitmap in shared memory
+// (rank_kernel).  (One cooperative launch for everything, its phases parted by
+// grid barriers of about 2 us, took 13.4, 20.0 and 77 us for the pools of 8192,
+// 131072 and 1048576 rows that take 7.2, 16.4 and 70 this way.)
 
 constexpr int64_t kMoveCtas = 4 * 152;
 constexpr int kPlaceThreads = 256;                       // one bitmap word each
@@ -564,6 +566,12 @@ count_kernel(const CompactArgs a)
     if (threadIdx.x == 0) a.counts[blockIdx.x] = n;
 }
 
+// DIRECT: every CTA reads the whole bitmap (at most kDirectWords words, 32 a
+// thread) and needs no counts.
+constexpr int kDirectLoads = 8;   // of four words, per thread
+constexpr int64_t kDirectWords = 4 * kDirectLoads * kPlaceThreads;
+
+template <bool DIRECT>
 __global__ void __launch_bounds__(kPlaceThreads)
 place_kernel(const CompactArgs a)
 {
@@ -572,26 +580,56 @@ place_kernel(const CompactArgs a)
     allow_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = blockIdx.x;
-    // L, and the live slots below this chunk
-    int all = 0, before = 0;
-    for (int i = tid; i < a.chunks; i += kPlaceThreads) {
-        const int n = __ldcg(a.counts + i);
-        all += n;
-        before += i < c ? n : 0;
+    // L, the live slots below this chunk, and U
+    int all = 0, before = 0, L, U;
+    if constexpr (DIRECT) {
+        uint4 b[kDirectLoads];
+        auto first_of = [&](int k) { return (k * kPlaceThreads + tid) * 4; };   // word
+#pragma unroll
+        for (int k = 0; k < kDirectLoads; ++k) {
+            b[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (first_of(k) < a.chunks * kPlaceThreads)
+                b[k] = __ldcg(reinterpret_cast<const uint4*>(a.bits + first_of(k)));
+        }
+#pragma unroll
+        for (int k = 0; k < kDirectLoads; ++k) {
+            const int n = __popc(b[k].x) + __popc(b[k].y) + __popc(b[k].z) + __popc(b[k].w);
+            all += n;
+            before += first_of(k) < c * kPlaceThreads ? n : 0;
+        }
+        L = block_sum(all, part);
+        before = block_sum(before, part);
+        int under = 0;
+#pragma unroll
+        for (int k = 0; k < kDirectLoads; ++k) {
+            const uint32_t w[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = L - (first_of(k) + i) * 32;   // slots of this word below L
+                under += n <= 0 ? 0 : __popc(n >= 32 ? w[i] : w[i] & ((1u << n) - 1u));
+            }
+        }
+        U = block_sum(under, part);
+    } else {
+        for (int i = tid; i < a.chunks; i += kPlaceThreads) {
+            const int n = __ldcg(a.counts + i);
+            all += n;
+            before += i < c ? n : 0;
+        }
+        L = block_sum(all, part);
+        before = block_sum(before, part);
+        // the chunks below L's chunk, and the bits of L's chunk below L
+        const int lc = (int)(L / kChunkSlots);
+        int under = 0;
+        for (int i = tid; i < lc; i += kPlaceThreads) under += __ldcg(a.counts + i);
+        if (lc < a.chunks) {
+            const int64_t first = lc * kChunkSlots + (int64_t)tid * 32;
+            const int64_t n = L - first;   // slots of this word below L
+            const uint32_t w = __ldcg(a.bits + (int64_t)lc * kPlaceThreads + tid);
+            under += n <= 0 ? 0 : __popc(n >= 32 ? w : w & ((1u << n) - 1u));
+        }
+        U = block_sum(under, part);
     }
-    const int L = block_sum(all, part);
-    before = block_sum(before, part);
-    // U: the chunks below L's chunk, and the bits of L's chunk below L
-    const int lc = (int)(L / kChunkSlots);
-    int under = 0;
-    for (int i = tid; i < lc; i += kPlaceThreads) under += __ldcg(a.counts + i);
-    if (lc < a.chunks) {
-        const int64_t first = lc * kChunkSlots + (int64_t)tid * 32;
-        const int64_t n = L - first;   // slots of this word below L
-        const uint32_t w = __ldcg(a.bits + (int64_t)lc * kPlaceThreads + tid);
-        under += n <= 0 ? 0 : __popc(n >= 32 ? w : w & ((1u << n) - 1u));
-    }
-    const int U = block_sum(under, part);
     if (c == 0 && tid == 0) {
         a.totals[0] = L;
         a.totals[1] = U;
@@ -925,11 +963,14 @@ int mla_cache_compact(void* pool, int64_t pool_rows, int32_t row_bytes,
         if (e == cudaSuccess && num_indices > 0)
             e = launch_dependent(mark_kernel, dim3((unsigned)((num_indices + per - 1) / per)),
                                  kCopyThreads, s, false, a);
-        if (e == cudaSuccess)
+        const bool direct = (int64_t)a.chunks * kPlaceThreads <= kDirectWords;
+        if (e == cudaSuccess && !direct)
             e = launch_dependent(count_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s,
                                  num_indices > 0, a);
         if (e == cudaSuccess)
-            e = launch_dependent(place_kernel, dim3((unsigned)a.chunks), kPlaceThreads, s, true, a);
+            e = launch_dependent(direct ? place_kernel<true> : place_kernel<false>,
+                                 dim3((unsigned)a.chunks), kPlaceThreads, s,
+                                 !direct || num_indices > 0, a);
     }
     if (e == cudaSuccess) {
         // one turn a warp in the worst case, at most four CTAs an SM of a full GPU

@@ -1133,10 +1133,10 @@ prefix_merge_kernel(const PrefixArgs a)
             s0 = tile * a.splits;
             np = a.splits;
         } else if (nb > 0) {
-            const int64_t U = __ldcg(a.tile_start + a.tiles), G = min((int64_t)a.ctas, U);
-            const int64_t g0 = cta_of(u0, U, G);
+            const int64_t U = __ldcg(a.tile_start + a.tiles), ctas = min((int64_t)a.ctas, U);
+            const int64_t g0 = cta_of(u0, U, ctas);
             s0 = g0 + tile;
-            np = (int)(cta_of(u1 - 1, U, G) - g0) + 1;
+            np = (int)(cta_of(u1 - 1, U, ctas) - g0) + 1;
         }
     }
     auto left_out = [&](int i) {   // equal parts of few blocks: some are empty

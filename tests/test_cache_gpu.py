@@ -464,9 +464,11 @@ def test_compact_where_the_live_rows_lie(place):
 
 
 @pytest.mark.parametrize("rows,entries", [(16384, 32768), (16385, 9000), (16384, 32769),
-                                          (500, 40000), (300000, 120000)])
+                                          (500, 40000), (262144, 100000), (262145, 120000),
+                                          (300000, 120000), (1300000, 700001), (100000, 0)])
 def test_compact_both_sides_of_the_small_pool_rule(rows, entries):
-    # up to 16384 rows and 32768 entries one CTA ranks the pool, above three kernels
+    # up to 16384 rows and 32768 entries one CTA ranks the pool, above kernels do, with
+    # counts of chunks above 262144 rows
     g = torch.Generator().manual_seed(rows)
     pool = torch.randint(0, 256, (rows, 512), generator=g).to(torch.uint8)
     slots = torch.randint(0, rows, (entries,), generator=g).int()

@@ -445,12 +445,14 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
  *                  Outside [0, prefix_cap] it is clamped and sets
  *                  MLA_DEVERR_BAD_LENGTH.
  *   seq_lens, kv_indices, kv_indptr: the requests' own keys, as for mla_decode
- *                  (a request may have none; kv_indices may be NULL when
- *                  total_keys was 0)
+ *                  (a request may have none; kv_indices has the plan's total_keys
+ *                  entries and may be NULL when that is 0)
  *   workspace >= plan->workspace_bytes bytes, 256-byte aligned, zeroed header;
  *                  calls that share it must not overlap on the GPU
- * Other arguments, layouts and device errors as for mla_decode.  The merge joins
- * partials in a fixed order, so results do not vary from call to call.
+ * Other arguments, layouts and device errors as for mla_decode.  A NaN (or an
+ * infinite query) makes NaN of the output rows that see it, not of the batch's
+ * others.  The merge joins partials in a fixed order, so results do not vary from
+ * call to call.
  */
 int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const void* q_pe,
                       const void* pool, int64_t pool_rows, const int32_t* prefix_indices,
@@ -519,7 +521,8 @@ int mla_cache_append(const void* kv, int64_t kv_stride, const void* kv_weight,
  *                              = fresh[fresh_indptr[f] + j - keep[f]]  otherwise,
  *   pool[table[...]] = pool[kv_indices[kv_indptr[p] + j]]              (bytes)
  * keep[f] <= 0 copies every row, keep[f] >= n_f none.  The fresh slots of a
- * call are distinct and none is a slot that the call copies from.
+ * call are distinct and none is a slot that the call copies from; table overlaps
+ * no other argument.
  *   pool [pool_rows, row_bytes], row_bytes 576 or 512, 16-byte aligned
  *   kv_indices int32 [num_indices]; kv_indptr int32 [num_parents + 1]
  *   parents, keep int32 [num_children]; child_indptr, fresh_indptr int32

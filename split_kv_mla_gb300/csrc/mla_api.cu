@@ -652,7 +652,7 @@ constexpr double kOwnCallUs = 3.0;       // one more kernel in the call
 constexpr int64_t kMaxJoinedKeys = 1 << 24;
 
 struct PrefixLayout {   // byte offsets in the workspace
-    int64_t own_o, own_lse, o_part, lse_part, k_image, k_valid, q_image, q_scale, q_window,
+    int64_t own_o, own_lse, o_part, lse_part, k_image, k_flags, q_image, q_scale, q_window,
         tile_start, end;
 };
 
@@ -683,7 +683,7 @@ PrefixLayout prefix_layout(const mla_prefix_plan_t* p)
     l.o_part = take(prefix_slots(p) * kPrefixRows * kDenseDv * 4);
     l.lse_part = take(prefix_slots(p) * kPrefixRows * 4);
     l.k_image = take(blocks * kPrefixImage);
-    l.k_valid = take(blocks * 16);
+    l.k_flags = take(blocks * 32);
     l.q_image = take(tiles * kPrefixImage);
     l.q_scale = take(tiles * kPrefixRows * 4);
     l.q_window = take(tiles * kPrefixRows * 4);
@@ -835,7 +835,7 @@ int mla_prefix_decode(const mla_prefix_plan_t* plan, const void* q_lat, const vo
     a.kv_scale = kv_scale;
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.k_image = reinterpret_cast<uint8_t*>(ws + l.k_image);
-    a.k_valid = reinterpret_cast<uint32_t*>(ws + l.k_valid);
+    a.k_flags = reinterpret_cast<uint2*>(ws + l.k_flags);
     a.q_image = reinterpret_cast<uint8_t*>(ws + l.q_image);
     a.q_scale = reinterpret_cast<float*>(ws + l.q_scale);
     a.q_window = reinterpret_cast<int32_t*>(ws + l.q_window);

@@ -167,7 +167,7 @@ struct PrefixArgs {
     // workspace
     uint32_t* err;
     uint8_t* k_image;            // [prefix blocks, then own blocks][kPrefixImage]
-    uint32_t* k_valid;           // [blocks][4]: bit per key
+    uint2* k_flags;              // [blocks][4]: bits of 32 valid keys, of keys with NaN codes
     uint8_t* q_image;            // [tiles][kPrefixImage]: e4m3 terms of the queries
     float* q_scale;              // [tiles * 64] raw dot -> base-2 logit
     int32_t* q_window;           // [tiles * 64] positions the row sees

@@ -137,13 +137,28 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepKeys = 32;     // keys per CTA
 constexpr int kPrepRows = kPrepThreads / 32;   // query rows per CTA, one per warp
 
+// The top bits of v's bytes that are e4m3fn NaN codes (magnitude 0x7f).
+__device__ __forceinline__ uint32_t nan_bits(uint32_t v)
+{
+    return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// v with its NaN codes as zeros.
+__device__ __forceinline__ uint32_t without_nan(uint32_t v)
+{
+    return v & ~((nan_bits(v) >> 7) * 0xffu);
+}
+
 // Keys [k0, k0 + 32) of a list of `len` into rows k0 % 128 .. of block k0 / 128 of
-// `image`, as zero rows past the list's end and for bad slots.  The whole CTA.
+// `image`, as zero rows past the list's end and for bad slots.  A tile's rows need
+// not all see a key, and 0 x NaN is NaN in P.V: NaN codes become zeros here and
+// their keys are marked, so that the rows that see such a key (and only they)
+// take a NaN logit.  flags: valid and marked keys, a bit each.  The whole CTA.
 __device__ __forceinline__ void prepare_keys(const PrefixArgs& a, const int32_t* list, int k0,
-                                             int len, uint8_t* image, uint32_t* valid)
+                                             int len, uint8_t* image, uint2* flags)
 {
     __shared__ int32_t slots[kPrepKeys];
     const int tid = threadIdx.x;
+    flags += k0 / kPrepKeys;
     if (tid < kPrepKeys) {
         int32_t s = k0 + tid < len ? __ldg(list + k0 + tid) : -1;
         if (k0 + tid < len && (s < 0 || s >= a.pool_rows)) {
@@ -151,8 +166,8 @@ __device__ __forceinline__ void prepare_keys(const PrefixArgs& a, const int32_t*
             s = -1;
         }
         slots[tid] = s;
-        const uint32_t bits = __ballot_sync(0xffffffffu, s >= 0);
-        if (tid == 0) valid[k0 / kPrepKeys] = bits;
+        const uint32_t valid = __ballot_sync(0xffffffffu, s >= 0);
+        if (tid == 0) *flags = make_uint2(valid, 0u);
     }
     __syncthreads();
     image += k0 / kKeys * kPrefixImage;
@@ -171,9 +186,13 @@ __device__ __forceinline__ void prepare_keys(const PrefixArgs& a, const int32_t*
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int p = tid + i * kPrepThreads, row = p / kPieces;
-        if (p < kPrepKeys * kPieces)
-            *reinterpret_cast<uint4*>(image + tile_offset(row0 + row, p % kPieces * 16, kKeys)) =
-                v[i];
+        if (p >= kPrepKeys * kPieces) continue;
+        if ((nan_bits(v[i].x) | nan_bits(v[i].y) | nan_bits(v[i].z) | nan_bits(v[i].w)) != 0) {
+            atomicOr(&flags->y, 1u << row);
+            v[i] = make_uint4(without_nan(v[i].x), without_nan(v[i].y), without_nan(v[i].z),
+                              without_nan(v[i].w));
+        }
+        *reinterpret_cast<uint4*>(image + tile_offset(row0 + row, p % kPieces * 16, kKeys)) = v[i];
     }
 }
 
@@ -196,7 +215,7 @@ __device__ void prepare_own(const PrefixArgs& a, int c)
     const int k0 = (block - own_block0(first, lo)) * kKeys + c % 4 * kPrepKeys;
     if (k0 < 0 || k0 >= (len + kKeys - 1) / kKeys * kKeys) return;
     const int64_t at = prefix_image_blocks(a) + own_block0(first, lo);
-    prepare_keys(a, a.kv_indices + first, k0, len, a.k_image + at * kPrefixImage, a.k_valid + at * 4);
+    prepare_keys(a, a.kv_indices + first, k0, len, a.k_image + at * kPrefixImage, a.k_flags + at * 4);
 }
 
 // Blocks before each tile, by one CTA; it also reports bad lengths.
@@ -300,7 +319,8 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
             win = max((int64_t)0, P + len - a.q_len + t + 1);
             win = min(win, a.joined ? (int64_t)INT32_MAX : P);
         }
-        a.q_scale[item] = on ? mul_pow2(a.logit_scale, -sh) : 0.f;
+        // (an infinite query has no finite terms: its logits are NaN)
+        a.q_scale[item] = !on ? 0.f : isinf(amax) ? CUDART_NAN_F : mul_pow2(a.logit_scale, -sh);
         a.q_window[item] = (int32_t)win;
     }
 }
@@ -323,7 +343,7 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
         c -= query_ctas;
         const int len = prefix_length(a);
         if (c * kPrepKeys < (len + kKeys - 1) / kKeys * kKeys)
-            prepare_keys(a, a.prefix_indices, c * kPrepKeys, len, a.k_image, a.k_valid);
+            prepare_keys(a, a.prefix_indices, c * kPrepKeys, len, a.k_image, a.k_flags);
     }
 }
 
@@ -685,17 +705,17 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
         tile_requests(a, r.tile, b0, b1);
         row0 = (int)((int64_t)b0 * per - r.tile * kRows) - r0;
     }
-    // one block ahead: its valid keys, and where its first key is and whose
+    // one block ahead: its keys' flags, and where its first key is and whose
     Walk walk(r);
     bool looked = false;
-    uint32_t valid_next;
+    uint2 flags_next;   // valid and marked keys of this warp's 32
     int pos_next, k_next;   // k_next < 0: a prefix block
     auto look_ahead = [&]() {
         const bool own = walk.own(r);
         if (own && !looked)
             looked = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
-        valid_next = 0;
-        if (!own || looked) valid_next = __ldcg(a.k_valid + walk.image(r, ms) * 4 + quad);
+        flags_next = make_uint2(0u, 0u);
+        if (!own || looked) flags_next = __ldcg(a.k_flags + walk.image(r, ms) * 4 + quad);
         k_next = own ? walk.k : -1;
         pos_next = own ? P + (walk.y - (looked ? ms.own_before[walk.k] : 0)) * kKeys
                        : (walk.x - walk.y) * kKeys;
@@ -705,7 +725,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     for (int j = 0; j < n; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
-        const uint32_t valid = valid_next;
+        const uint32_t valid = flags_next.x, marked = flags_next.y;
         const int pos0 = pos_next, k_now = k_next;
         if (j + 1 < n) look_ahead();
         const bool ok = warp_wait(&ms.s_full[st], (uint32_t)(jj >> 1) & 1, abort_flag, 0,
@@ -750,8 +770,9 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
         // this rare path short: unrolled, it cost 2,500 cycles, most of them
         // fetching it.)
         uint32_t vis = 0xffffffffu;
-        if (k_now >= 0 || valid != 0xffffffffu || pos0 + kKeys > win_min) {
+        if (k_now >= 0 || valid != 0xffffffffu || marked != 0 || pos0 + kKeys > win_min) {
             const int pos = pos0 + ti;
+            const float bump = (marked >> lane) & 1u ? CUDART_NAN_F : 0.f;   // a key with NaN codes
             vis = 0;
             if ((valid >> lane) & 1u) {
 #pragma unroll 1
@@ -767,7 +788,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
                 vis &= hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
             }
 #pragma unroll
-            for (int k = 0; k < R; ++k) x[k] = (vis >> k) & 1u ? x[k] : -CUDART_INF_F;
+            for (int k = 0; k < R; ++k) x[k] = (vis >> k) & 1u ? x[k] + bump : -CUDART_INF_F;
         }
         float top = x[0];
 #pragma unroll

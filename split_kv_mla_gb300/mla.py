@@ -551,8 +551,10 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
             p.shape[-1] != 576 or kv_indptr.numel() != batch + 1):
         raise ValueError("q_lat [B * q_len, H, 512], q_pe [B * q_len, H, 64], pool [N, 576] and "
                          "kv_indptr [B + 1] must agree")
-    if prefix_indices.numel() != plan.prefix_cap or kv_indices.numel() < plan.own.total_keys:
+    if prefix_indices.numel() != plan.prefix_cap or kv_indices.numel() != plan.own.total_keys:
         raise ValueError("prefix_indices and kv_indices must have the plan's entries")
+    if prefix_len is not None and prefix_len.numel() != 1:
+        raise ValueError("prefix_len must have one entry")
     if o is None:
         o = torch.empty_like(q_lat)
     elif o.shape != q_lat.shape:

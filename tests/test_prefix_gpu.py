@@ -331,7 +331,37 @@ def test_a_query_with_nan_or_inf_stays_in_its_row():
     same[1, 3] = same[2, 0] = False
     assert torch.equal(got[0][same.cuda()], want[0][same.cuda()])
     assert torch.equal(got[1][same.cuda()], want[1][same.cuda()])
-    assert bool(torch.isnan(got[0][1, 3]).all()) and bool(torch.isnan(got[1][1, 3]))
+    for row in ((1, 3), (2, 0)):
+        assert bool(torch.isnan(got[0][row]).all()) and bool(torch.isnan(got[1][row]))
+
+
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+@pytest.mark.parametrize("column", [0, 300, 511, 570])
+def test_a_nan_row_stays_with_the_requests_that_see_it(byte, column):
+    # NaN codes in one request's own row, in a tile of four requests
+    s = make(1, 16, 400, [30, 5, 260, 2, 9], seed=24)
+    assert plan_of(s).joined == 1
+    want, _ = run(s)
+    pool = s.own.pool.clone()
+    slot = int(s.own.kv_indices[35 + 200])   # the third request's
+    pool[slot, 0, column] = byte
+    got, ws = run(Shared(dataclasses.replace(s.own, pool=pool), s.joined, s.prefix))
+    same = torch.arange(5, device="cuda") != 2
+    assert torch.equal(got[0][same], want[0][same]) and torch.equal(got[1][same], want[1][same])
+    assert bool(torch.isnan(got[0][2]).all()) and bool(torch.isnan(got[1][2]).all())
+    assert mla.mla_read_device_error(ws) == 0
+    # in the prefix every request sees it, but for the draft rows whose window ends before
+    s = make(3, 8, 400, [0, 1, 40], seed=25)
+    want, _ = run(s)
+    pool = s.own.pool.clone()
+    pool[int(s.prefix[398]), 0, column] = byte
+    for plan in both(s):
+        got, _ = run(Shared(dataclasses.replace(s.own, pool=pool), s.joined, s.prefix), plan)
+        blind = torch.zeros(9, dtype=torch.bool, device="cuda")
+        blind[0] = True   # request 0, draft 0: positions up to 397
+        want, _ = run(s, plan)
+        assert torch.equal(got[0][blind], want[0][blind])
+        assert bool(torch.isnan(got[0][~blind]).all()) and bool(torch.isnan(got[1][~blind]).all())
 
 
 def test_repeat_permuted_pool_and_given_outputs():
@@ -390,6 +420,30 @@ def test_pool_past_four_gigabytes():
     want, _ = run(s)
     got, _ = run(s, d=d)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_seeded_random_calls(seed):
+    rng = np.random.default_rng(1000 + seed)
+    q_len = int(rng.choice([1, 1, 1, 2, 3, 5]))
+    heads = int(rng.choice([1, 2, 7, 8, 16, 24, 64, 100, 128]))
+    batch = int(rng.integers(1, max(2, min(40, 2000 // (q_len * heads)))))
+    P = int(rng.choice([1, 64, 127, 128, 129, 500, 2000, 5000])) + int(rng.integers(0, 130))
+    top = int(rng.choice([1, 30, 129, 700]))
+    s = make(q_len, heads, P, rng.integers(0, top + 1, batch).tolist(), seed=seed)
+    plan = plan_of(s)
+    plans = [plan]
+    ctas = int(rng.integers(1, 153))
+    most = max(1, 152 // plan.tiles)
+    for j in (0, 1) if s.own.total_keys else (0,):
+        plans.append(variant(plan, ctas=ctas, splits=0, joined=j))
+        n = int(rng.integers(1, most + 1))
+        plans.append(variant(plan, ctas=plan.tiles * n, splits=n, joined=j))
+    ro, rl = oracle.dense_decode(s.joined)
+    for p in plans:
+        (o, lse), ws = run(s, p)
+        compare(o, lse, ro, rl, f"seed {seed} ctas {p.ctas} splits {p.splits} joined {p.joined}")
+        assert mla.mla_read_device_error(ws) == 0
 
 
 def test_a_wait_that_runs_out_ends_the_call():

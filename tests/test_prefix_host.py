@@ -42,7 +42,7 @@ def workspace_bytes(p):
     slots = 0 if p.ctas == 0 else p.ctas if p.splits else p.ctas + p.tiles
     tiles = p.tiles if p.ctas else 0
     return mla.MLA_WORKSPACE_HEADER_BYTES + sum(map(up, (
-        own * 2048, own * 4, slots * 64 * 2048, slots * 64 * 4, blocks * 73728, blocks * 16,
+        own * 2048, own * 4, slots * 64 * 2048, slots * 64 * 4, blocks * 73728, blocks * 32,
         tiles * 73728, tiles * 256, tiles * 256, (tiles + 1) * 8 if tiles else 0)))
 
 

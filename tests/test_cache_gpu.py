@@ -465,7 +465,8 @@ def test_compact_where_the_live_rows_lie(place):
 
 @pytest.mark.parametrize("rows,entries", [(16384, 32768), (16385, 9000), (16384, 32769),
                                           (500, 40000), (262144, 100000), (262145, 120000),
-                                          (300000, 120000), (1300000, 700001), (100000, 0)])
+                                          (300000, 120000), (1048576, 500000), (1048577, 300001),
+                                          (1300000, 700001), (100000, 0)])
 def test_compact_both_sides_of_the_small_pool_rule(rows, entries):
     # up to 16384 rows and 32768 entries one CTA ranks the pool, above kernels do, with
     # counts of chunks above 262144 rows

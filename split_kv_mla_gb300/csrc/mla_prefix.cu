@@ -232,14 +232,14 @@ __device__ void prepare_tiles(const PrefixArgs& a)
         int64_t mine = 0;
         if (t < a.tiles) {
             mine = (len + kKeys - 1) / kKeys;
-            if (a.joined) {
+            if (a.joined || a.own_splits == 0) {   // (else the split kernel reports)
                 int b0, b1;
                 tile_requests(a, t, b0, b1);
                 for (int b = b0; b <= b1; ++b) {
                     int first;
                     const int n = own_length(a, b, first);
                     if (n != __ldg(a.seq_lens + b)) atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
-                    mine += (n + kKeys - 1) / kKeys;
+                    mine += (n + kKeys - 1) / kKeys;   // none without entries
                 }
             }
         }
@@ -308,7 +308,8 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
             make_uint2((uint32_t)l[0] | ((uint32_t)l[1] << 16), (uint32_t)l[2] | ((uint32_t)l[3] << 16));
     }
     if (lane == 0) {
-        int64_t win = 0;
+        // (rows past the batch's last see everything: a mask would cost every block)
+        int64_t win = INT32_MAX;
         if (on) {
             // draft row t sees positions <= P + S_b - q_len + t, the prefix's first
             const int64_t r = item / a.num_heads;
@@ -349,11 +350,10 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 
 // ---- prefix_split -----------------------------------------------------------------------------
 //
-// Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests,
-// warps 4-11 are two softmax sets of four
-// warps; set s owns query rows 32 s .. 32 s + 31, warp w % 4 of a set the TMEM
-// lanes (keys) 32 (w % 4) .. + 31, one key per thread, as in the split kernel.
-// Warp 3 completes its warpgroup.
+// Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests, warps
+// 4-11 are two softmax sets of four warps; set s owns query rows 32 s .. 32 s + 31,
+// warp w % 4 of a set the TMEM lanes (keys) 32 (w % 4) .. + 31, one key per thread,
+// as in the split kernel.  Warp 3 completes its warpgroup.
 //
 // A stage's four latent chunks are released one by one, as the P.V MMAs of that
 // chunk finish, so the next block's chunks stream in behind them; the RoPE

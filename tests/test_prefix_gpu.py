@@ -177,6 +177,16 @@ def test_no_prefix_and_no_keys_at_all():
     check(s, "only the prefix")
 
 
+def test_lengths_without_a_table_are_reported():
+    s = make(1, 16, 200, [0, 0], seed=26)
+    d = to_cuda(s)
+    d["seq_lens"] = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    (o, lse), ws = run(s, d=d)
+    assert mla.mla_read_device_error(ws) == mla.MLA_DEVERR_BAD_LENGTH
+    ro, rl = oracle.dense_decode(s.joined)
+    compare(o, lse, ro, rl, "clamped to none")
+
+
 def test_length_on_the_device():
     # one plan and one captured graph serve every length up to the capacity
     s = make(2, 16, 1400, [30, 2, 250], seed=8)

@@ -1,4 +1,6 @@
-"""Thin Python binding of libmla (ctypes): argument marshalling only.
+"""Thin Python binding of libmla: argument marshalling only, through ctypes, and for
+the cache and shared-prefix calls, whose small sizes are bound by the host's time,
+through an extension module (``csrc/mla_binding.cpp``).
 
 Every function has the name of the C entry point it calls (``mla_decode_plan``,
 ``mla_decode``, ``mla_sparse_decode``, ``mla_splitk_reduce`` ...).  Tensors are
@@ -9,6 +11,8 @@ is not on a CUDA device the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -19,6 +23,7 @@ import torch
 from . import build as _build
 
 _lib = None
+_binding = None
 _lock = threading.Lock()
 
 MLA_OK = 0
@@ -497,31 +502,39 @@ def mla_decode_noalloc(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices
     return o_lat, lse
 
 
-# ---- arguments of the entry points below: checked once, in one place -----------------
+# ---- the extension module of the calls below -----------------------------------------
 
-def _device(t: torch.Tensor) -> int:
-    """The CUDA device of a call's first tensor, which must be the current one
-    (the library launches on the current device)."""
-    dev = t.get_device()
-    if dev < 0:
+def _native():
+    """The module that checks the calls' arguments and makes them, on the loaded
+    library (built first if it is missing)."""
+    global _binding
+    lib = load()
+    with _lock:
+        if _binding is None:
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                _build.build_binding()
+            loader = importlib.machinery.ExtensionFileLoader("mla_binding", path)
+            module = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader("mla_binding", loader))
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                          for n in ("mla_prefix_decode", "mla_cache_append", "mla_cache_fork",
+                                    "mla_cache_compact")), MlaError)
+            _binding = module
+    return _binding
+
+
+def _cuda_device(t: torch.Tensor) -> torch.device:
+    """Where a call's own workspace goes: its first tensor's device."""
+    if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on cuda:{dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
+    return t.device
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor of the dtype on device dev, or None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _stream_arg(stream) -> Optional[int]:
+    """None (the current stream) or a stream's handle."""
+    return None if stream is None else _stream_ptr(stream)
 
 
 # ---- decode over a shared prefix -----------------------------------------------------
@@ -542,63 +555,17 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
     """Dense decode of requests that share the prefix's slots and continue with
     their own (seq_lens, kv_indices, kv_indptr); returns (o, lse).  prefix_len
     int32 [1] on the device: how many of prefix_indices are in use (None: all)."""
-    dev = _device(q_lat)
-    R, H = q_lat.shape[0], q_lat.shape[1]
-    batch = seq_lens.shape[0]
-    q_len = R // batch if batch else plan.own.q_len
-    p = _pool_2d(pool, dev)
-    if (R != batch * q_len or q_lat.shape[2:] != (512,) or q_pe.shape != (R, H, 64) or
-            p.shape[-1] != 576 or kv_indptr.numel() != batch + 1):
-        raise ValueError("q_lat [B * q_len, H, 512], q_pe [B * q_len, H, 64], pool [N, 576] and "
-                         "kv_indptr [B + 1] must agree")
-    if prefix_indices.numel() != plan.prefix_cap or kv_indices.numel() != plan.own.total_keys:
-        raise ValueError("prefix_indices and kv_indices must have the plan's entries")
-    if prefix_len is not None and prefix_len.numel() != 1:
-        raise ValueError("prefix_len must have one entry")
-    if o is None:
-        o = torch.empty_like(q_lat)
-    elif o.shape != q_lat.shape:
-        raise ValueError("o must have q_lat's shape")
-    if lse is None and return_lse:
-        lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
-    elif lse is not None and lse.numel() != R * H:
-        raise ValueError("lse must be [B * q_len, H]")
+    if not isinstance(plan, mla_prefix_plan_t):
+        raise TypeError("plan must come from mla_prefix_decode_plan")
     if workspace_t is None:
-        workspace_t = workspace(plan, q_lat.device)
-    i32, bf16 = torch.int32, torch.bfloat16
-    _check((_lib or load()).mla_prefix_decode(
-        ctypes.byref(plan), _ptr(q_lat, "q_lat", bf16, dev), _ptr(q_pe, "q_pe", bf16, dev),
-        p.data_ptr(), p.shape[0], _ptr(prefix_indices, "prefix_indices", i32, dev),
-        _ptr(prefix_len, "prefix_len", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev),
-        _ptr(kv_indices, "kv_indices", i32, dev), _ptr(kv_indptr, "kv_indptr", i32, dev), batch,
-        q_len, H, scale, kv_scale, _ptr(o, "o", bf16, dev), _ptr(lse, "lse", torch.float32, dev),
-        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
-        _stream_ptr(stream)), "mla_prefix_decode")
-    return o, lse
+        workspace_t = workspace(plan, _cuda_device(q_lat))
+    return (_binding or _native()).prefix_decode(
+        ctypes.addressof(plan), q_lat, q_pe, pool, prefix_indices, seq_lens, kv_indices,
+        kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace_t, _stream_arg(stream),
+        return_lse)
 
 
 # ---- the cache: append, fork, compact ------------------------------------------------
-
-def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
-    """t as [..., columns] whose last dimension is contiguous."""
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t
-
-
-def _pool_2d(pool: torch.Tensor, dev: int) -> torch.Tensor:
-    """The pool: [rows, row_bytes], or a [rows, 1, row_bytes] cache, of bytes."""
-    if pool.element_size() != 1 or pool.dim() not in (2, 3) or (pool.dim() == 3 and
-                                                               pool.shape[1] != 1):
-        raise ValueError("pool must hold one byte per element, [rows, row_bytes]")
-    if pool.get_device() != dev:
-        raise ValueError(f"pool must be on cuda:{dev}, got {pool.device}")
-    if not pool.is_contiguous():
-        raise ValueError("pool must be contiguous")
-    return pool
-
 
 def cache_workspace(pool_rows: int = 0, device=None) -> torch.Tensor:
     """A zeroed workspace for mla_cache_append and mla_cache_fork, and with the
@@ -622,55 +589,12 @@ def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0,
     queries), rows contiguous, other strides free in steps of 8 elements;
     positions int32 [T]; cos_sin fp32 [max_positions, 64], 32 cosines then 32
     sines.  q_nope is None when q_cols is 64 (or without queries)."""
-    first = kv if kv is not None else q
-    if first is None:
-        raise ValueError("kv or q must be given")
-    dev = _device(first)
-    T = first.shape[0]
-    kv_ptr = kv_stride = pool_rows = width = 0
-    if kv is not None:
-        if slots is None or pool is None:
-            raise ValueError("slots and pool must be given with kv")
-        p = _pool_2d(pool, dev)
-        pool_rows, width = p.shape[0], p.shape[-1]
-        if _rows(kv, "kv").dim() != 2 or kv.shape[1] != width:
-            raise ValueError(f"kv must be [T, {width}], the pool's row width")
-        if slots.numel() != T:
-            raise ValueError("slots must have one entry per token")
-        if kv_weight is not None and kv_weight.numel() != int(kv_norm_cols):
-            raise ValueError("kv_weight must have kv_norm_cols entries")
-        kv_ptr, kv_stride = kv.data_ptr(), kv.stride(0)
-    if positions.numel() != T:
-        raise ValueError("positions must have one entry per token")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
-        raise ValueError("cos_sin must be [max_positions, 64]")
-    H = cols = q_ptr = qts = qhs = 0
-    if q is not None:
-        if _rows(q, "q").dim() != 3 or q.shape[0] != T or q.get_device() != dev:
-            raise ValueError(f"q must be [T, H, q_cols] on cuda:{dev}")
-        H, cols = q.shape[1], q.shape[2]
-        if q_weight is not None and q_weight.numel() != cols:
-            raise ValueError("q_weight must have q_cols entries")
-        q_ptr, qts, qhs = q.data_ptr(), q.stride(0), q.stride(1)
-        if q_nope is None and cols > 64:
-            q_nope = torch.empty(T, H, cols - 64, dtype=torch.bfloat16, device=q.device)
-        if q_pe is None:
-            q_pe = torch.empty(T, H, 64, dtype=torch.bfloat16, device=q.device)
-        if q_pe.numel() != T * H * 64 or (cols > 64 and q_nope.numel() != T * H * (cols - 64)):
-            raise ValueError("q_nope and q_pe must be [T, H, q_cols - 64] and [T, H, 64]")
     if workspace_t is None:
-        workspace_t = cache_workspace(device=first.device)
-    i32, bf16 = torch.int32, torch.bfloat16
-    _check((_lib or load()).mla_cache_append(
-        kv_ptr or None, kv_stride, _ptr(kv_weight, "kv_weight", bf16, dev), kv_norm_cols,
-        _ptr(slots, "slots", i32, dev), pool.data_ptr() if kv is not None else None, pool_rows,
-        width, kv_scale, q_ptr or None, qts, qhs, _ptr(q_weight, "q_weight", bf16, dev),
-        1 if q_norm else 0, cols, _ptr(q_nope, "q_nope", bf16, dev), _ptr(q_pe, "q_pe", bf16, dev),
-        _ptr(positions, "positions", i32, dev), _ptr(cos_sin, "cos_sin", torch.float32, dev),
-        cos_sin.shape[0], 1 if half_split else 0, eps, T, H,
-        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
-        _stream_ptr(stream)), "mla_cache_append")
-    return q_nope, q_pe
+        first = kv if kv is not None else q
+        workspace_t = None if first is None else cache_workspace(device=_cuda_device(first))
+    return (_binding or _native()).cache_append(
+        kv, slots, pool, positions, cos_sin, kv_scale, q, kv_weight, kv_norm_cols, q_weight,
+        q_norm, eps, half_split, q_nope, q_pe, workspace_t, _stream_arg(stream))
 
 
 def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, total: int, fresh,
@@ -678,28 +602,11 @@ def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, tot
     """Page tables of requests that continue `parents`, sharing their first
     keep[f] slots and copying the other rows to fresh slots; returns the
     children's kv_indices int32 [total] (their kv_indptr is child_indptr)."""
-    dev = _device(pool)
-    p = _pool_2d(pool, dev)
-    F = parents.numel()
-    if keep.numel() != F or child_indptr.numel() != F + 1 or fresh_indptr.numel() != F + 1:
-        raise ValueError("keep, child_indptr and fresh_indptr must match parents")
-    if table is None:
-        table = torch.empty(int(total), dtype=torch.int32, device=pool.device)
-    elif table.numel() < total:
-        raise ValueError("table must have total entries")
     if workspace_t is None:
-        workspace_t = cache_workspace(device=pool.device)
-    i32 = torch.int32
-    _check((_lib or load()).mla_cache_fork(
-        p.data_ptr(), p.shape[0], p.shape[-1], _ptr(kv_indices, "kv_indices", i32, dev),
-        kv_indices.numel(), _ptr(kv_indptr, "kv_indptr", i32, dev),
-        max(0, kv_indptr.numel() - 1), _ptr(parents, "parents", i32, dev),
-        _ptr(keep, "keep", i32, dev), _ptr(child_indptr, "child_indptr", i32, dev), F,
-        _ptr(fresh, "fresh", i32, dev), fresh.numel(),
-        _ptr(fresh_indptr, "fresh_indptr", i32, dev), _ptr(table, "table", i32, dev), total,
-        _ptr(workspace_t, "workspace", torch.uint8, dev), workspace_t.numel(),
-        _stream_ptr(stream)), "mla_cache_fork")
-    return table
+        workspace_t = cache_workspace(device=_cuda_device(pool))
+    return (_binding or _native()).cache_fork(
+        pool, kv_indices, kv_indptr, parents, keep, child_indptr, total, fresh, fresh_indptr,
+        table, workspace_t, _stream_arg(stream))
 
 
 def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t=None,
@@ -707,20 +614,7 @@ def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t
     """Move the rows that kv_indices names to the front of the pool, in place;
     returns (new_indices, live): the rewritten table and the live row count
     int32 [1] (rows from there on are free).  new_indices may be kv_indices."""
-    dev = _device(pool)
-    p = _pool_2d(pool, dev)
-    if new_indices is None:
-        new_indices = torch.empty_like(kv_indices)
-    elif new_indices.numel() != kv_indices.numel():
-        raise ValueError("new_indices must match kv_indices")
-    if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=pool.device)
     if workspace_t is None:
-        workspace_t = cache_workspace(p.shape[0], device=pool.device)
-    i32 = torch.int32
-    _check((_lib or load()).mla_cache_compact(
-        p.data_ptr(), p.shape[0], p.shape[-1], _ptr(kv_indices, "kv_indices", i32, dev),
-        kv_indices.numel(), _ptr(new_indices, "new_indices", i32, dev),
-        _ptr(live, "live", i32, dev), _ptr(workspace_t, "workspace", torch.uint8, dev),
-        workspace_t.numel(), _stream_ptr(stream)), "mla_cache_compact")
-    return new_indices, live
+        workspace_t = cache_workspace(pool.shape[0], device=_cuda_device(pool))
+    return (_binding or _native()).cache_compact(pool, kv_indices, new_indices, live, workspace_t,
+                                                 _stream_arg(stream))

@@ -394,6 +394,27 @@ def test_repeat_permuted_pool_and_given_outputs():
     assert torch.equal(o, o4) and torch.equal(lse, lse4)
 
 
+def test_tensors_that_do_not_agree_are_refused():
+    """Every wrong tensor here is larger than the right one: it holds what a call would read."""
+    s = make(1, 16, 100, [30, 7], seed=91)
+    plan, d = plan_of(s), to_cuda(s)
+    ws = mla.workspace(plan)
+    for name, t in d.items():
+        wider = torch.zeros(t.shape, device="cuda",
+                            dtype=torch.int64 if t.dtype == torch.int32 else torch.float64)
+        longer = torch.cat([t, t])
+        apart = torch.stack([t, t], dim=-1)[..., 0]
+        for other in (wider, apart) + (() if name == "pool" else (longer,)):
+            with pytest.raises(ValueError):
+                run(s, plan, ws, dict(d, **{name: other}))
+    for kw in (dict(o=torch.empty(4, 16, 512, dtype=torch.bfloat16, device="cuda")),
+               dict(o=torch.empty(2, 16, 512, dtype=torch.float32, device="cuda")),
+               dict(lse=torch.empty(2, 32, device="cuda")),
+               dict(lse=torch.empty(2, 16, dtype=torch.float64, device="cuda"))):
+        with pytest.raises(ValueError):
+            run(s, plan, ws, d, **kw)
+
+
 def test_another_stream_and_calls_back_to_back():
     a, b = make(1, 16, 900, [30, 5], seed=17), make(1, 64, 300, [3, 80, 9], seed=18)
     da, db, pa, pb = to_cuda(a), to_cuda(b), plan_of(a), plan_of(b)

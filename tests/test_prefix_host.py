@@ -188,6 +188,23 @@ def test_no_device_is_an_error(lib):
     assert call(lib, empty, batch=0) == 0
 
 
+def test_binding_refuses_other_objects():
+    z = torch.zeros
+    i = z(4, dtype=torch.int32)
+    args = (z(2, 16, 512, dtype=torch.bfloat16), z(2, 16, 64, dtype=torch.bfloat16),
+            z(8, 576, dtype=torch.uint8), i, i[:2], i, i[:3], 0.04, 0.03)
+    ws = z(1 << 20, dtype=torch.uint8)
+    with pytest.raises(TypeError):    # the plan of the plain decode
+        mla.mla_prefix_decode(mla.mla_plan_t(), *args)
+    with pytest.raises(TypeError):
+        mla.mla_prefix_decode(None, *args)
+    p = mla.mla_prefix_decode_plan(2, 1, 16, 4, 4, 152)
+    for k in range(7):                # neither a list nor nothing is a tensor
+        for other in ([1, 2], None):
+            with pytest.raises(ValueError):
+                mla.mla_prefix_decode(p, *args[:k], other, *args[k + 1:], workspace_t=ws)
+
+
 def test_binding_refusals():
     p = mla.mla_prefix_decode_plan(2, 1, 16, 4, 4, 152)
     z = torch.zeros

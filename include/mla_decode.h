@@ -180,7 +180,9 @@ int mla_sparse_decode_plan(int32_t num_tokens, int32_t num_heads, int32_t topk,
  * (512+64)^-0.5); kv_scale dequantizes the pool.  Rows are copied in 128-key
  * blocks: the keys of a block that a call masks (past a request's length, or
  * invalid sparse entries) become zero rows without reading the pool, so only
- * the rows the page table names need finite e4m3fn bytes.
+ * the rows the page table names matter.  A NaN code in one of those, or a NaN or
+ * infinite query, makes NaN of o and lse in the rows that see it and leaves every
+ * other row as it is.
  */
 int mla_decode(const mla_plan_t* plan, const void* q_lat, const void* q_pe,
                const void* pool, int64_t pool_rows, const int32_t* seq_lens,

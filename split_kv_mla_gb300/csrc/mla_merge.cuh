@@ -5,7 +5,7 @@
 // association, so results are deterministic).  For one output row with split
 // partials o_s (already normalised, o_s = O_s / l_s) and base-2 LSEs lse_s:
 //   M    = max_s lse_s
-//   w_s  = 2^(lse_s - M)            (0 when lse_s or M is -inf)
+//   w_s  = 2^(lse_s - M)            (0 when lse_s is -inf; NaN makes NaN of the row)
 //   o    = out_scale * (sum_s w_s o_s) / (sum_s w_s)
 //   lse  = M + log2(sum_s w_s)      (-inf when every lse_s is -inf)
 // The fixed association: sum_s w_s is a per-lane sum over s = lane, lane + 32,
@@ -47,7 +47,7 @@ __device__ __forceinline__ void merge_weights(const float* lse, int ns, float* w
     for (int k = 0; k < kPer; ++k) {
         const int s = lane + 32 * k;
         if (s < ns) {
-            const float ws = (m == -CUDART_INF_F || l[k] == -CUDART_INF_F) ? 0.f : exp2f(l[k] - m);
+            const float ws = l[k] == -CUDART_INF_F ? 0.f : exp2f(l[k] - m);
             w[s] = ws;
             part += ws;
         }

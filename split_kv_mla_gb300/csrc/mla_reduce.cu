@@ -74,8 +74,8 @@ splitk_reduce_kernel(const float* __restrict__ o_part, const float* __restrict__
         float m, wsum;
         merge_weights(lse_part + row * num_splits, num_splits, w_s, m, wsum, tid);
         if (tid == 0) {
-            fscale = wsum > 0.f ? out_scale / wsum : 0.f;
-            if (lse != nullptr) lse[row] = wsum > 0.f ? m + log2f(wsum) : -CUDART_INF_F;
+            fscale = wsum != 0.f ? out_scale / wsum : 0.f;
+            if (lse != nullptr) lse[row] = wsum != 0.f ? m + log2f(wsum) : -CUDART_INF_F;
         }
     }
     __syncthreads();
@@ -153,8 +153,8 @@ dcp_merge_kernel(const PartT* __restrict__ parts, const float* __restrict__ lse_
         float m, wsum;
         merge_weights(lse_in + row, world, w_s, m, wsum, tid, rows);
         if (tid == 0) {
-            fscale = wsum > 0.f ? 1.f / wsum : 0.f;
-            if (lse != nullptr) lse[row] = wsum > 0.f ? m + log2f(wsum) : -CUDART_INF_F;
+            fscale = wsum != 0.f ? 1.f / wsum : 0.f;
+            if (lse != nullptr) lse[row] = wsum != 0.f ? m + log2f(wsum) : -CUDART_INF_F;
         }
     }
     __syncthreads();

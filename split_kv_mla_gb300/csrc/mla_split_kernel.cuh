@@ -222,6 +222,18 @@ __device__ __forceinline__ float split_q3(float a, float b, uint16_t& hi, uint16
     return fabsf(la) + fabsf(lb);   // the two lo terms' size, before their rounding
 }
 
+// Zeros in place of the NaN codes (magnitude 0x7f) of a key's latent columns in its
+// stage, four chunks of 128 bytes from `row` on.
+__device__ __forceinline__ void clear_nan_codes(uint8_t* row)
+{
+#pragma unroll 1
+    for (int i = 0; i < 4 * 32; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(row + i / 32 * (kBlockN * 128)) + i % 32;
+        const uint32_t nan = ((*w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        if (nan != 0) *w &= ~((nan >> 7) * 0xffu);
+    }
+}
+
 // One TMEM row of R query-row columns: hi columns at taddr_hi plus lo columns
 // at taddr_lo (the two halves of the stacked MMA output), summed.
 // The hi and lo columns of R rows, loads issued without waiting.
@@ -292,8 +304,9 @@ __device__ __forceinline__ void load_rows(uint32_t taddr_hi, uint32_t taddr_mid,
 // % MC) each hold their normalised fp32 partial rows o_s (staged in the idle KV
 // stages) and base-2 LSEs lse_s in shared memory.  Cluster rank r merges rows
 // [r RS, (r + 1) RS) of the tile, RS = N / MC, over the MC peers' shared memory
-// (the merge of mla_splitk_reduce: M = max lse_s, w_s = 2^(lse_s - M),
-// o = sum w_s o_s / sum w_s in increasing split order, lse = M + log2 sum w_s).
+// (the merge of mla_splitk_reduce: M = max lse_s, w_s = 2^(lse_s - M), o = sum w_s
+// o_s / sum w_s in increasing split order, lse = M + log2 sum w_s; a NaN LSE makes
+// NaN of the row).
 // With one cluster per tile that is the final row.  Otherwise each cluster
 // writes its merged slice (normalised, with its LSE) to the workspace and takes
 // a ticket per (tile, rank); the rank-r CTA of the last cluster to arrive merges
@@ -347,7 +360,7 @@ __device__ __forceinline__ void fused_merge(uint8_t* smem, Misc& ms, const Split
 #pragma unroll
             for (int p = 0; p < MC; ++p) {
                 const float l = ms.mlse[rr * MC + p];
-                const float wp = (m == -CUDART_INF_F || l == -CUDART_INF_F) ? 0.f : exp2f(l - m);
+                const float wp = l == -CUDART_INF_F ? 0.f : exp2f(l - m);
                 wsum[k] += wp;
                 const float4 v = ld_dsmem_f32x4(dsmem_addr(src, (uint32_t)p));
                 acc[k].x += wp * v.x;
@@ -371,9 +384,9 @@ __device__ __forceinline__ void fused_merge(uint8_t* smem, Misc& ms, const Split
 #pragma unroll
         for (int p = 0; p < MC; ++p) {
             const float l = ms.mlse[rr * MC + p];
-            ws += (m == -CUDART_INF_F || l == -CUDART_INF_F) ? 0.f : exp2f(l - m);
+            ws += l == -CUDART_INF_F ? 0.f : exp2f(l - m);
         }
-        return ws > 0.f ? m + log2f(ws) : -CUDART_INF_F;
+        return ws != 0.f ? m + log2f(ws) : -CUDART_INF_F;
     };
     auto store_final = [&](long long item, int q, float4 v) {
         if (a.o_f32 != nullptr) {
@@ -395,7 +408,7 @@ __device__ __forceinline__ void fused_merge(uint8_t* smem, Misc& ms, const Split
             const int rr = rr_of[k], q = w % kQuads;
             const long long item = ms.row_item[r0 + rr];
             if (item < 0) continue;
-            const float f = wsum[k] > 0.f ? a.out_scale / wsum[k] : 0.f;
+            const float f = wsum[k] != 0.f ? a.out_scale / wsum[k] : 0.f;
             store_final(item, q, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
             if (q == 0 && a.lse != nullptr) a.lse[item] = slice_lse(rr);
         }
@@ -409,7 +422,7 @@ __device__ __forceinline__ void fused_merge(uint8_t* smem, Misc& ms, const Split
         const int rr = rr_of[k], q = w % kQuads;
         const long long item = ms.row_item[r0 + rr];
         if (item < 0) continue;
-        const float f = wsum[k] > 0.f ? 1.f / wsum[k] : 0.f;
+        const float f = wsum[k] != 0.f ? 1.f / wsum[k] : 0.f;
         *reinterpret_cast<float4*>(a.o_part + (item * nclus + clus) * C::kDv + q * 4) =
             make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
         if (q == 0) a.lse_part[item * nclus + clus] = slice_lse(rr);
@@ -437,12 +450,12 @@ __device__ __forceinline__ void fused_merge(uint8_t* smem, Misc& ms, const Split
         float m = -CUDART_INF_F, ws = 0.f;
         for (int c = 0; c < nclus; ++c) m = fmaxf(m, w[c]);
         for (int c = 0; c < nclus; ++c) {
-            const float wc = (m == -CUDART_INF_F || w[c] == -CUDART_INF_F) ? 0.f : exp2f(w[c] - m);
+            const float wc = w[c] == -CUDART_INF_F ? 0.f : exp2f(w[c] - m);
             w[c] = wc;
             ws += wc;
         }
-        if (item >= 0 && a.lse != nullptr) a.lse[item] = ws > 0.f ? m + log2f(ws) : -CUDART_INF_F;
-        ms.xs[t] = ws > 0.f ? a.out_scale / ws : 0.f;
+        if (item >= 0 && a.lse != nullptr) a.lse[item] = ws != 0.f ? m + log2f(ws) : -CUDART_INF_F;
+        ms.xs[t] = ws != 0.f ? a.out_scale / ws : 0.f;
     }
     asm volatile("bar.sync 4, %0;" ::"n"(kThr) : "memory");
 #pragma unroll
@@ -688,7 +701,7 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
     // Block j into stage j & 1.  Warp 0 announces the stage's bytes, which
     // arrive from the seven warps' copies.  The four-row groups past the split's
     // end are not fetched from block 2 on: their rows are masked, and the stage
-    // still holds block j-2's rows there (finite bytes; the copy engine's issue
+    // still holds block j-2's rows there (cleared of NaN codes; the copy engine's issue
     // rate, not DRAM, bounds a block, so a short last block costs less).  The
     // stages' first fills copy every group (zero rows for masked keys), so no
     // row of a stage is ever read uninitialised.
@@ -882,7 +895,9 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
             if (lane == 0) {
                 const int idx = hb * N + n;
                 const bool valid = idx < rows_in_req;
-                const float cq = valid ? mul_pow2(a.logit_scale, -sh) : 0.f;
+                // (an infinite query has no finite terms: its logits are NaN)
+                const float cq = !valid ? 0.f : isinf(amax) ? CUDART_NAN_F
+                                                            : mul_pow2(a.logit_scale, -sh);
                 ms.cq[n] = cq;
                 ms.win[n] = valid ? window(idx / a.num_heads) : -1;
                 if (lsum * (448.f / 1024.f) * fabsf(cq) > 1.f / 65536.f) ms.q3 = 1;
@@ -1103,6 +1118,11 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.s_free[st]);
             const bool kval = ms.kvalid[st][ti] != 0;
+            // A key with NaN codes has a NaN dot product with every row (so has every
+            // key with a NaN query: nothing is found then).  Rows that see it take a
+            // NaN weight from it; the others' weight is 0, and so V has to be
+            // finite, for them and for a later block that leaves this row in the stage.
+            if (s[0] != s[0]) clear_nan_codes(smem + C::kOffStage + st * C::kStageBytes + ti * 128);
             const int j = k0 + blk * kBlockN + ti;
             // Per-row logit scales and windows as 16-byte loads, and a
             // branch-free mask.  The draft window only bites in blocks that reach
@@ -1261,7 +1281,7 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
 #pragma unroll
             for (int n = 0; n < R; ++n)
                 if (n == ti) mr = m_ref[n];
-            ms.fin[1][row] = lsum > 0.f ? mr + log2f(lsum) - kShift : -CUDART_INF_F;
+            ms.fin[1][row] = lsum != 0.f ? mr + log2f(lsum) - kShift : -CUDART_INF_F;
             const int idx = hb * N + row;
             ms.row_item[row] = idx < rows_in_req
                 ? ((int64_t)b * a.q_len + idx / a.num_heads) * a.num_heads + idx % a.num_heads
@@ -1286,7 +1306,7 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
         for (int n = 0; n < R; ++n) {
             const float lt = (ms.redt[set * 4][n] + ms.redt[set * 4 + 1][n]) +
                              (ms.redt[set * 4 + 2][n] + ms.redt[set * 4 + 3][n]);
-            scl[n] = (have_o && lt > 0.f) ? rcp_approx(lt) * fscale : 0.f;
+            scl[n] = (have_o && lt != 0.f) ? rcp_approx(lt) * fscale : 0.f;
         }
         auto stage_chunk = [&](int c, const uint32_t (&h)[R], const uint32_t (&l)[R]) {
             if (final16) {

@@ -170,7 +170,8 @@ struct PrefixArgs {
     uint2* k_flags;              // [blocks][4]: bits of 32 valid keys, of keys with NaN codes
     uint8_t* q_image;            // [tiles][kPrefixImage]: e4m3 terms of the queries
     float* q_scale;              // [tiles * 64] raw dot -> base-2 logit
-    int32_t* q_window;           // [tiles * 64] positions the row sees
+    int32_t* q_window;           // [tiles * 64] positions the row sees; sign bit: the row
+                                 // wants its query's third term
     int64_t* tile_start;         // [tiles + 1] blocks before the tile
     float* o_part;               // [slots][64][512], normalised
     float* lse_part;             // [slots][64]

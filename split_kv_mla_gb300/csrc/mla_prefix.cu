@@ -20,7 +20,10 @@
 //     p = 2^(s - m),  O^T[512 x 64] += V^T[512 x 128] . (p_hi + p_lo)
 //   with K and V e4m3 as they are stored.  A query row, scaled to max |q| in
 //   [128, 256), is q_hi + 2^-5 q_lo, both e4m3: exact for a bf16 element within
-//   2^-14 of the row's maximum and within 2^-23 of that maximum below.
+//   2^-14 of the row's maximum and off by at most 2^-22 of that maximum below.
+//   Where that could move a logit by 2^-11, the row's tile adds a third term, the
+//   rest in e5m2 in q_lo's units: exact within 2^-18 of the maximum, off by at most
+//   2^-26 of it below.
 //   p = p_hi + p_lo is an e4m3 term and the residual in e5m2, whose 2^-16
 //   smallest step lets both terms accumulate into the same columns without a
 //   scale of their own (a second set of columns does not fit: O^T takes 256 of
@@ -60,6 +63,9 @@ static_assert(4 * kChunk + kRopeBytes == kPrefixImage, "image of a block or a qu
 static_assert(2 * kRows == kKeys, "a query tile's two terms have a block's layout");
 constexpr int kQLoBits = 5;                   // q_lo is stored times 2^5
 constexpr float kQLoBack = 1.f / (1 << kQLoBits);
+// The largest error of a base-2 logit that a tile's two terms may leave (by a bound
+// with every key at +-448; with random keys a thirtieth of it): half the LSE's bar.
+constexpr float kThirdAbove = 1.f / 2048.f;
 
 // A grid kernel launched as a programmatic dependent of its predecessor.
 template <typename... KArgs, typename... Args>
@@ -262,22 +268,18 @@ __device__ void prepare_tiles(const PrefixArgs& a)
     if (tid == 0) a.tile_start[a.tiles] = before;
 }
 
-// Query row `item` (one warp) into its tile's image, rows 0..63 the high terms
-// and 64..127 the low ones; its logit scale and the prefix positions it sees.
-__device__ void prepare_query(const PrefixArgs& a, int64_t item)
+// Query row `item`, eight columns (lane + 32 i) 8 .. + 7 per lane and i, and the
+// largest magnitude in it.  The whole warp.
+constexpr int kQueryVec = (kWidth / 8 + 31) / 32;
+__device__ __forceinline__ float load_query(const PrefixArgs& a, int64_t item, int lane,
+                                            uint4 (&v)[kQueryVec])
 {
-    const int lane = threadIdx.x & 31;
-    if (item >= (int64_t)a.tiles * kRows) return;
-    const bool on = item < a.rows;
-    constexpr int kGroups = kWidth / 8;   // 8-column groups
-    constexpr int kVec = (kGroups + 31) / 32;
-    uint4 v[kVec];
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < kQueryVec; ++i) {
         const int c = (lane + 32 * i) * 8;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (on && c < kWidth)
+        if (item < a.rows && c < kWidth)
             v[i] = c < kDv ? __ldg(reinterpret_cast<const uint4*>(a.q_lat + item * kDv + c))
                            : __ldg(reinterpret_cast<const uint4*>(a.q_pe + item * kDr + (c - kDv)));
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -289,24 +291,43 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    return amax;
+}
+
+// Query row `item` (one warp) into its tile's image, rows 0..63 the high terms
+// and 64..127 the low ones; its logit scale and the positions it sees, with the
+// sign bit set if the row wants its third term.
+__device__ void prepare_query(const PrefixArgs& a, int64_t item)
+{
+    const int lane = threadIdx.x & 31;
+    if (item >= (int64_t)a.tiles * kRows) return;
+    const bool on = item < a.rows;
+    uint4 v[kQueryVec];
+    const float amax = load_query(a, item, lane, v);
     const int sh = q_shift(amax);
     uint8_t* image = a.q_image + item / kRows * kPrefixImage;
     const int row = (int)(item % kRows);
+    float left = 0.f;   // sum of what the two terms leave of the (scaled) elements
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < kQueryVec; ++i) {
         const int c = (lane + 32 * i) * 8;
         if (c >= kWidth) continue;
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         uint16_t h[4], l[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            split_pair<kQLoBits>(mul_pow2(__uint_as_float(w[k] << 16), sh),
-                                 mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh), h[k], l[k]);
+        for (int k = 0; k < 4; ++k) {
+            const float x0 = mul_pow2(__uint_as_float(w[k] << 16), sh);
+            const float x1 = mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh);
+            const float2 t = split_pair<kQLoBits>(x0, x1, h[k], l[k]);
+            left += fabsf(x0 - t.x) + fabsf(x1 - t.y);
+        }
         *reinterpret_cast<uint2*>(image + tile_offset(row, c, kKeys)) =
             make_uint2((uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16));
         *reinterpret_cast<uint2*>(image + tile_offset(kRows + row, c, kKeys)) =
             make_uint2((uint32_t)l[0] | ((uint32_t)l[1] << 16), (uint32_t)l[2] | ((uint32_t)l[3] << 16));
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) left += __shfl_xor_sync(0xffffffffu, left, off);
     if (lane == 0) {
         // (rows past the batch's last see everything: a mask would cost every block)
         int64_t win = INT32_MAX;
@@ -321,8 +342,10 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
             win = min(win, a.joined ? (int64_t)INT32_MAX : P);
         }
         // (an infinite query has no finite terms: its logits are NaN)
-        a.q_scale[item] = !on ? 0.f : isinf(amax) ? CUDART_NAN_F : mul_pow2(a.logit_scale, -sh);
-        a.q_window[item] = (int32_t)win;
+        const float cq = !on ? 0.f : isinf(amax) ? CUDART_NAN_F : mul_pow2(a.logit_scale, -sh);
+        const bool third = left * 448.f * fabsf(cq) > kThirdAbove;
+        a.q_scale[item] = cq;
+        a.q_window[item] = (int32_t)win | (third ? INT32_MIN : 0);
     }
 }
 
@@ -350,15 +373,24 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 
 // ---- prefix_split -----------------------------------------------------------------------------
 //
-// Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests, warps
-// 4-11 are two softmax sets of four warps; set s owns query rows 32 s .. 32 s + 31,
+// Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests, warps 2
+// and 3 write third terms, warps 4-11 are two softmax sets of four warps; set s owns query rows 32 s .. 32 s + 31,
 // warp w % 4 of a set the TMEM lanes (keys) 32 (w % 4) .. + 31, one key per thread,
-// as in the split kernel.  Warp 3 completes its warpgroup.
+// as in the split kernel.
 //
 // A stage's four latent chunks are released one by one, as the P.V MMAs of that
 // chunk finish, so the next block's chunks stream in behind them; the RoPE
 // chunk, which only QK reads, has one buffer.  QK of block j + 1 runs while the
 // softmax works on block j, and P.V of block j - 1 before it.
+//
+// A tile with a row that wants its third term holds those terms (64 rows, 36 KB) in
+// one of the two stages, where warps 2 and 3 write them from the queries when a run
+// starts.  All of its blocks then pass through the other stage, each chunk behind the
+// P.V of the block before, and QK has a second set of MMAs, which adds the third
+// terms to the low terms' columns of S^T.  (Measured: 64 requests of 128 heads on
+// 32768 positions 445 us without such a row, 875 with one in the batch, 960 with all
+// rows; 4 of 16 heads on 1024 20.4, 25.7 and 45.5.  Nothing else held those 36 KB:
+// shared memory is full, and the workspace's layout is the plan's.)
 
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kTileWarp = 2, kSoftmaxWarp0 = 4;
@@ -383,10 +415,11 @@ constexpr int kOffMisc = kOffP + 2 * kPTerm;
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
 static_assert(kRows * kDv * 4 <= kOffRope, "the epilogue stages its rows in the idle stages");
+static_assert(kRows * kWidth <= 4 * kChunk, "the third terms fit in a stage");
 
 struct PrefixShared {
     uint64_t k_full[2][4], k_empty[2][4];   // per stage and chunk
-    uint64_t r_full, r_empty, q_full;
+    uint64_t r_full, r_empty, q_full, q3_full;
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done;
     uint64_t mma_drain;   // after an abort: every MMA issued has completed
@@ -476,6 +509,30 @@ struct Walk {
     }
 };
 
+// Two of the tile's rows per lane, negative if one wants its third term, and whether
+// any of the tile's does.  The whole warp.
+__device__ __forceinline__ int32_t third_flags(const PrefixArgs& a, const Run& r, int lane)
+{
+    const int32_t* w = a.q_window + r.tile * kRows + lane;
+    return __ldcg(w) | __ldcg(w + 32);
+}
+__device__ __forceinline__ bool any_third(int32_t flags)
+{
+    return __any_sync(0xffffffffu, flags < 0);
+}
+
+// The stage that holds block jj of the run.
+__device__ __forceinline__ int stage_of(const Run& r, int64_t jj, bool third)
+{
+    return (int)((third ? r.j0 : jj) & 1);
+}
+
+// Where a run keeps its tile's third terms.
+__device__ __forceinline__ uint32_t third_offset(const Run& r)
+{
+    return (uint32_t)((r.j0 + 1) & 1) * (4 * kChunk);
+}
+
 // Warp 2: the run's tile's requests into shared memory.
 __device__ __forceinline__ void tile_role(const PrefixArgs& a, PrefixShared& ms, const Run& r,
                                           int lane)
@@ -512,6 +569,8 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
     Walk walk(r);
     bool looked = false;   // the tile's requests are known
     int64_t issued = 0, ropes = 0;   // latent chunks and RoPE chunks of this run
+    const int32_t flags = third_flags(a, r, lane);   // (the first block goes to one stage either way)
+    bool third = false;
     if (lane == 0) {
         mbar_arrive_expect_tx(&ms.q_full, (uint32_t)kPrefixImage);
         bulk_load(smem + kOffQ, a.q_image + r.tile * kPrefixImage, (uint32_t)kPrefixImage,
@@ -521,6 +580,9 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
     for (int j = 0; j < n && ok; ++j) {
         const int64_t jj = r.j0 + j;
         const int st = (int)(jj & 1);
+        if (j == 1) third = any_third(flags);
+        const int mem = stage_of(r, jj, third);
+        const int64_t before = jj - (third ? 1 : 2);   // the block that was there
         if (!looked && walk.own(r)) {
             ok = looked = warp_wait(&ms.own_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
             if (!ok) break;
@@ -528,13 +590,13 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
         const uint8_t* src = a.k_image + walk.image(r, ms) * kPrefixImage;
         walk.next(r);
         for (int c = 0; c < 4 && ok; ++c) {
-            if (jj >= 2)
-                ok = warp_wait(&ms.k_empty[st][c], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
-                               a.wait_limit);
+            if (before >= 0)
+                ok = warp_wait(&ms.k_empty[before & 1][c], (uint32_t)(before >> 1) & 1, abort_flag,
+                               0, a.wait_limit);
             if (!ok) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&ms.k_full[st][c], kChunk);
-                bulk_load(smem + st * 4 * kChunk + c * kChunk, src + c * kChunk, kChunk,
+                bulk_load(smem + mem * 4 * kChunk + c * kChunk, src + c * kChunk, kChunk,
                           &ms.k_full[st][c]);
             }
             ++issued;
@@ -559,6 +621,18 @@ __device__ __forceinline__ void load_role(const PrefixArgs& a, uint8_t* smem, Pr
     }
     if (ropes > 0) warp_wait(&ms.r_full, (uint32_t)(r.j0 + ropes - 1) & 1, &drain);
     warp_wait(&ms.q_full, (uint32_t)r.run & 1, &drain);
+}
+
+// After an abort, MMAs already issued may still be running: wait for them (with the
+// full bound) before the CTA releases TMEM and its stages.  The MMA warp.
+__device__ __forceinline__ void drain_after_abort(PrefixShared& ms)
+{
+    if (__shfl_sync(0xffffffffu, *static_cast<volatile int*>(&ms.abort) != 0 ? 1 : 0, 0) != 0) {
+        umma_commit_warp(&ms.mma_drain);
+        volatile int drain = 0;
+        warp_wait(&ms.mma_drain, 0, &drain);
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base, uint32_t tmem,
@@ -651,14 +725,132 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
             }
         }
     }
-    // After an abort, MMAs already issued may still be running: wait for them
-    // (with the full bound) before the CTA releases TMEM and its stages.
-    if (__shfl_sync(0xffffffffu, *abort_flag != 0 ? 1 : 0, 0) != 0) {
-        umma_commit_warp(&ms.mma_drain);
-        volatile int drain = 0;
-        warp_wait(&ms.mma_drain, 0, &drain);
+    drain_after_abort(ms);
+}
+
+// The same for a tile with third terms: all blocks in one stage, so each in turn, QK
+// (with the third terms' MMAs) and then P.V.  A loop of its own: one loop for both ways
+// took 8 % longer a block of the ordinary one, and so did a second loop unrolled like
+// it (the compiler's registers for both).
+__device__ __forceinline__ void mma_role_third(const PrefixArgs& a, uint32_t smem_base,
+                                               uint32_t tmem, PrefixShared& ms, const Run& r)
+{
+    volatile int* abort_flag = &ms.abort;
+    const int n = r.x1 - r.x0;
+    constexpr uint32_t id_qk = idesc_e4m3(128, 2 * kRows, false, false);
+    constexpr uint32_t id_q3 = idesc_e4m3(128, kRows, false, false, true);
+    constexpr uint32_t id_hi = idesc_e4m3(128, kRows, true, true);
+    constexpr uint32_t id_lo = idesc_e4m3(128, kRows, true, true, true);
+    const uint32_t stage = smem_base + (uint32_t)(r.j0 & 1) * (4 * kChunk);
+    const uint32_t q3 = smem_base + third_offset(r);
+    bool ok = warp_wait(&ms.q_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit) &&
+              warp_wait(&ms.q3_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+#pragma unroll 1
+    for (int j = 0; j < n && ok; ++j) {
+        const int64_t jj = r.j0 + j;
+        const int st = (int)(jj & 1);
+        const uint32_t ph = (uint32_t)(jj >> 1) & 1;
+        const uint32_t s = tmem + kColS + st * 2 * kRows;
+        ok = jj < 2 || warp_wait(&ms.s_free[st], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
+                                 a.wait_limit);
+#pragma unroll 1
+        for (int c = 0; c < 4 && ok; ++c) {
+            ok = warp_wait(&ms.k_full[st][c], ph, abort_flag, 0, a.wait_limit);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t k = smem_desc(stage + c * kChunk + kk * 32, 16, 1024, kSw128);
+                umma_f8_warp(s, k, smem_desc(smem_base + kOffQ + c * kChunk + kk * 32, 16, 1024, kSw128),
+                             id_qk, (c > 0 || kk > 0) ? 1u : 0u);
+                umma_f8_warp(s + kRows, k,
+                             smem_desc(q3 + c * (kRows * 128) + kk * 32, 16, 1024, kSw128), id_q3, 1u);
+            }
+        }
+        ok = ok && warp_wait(&ms.r_full, (uint32_t)jj & 1, abort_flag, 0, a.wait_limit);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const uint64_t k = smem_desc(smem_base + kOffRope + kk * 32, 16, 512, kSw64);
+            umma_f8_warp(s, k, smem_desc(smem_base + kOffQ + 4 * kChunk + kk * 32, 16, 512, kSw64),
+                         id_qk, 1u);
+            umma_f8_warp(s + kRows, k, smem_desc(q3 + kRows * kDv + kk * 32, 16, 512, kSw64), id_q3, 1u);
+        }
+        umma_commit_warp(&ms.s_full[st]);
+        umma_commit_warp(&ms.r_empty);
+        ok = warp_wait(&ms.p_full, (uint32_t)jj & 1, abort_flag, 0, a.wait_limit);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t v = smem_desc(stage + c * kChunk + kk * 4096, kChunk, 1024, kSw128);
+                const uint32_t p = smem_base + kOffP + kk * 512, d = tmem + kColO + c * kRows;
+                umma_f8_warp(d, v, smem_desc(p, 128, 2048, kSwNone), id_hi,
+                             (j > 0 || kk > 0) ? 1u : 0u);
+                umma_f8_warp(d, v, smem_desc(p + kPTerm, 128, 2048, kSwNone), id_lo, 1u);
+            }
+            umma_commit_warp(&ms.k_empty[st][c]);
+        }
+        umma_commit_warp(&ms.pv_done);
     }
-    __syncwarp();
+    drain_after_abort(ms);
+}
+
+// Row `item`'s third terms into row `row` of the 64 at `tile`: what split_pair leaves
+// of q_lo, in q_lo's units.  One warp.
+__device__ __forceinline__ void third_terms(const PrefixArgs& a, int64_t item, int row, int lane,
+                                            uint8_t* tile)
+{
+    uint4 v[kQueryVec];
+    const int sh = q_shift(load_query(a, item, lane, v));
+#pragma unroll
+    for (int i = 0; i < kQueryVec; ++i) {
+        const int c = (lane + 32 * i) * 8;
+        if (c >= kWidth) continue;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint16_t t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x0 = mul_pow2(__uint_as_float(w[k] << 16), sh);
+            const float x1 = mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh);
+            uint16_t h, l;
+            const float2 p = split_pair<kQLoBits>(x0, x1, h, l);
+            t[k] = f32x2_to_e5m2x2((x0 - p.x) * (1 << kQLoBits), (x1 - p.y) * (1 << kQLoBits));
+        }
+        *reinterpret_cast<uint2*>(tile + tile_offset(row, c, kRows)) =
+            make_uint2((uint32_t)t[0] | ((uint32_t)t[1] << 16), (uint32_t)t[2] | ((uint32_t)t[3] << 16));
+    }
+}
+
+// Warps 2 and 3: the third terms of a tile that wants them, 32 rows each, zeros for
+// the rows that do not (so a row's result does not depend on its tile's others); warp
+// 2 looks up the tile's requests first.
+__device__ __forceinline__ void third_role(const PrefixArgs& a, uint8_t* smem, PrefixShared& ms,
+                                           const Run& r, int warp, int lane)
+{
+    const int row0 = (warp - kTileWarp) * 32;
+    const int32_t flags = third_flags(a, r, lane);
+    const uint32_t mine = __ballot_sync(0xffffffffu, __ldcg(a.q_window + r.tile * kRows + row0 + lane) < 0);
+    if (warp == kTileWarp) tile_role(a, ms, r, lane);
+    if (any_third(flags)) {
+        uint8_t* tile = smem + third_offset(r);
+#pragma unroll 1
+        for (int k = 0; k < 32; ++k) {
+            const int row = row0 + k;
+            if ((mine >> k) & 1u) {
+                third_terms(a, r.tile * kRows + row, row, lane, tile);
+            } else {
+                for (int c = lane * 16; c < kWidth; c += 512)
+                    *reinterpret_cast<uint4*>(tile + tile_offset(row, c, kRows)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    }
+    if (lane == 0) mbar_arrive(&ms.q3_full);
 }
 
 __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem, uint32_t tmem,
@@ -679,7 +871,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
     // the rows' logit scales and windows (every set its own rows)
     if (ti < R) {
         ms.cq[r0 + ti] = __ldcg(a.q_scale + r.tile * kRows + r0 + ti);
-        ms.win[r0 + ti] = __ldcg(a.q_window + r.tile * kRows + r0 + ti);
+        ms.win[r0 + ti] = __ldcg(a.q_window + r.tile * kRows + r0 + ti) & INT32_MAX;
     }
     softmax_bar(bar_id);
     int win_min = ms.win[r0 + lane];
@@ -991,6 +1183,7 @@ prefix_split_kernel(const PrefixArgs a)
         mbar_init(&ms.r_full, 1);
         mbar_init(&ms.r_empty, 1);
         mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.q3_full, 2);
         mbar_init(&ms.p_full, kSoftmaxWarps);
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.mma_drain, 1);
@@ -1076,8 +1269,10 @@ prefix_split_kernel(const PrefixArgs a)
         regs_lower<kRegsLow>();
         while (next_run()) {
             if (warp == kLoadWarp) load_role(a, smem, ms, r, lane);
+            else if (warp == kMmaWarp && any_third(third_flags(a, r, lane)))
+                mma_role_third(a, smem_base, tmem, ms, r);
             else if (warp == kMmaWarp) mma_role(a, smem_base, tmem, ms, r);
-            else if (warp == kTileWarp) tile_role(a, ms, r, lane);
+            else third_role(a, smem, ms, r, warp, lane);
             tc_fence_before();
             const bool stop = __syncthreads_or(ms.abort);
             tc_fence_after();

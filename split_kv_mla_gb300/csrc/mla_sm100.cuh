@@ -450,6 +450,14 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi)
     return r;
 }
 
+// The same to e5m2x2 (saturating to +-57344).
+__device__ __forceinline__ uint16_t f32x2_to_e5m2x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Packed e4m3x2 -> two fp32 (exact), with integer and fp32-multiply ops only
 // (no conversion-pipe instructions).  An e4m3fn byte is 1 sign, 4 exponent
 // (bias 7) and 3 mantissa bits; placing its 7 magnitude bits at fp32 bits 20..26

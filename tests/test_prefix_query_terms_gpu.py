@@ -84,6 +84,11 @@ def test_tiles_with_and_without_a_third_term_in_one_cta(ctas, splits):
             same = same.cuda()
             assert torch.equal(o.view(576, 512)[same], o2.view(576, 512)[same])
             assert torch.equal(lse.view(-1)[same], lse2.view(-1)[same])
+            if joined:   # nor do such a tile's other rows change
+                same = torch.ones(576, dtype=torch.bool, device="cuda")
+                same[[r * 24 + h for r, h in rows]] = False
+                assert torch.equal(o.view(576, 512)[same], o2.view(576, 512)[same])
+                assert torch.equal(lse.view(-1)[same], lse2.view(-1)[same])
 
 
 def test_repeat_and_long_runs():

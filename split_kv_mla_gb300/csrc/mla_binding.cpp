@@ -150,11 +150,7 @@ bool truth(PyObject* o)
     return v != 0;
 }
 
-void* stream_of(PyObject* o, int dev)
-{
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
-    return reinterpret_cast<void*>(static_cast<uintptr_t>(integer(o)));
-}
+void* current_stream(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
 // The status of a C call as an exception, if it is one.
 void check(int status, const char* where)
@@ -222,10 +218,10 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n)
 }
 
 // prefix_decode(plan address, q_lat, q_pe, pool, prefix_indices, seq_lens, kv_indices,
-// kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace, stream, return_lse)
+// kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace, return_lse)
 PyObject* prefix_decode(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
-    return guarded(n, 16, [&]() -> PyObject* {
+    return guarded(n, 15, [&]() -> PyObject* {
         const auto* plan = reinterpret_cast<const mla_prefix_plan_t*>(integer(v[0]));
         const at::Tensor& q_lat = given(v[1], "q_lat");
         const at::Tensor& q_pe = given(v[2], "q_pe");
@@ -253,7 +249,7 @@ PyObject* prefix_decode(PyObject*, PyObject* const* v, Py_ssize_t n)
         if (!o.defined()) o = allocate({R, H, 512}, at::kBFloat16, dev);
         else if (o.sizes() != q_lat.sizes()) bad("o must have q_lat's shape");
         if (lse.defined() ? lse.numel() != R * H : false) bad("lse must be [B * q_len, H]");
-        if (!lse.defined() && truth(v[15])) lse = allocate({R, H}, at::kFloat, dev);
+        if (!lse.defined() && truth(v[14])) lse = allocate({R, H}, at::kFloat, dev);
         const void* q0 = address(q_lat, "q_lat", at::kBFloat16, dev);
         const void* q1 = address(q_pe, "q_pe", at::kBFloat16, dev);
         const int32_t* pi = table(prefix, "prefix_indices", dev);
@@ -265,7 +261,7 @@ PyObject* prefix_decode(PyObject*, PyObject* const* v, Py_ssize_t n)
         float* pz = static_cast<float*>(address(lse, "lse", at::kFloat, dev));
         void* pw = address(ws, "workspace", at::kByte, dev);
         const float scale = real(v[8]), kv_scale = real(v[9]);
-        void* stream = stream_of(v[14], dev);
+        void* stream = current_stream(dev);
         const int b = size32(batch), ql = size32(q_len), h = size32(H);
         int status;
         Py_BEGIN_ALLOW_THREADS
@@ -278,10 +274,10 @@ PyObject* prefix_decode(PyObject*, PyObject* const* v, Py_ssize_t n)
 }
 
 // cache_append(kv, slots, pool, positions, cos_sin, kv_scale, q, kv_weight, kv_norm_cols,
-// q_weight, q_norm, eps, half_split, q_nope, q_pe, workspace, stream)
+// q_weight, q_norm, eps, half_split, q_nope, q_pe, workspace)
 PyObject* cache_append(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
-    return guarded(n, 17, [&]() -> PyObject* {
+    return guarded(n, 16, [&]() -> PyObject* {
         const at::Tensor& kv = tensor(v[0], "kv");
         const at::Tensor& slots = tensor(v[1], "slots");
         const at::Tensor& pool = tensor(v[2], "pool");
@@ -334,7 +330,7 @@ PyObject* cache_append(PyObject*, PyObject* const* v, Py_ssize_t n)
         void* pw = address(ws, "workspace", at::kByte, dev);
         const float kv_scale = real(v[5]), eps = real(v[11]);
         const int q_norm = truth(v[10]) ? 1 : 0, half = truth(v[12]) ? 1 : 0;
-        void* stream = stream_of(v[16], dev);
+        void* stream = current_stream(dev);
         const void* kvp = kv.defined() ? kv.data_ptr() : nullptr;
         void* pool_p = kv.defined() ? pool.data_ptr() : nullptr;
         const void* qd = q.defined() ? q.data_ptr() : nullptr;
@@ -354,10 +350,10 @@ PyObject* cache_append(PyObject*, PyObject* const* v, Py_ssize_t n)
 }
 
 // cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, total, fresh,
-// fresh_indptr, table, workspace, stream)
+// fresh_indptr, table, workspace)
 PyObject* cache_fork(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
-    return guarded(n, 12, [&]() -> PyObject* {
+    return guarded(n, 11, [&]() -> PyObject* {
         const at::Tensor& pool = given(v[0], "pool");
         const at::Tensor& indices = given(v[1], "kv_indices");
         const at::Tensor& indptr = given(v[2], "kv_indptr");
@@ -385,7 +381,7 @@ PyObject* cache_fork(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int32_t* fi = table(fresh_indptr, "fresh_indptr", dev);
         int32_t* to = static_cast<int32_t*>(address(out, "table", at::kInt, dev));
         void* pw = address(ws, "workspace", at::kByte, dev);
-        void* stream = stream_of(v[11], dev);
+        void* stream = current_stream(dev);
         const int w = size32(pool.size(-1)), f = size32(F);
         const int np = size32(indptr.numel() > 0 ? indptr.numel() - 1 : 0);
         int status;
@@ -398,10 +394,10 @@ PyObject* cache_fork(PyObject*, PyObject* const* v, Py_ssize_t n)
     });
 }
 
-// cache_compact(pool, kv_indices, new_indices, live, workspace, stream)
+// cache_compact(pool, kv_indices, new_indices, live, workspace)
 PyObject* cache_compact(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
-    return guarded(n, 6, [&]() -> PyObject* {
+    return guarded(n, 5, [&]() -> PyObject* {
         const at::Tensor& pool = given(v[0], "pool");
         const at::Tensor& indices = given(v[1], "kv_indices");
         at::Tensor out = tensor(v[2], "new_indices"), live = tensor(v[3], "live");
@@ -416,7 +412,7 @@ PyObject* cache_compact(PyObject*, PyObject* const* v, Py_ssize_t n)
         int32_t* to = static_cast<int32_t*>(address(out, "new_indices", at::kInt, dev));
         int32_t* pl = static_cast<int32_t*>(address(live, "live", at::kInt, dev));
         void* pw = address(ws, "workspace", at::kByte, dev);
-        void* stream = stream_of(v[5], dev);
+        void* stream = current_stream(dev);
         const int w = size32(pool.size(-1));
         int status;
         Py_BEGIN_ALLOW_THREADS

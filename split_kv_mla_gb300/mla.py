@@ -5,11 +5,14 @@ through an extension module (``csrc/mla_binding.cpp``).
 Every function has the name of the C entry point it calls (``mla_decode_plan``,
 ``mla_decode``, ``mla_sparse_decode``, ``mla_splitk_reduce`` ...).  Tensors are
 PyTorch CUDA tensors: PyTorch owns device memory and streams, the library does
-all of the work.  There is no fallback: if ``libmla.so`` is missing or a tensor
+all of the work.  ``stream`` (a torch stream or a raw handle, None: the current
+one) means what ``torch.cuda.stream(stream)`` around the call means: outputs and a
+workspace that the call allocates belong to that stream.  There is no fallback: if ``libmla.so`` is missing or a tensor
 is not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -183,6 +186,29 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream) -> torch.cuda.Stream:
+    """The torch stream of a ``stream`` argument, a torch stream or a raw handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_ptr(stream)
+        # 0 and 1 are the runtime's names of the default stream
+        stream = (torch.cuda.ExternalStream(handle) if handle > 1
+                  else torch.cuda.default_stream())
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream is on {stream.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Context in which a call allocates and zeroes what its caller did not give: on
+    ``stream``, as under torch.cuda.stream.  Memory of the current stream might still
+    be in use there, and would go back to it while ``stream``'s kernels run."""
+    return _HERE if stream is None else torch.cuda.stream(_torch_stream(stream))
+
+
 def sm_count(device=None) -> int:
     return torch.cuda.get_device_properties(device or torch.cuda.current_device()).multi_processor_count
 
@@ -221,9 +247,21 @@ def mla_wave_fill_splits(batch, keys_per_request, heads, sm_count, bm, page,
 
 
 def workspace(plan: mla_plan_t, device=None) -> torch.Tensor:
-    """A zeroed workspace of plan.workspace_bytes (256-byte aligned by the allocator)."""
-    n = max(int(plan.workspace_bytes), MLA_WORKSPACE_HEADER_BYTES)
-    ws = torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    """A workspace of plan.workspace_bytes with a zeroed header (256-byte aligned by the
+    allocator; the rest is scratch)."""
+    return _workspace(int(plan.workspace_bytes), device)
+
+
+_ZEROED_WHOLE = 4 << 20   # bytes up to which one fill takes less than a view and its fill
+
+
+def _workspace(n: int, device=None) -> torch.Tensor:
+    n = max(n, MLA_WORKSPACE_HEADER_BYTES)
+    if n <= _ZEROED_WHOLE:
+        ws = torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    else:
+        ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        ws[:MLA_WORKSPACE_HEADER_BYTES].zero_()
     assert ws.data_ptr() % 256 == 0
     return ws
 
@@ -241,12 +279,13 @@ def mla_decode(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices, kv_ind
     R, H = q_lat.shape[0], q_lat.shape[1]
     batch = seq_lens.shape[0]
     q_len = R // batch if batch else 1
-    if o_lat is None:
-        o_lat = torch.empty_like(q_lat)
-    if lse is None and return_lse:
-        lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
-    if workspace_t is None:
-        workspace_t = workspace(plan, q_lat.device)
+    with _on(stream):
+        if o_lat is None:
+            o_lat = torch.empty_like(q_lat)
+        if lse is None and return_lse:
+            lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
+        if workspace_t is None:
+            workspace_t = workspace(plan, q_lat.device)
     pool_u8 = pool.view(torch.uint8) if pool.dtype != torch.uint8 else pool
     rc = getattr(load(), _entry)(
         ctypes.byref(plan), _dev_ptr(q_lat, "q_lat", torch.bfloat16),
@@ -284,14 +323,16 @@ def mla_decode_dcp(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices, kv
     R, H = q_lat.shape[0], q_lat.shape[1]
     batch = seq_lens.shape[0]
     q_len = R // batch if batch else 1
-    if o is None:
-        o = torch.empty(q_lat.shape, dtype=out_dtype, device=q_lat.device)
+    with _on(stream):
+        if o is None:
+            o = torch.empty(q_lat.shape, dtype=out_dtype, device=q_lat.device)
     if o.dtype not in _DTYPE_CODE:
         raise ValueError("o must be bf16 or fp32")
-    if lse is None:
-        lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
-    if workspace_t is None:
-        workspace_t = workspace(plan, q_lat.device)
+    with _on(stream):
+        if lse is None:
+            lse = torch.empty(R, H, dtype=torch.float32, device=q_lat.device)
+        if workspace_t is None:
+            workspace_t = workspace(plan, q_lat.device)
     pool_u8 = pool.view(torch.uint8) if pool.dtype != torch.uint8 else pool
     rc = getattr(load(), _entry)(
         ctypes.byref(plan), _dev_ptr(q_lat, "q_lat", torch.bfloat16),
@@ -324,10 +365,11 @@ def mla_dcp_lse_merge_ranks(parts_in, lse_in, out=None, lse_out=None, stream=Non
     rows = lse_in[0].numel()
     if parts_in[0].numel() != rows * d_v:
         raise ValueError("parts_in and lse_in disagree on the rows")
-    if out is None:
-        out = torch.empty(rows_shape + (d_v,), dtype=torch.bfloat16, device=parts_in.device)
-    if lse_out is None and return_lse:
-        lse_out = torch.empty(rows_shape, dtype=torch.float32, device=parts_in.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(rows_shape + (d_v,), dtype=torch.bfloat16, device=parts_in.device)
+        if lse_out is None and return_lse:
+            lse_out = torch.empty(rows_shape, dtype=torch.float32, device=parts_in.device)
     rc = load().mla_dcp_lse_merge_ranks(
         _dev_ptr(parts_in, "parts_in"), _DTYPE_CODE[parts_in.dtype],
         _dev_ptr(lse_in, "lse_in", torch.float32), W, rows, d_v, _dev_ptr(out, "out", torch.bfloat16), _dev_ptr(lse_out, "lse_out", torch.float32),
@@ -345,12 +387,13 @@ def mla_sparse_decode(plan: mla_plan_t, q_nope, q_pe, pool, indices, scale: floa
             raise ValueError(f"{name} must be a CUDA tensor")
     T, H = q_nope.shape[0], q_nope.shape[1]
     topk = indices.shape[1] if indices.dim() == 2 else 0
-    if o is None:
-        o = torch.empty_like(q_nope)
-    if lse is None and return_lse:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
-    if workspace_t is None:
-        workspace_t = workspace(plan, q_nope.device)
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(q_nope)
+        if lse is None and return_lse:
+            lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
+        if workspace_t is None:
+            workspace_t = workspace(plan, q_nope.device)
     pool_u8 = pool.view(torch.uint8) if pool.dtype != torch.uint8 else pool
     rc = getattr(load(), _entry)(
         ctypes.byref(plan), _dev_ptr(q_nope, "q_nope", torch.bfloat16),
@@ -376,12 +419,13 @@ def mla_sparse_decode_extra(plan: mla_plan_t, q_nope, q_pe, pool, indices, extra
     T, H = q_nope.shape[0], q_nope.shape[1]
     topk = indices.shape[1] if indices.dim() == 2 else 0
     extra_topk = extra_indices.shape[1] if extra_indices.dim() == 2 else 0
-    if o is None:
-        o = torch.empty_like(q_nope)
-    if lse is None and return_lse:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
-    if workspace_t is None:
-        workspace_t = workspace(plan, q_nope.device)
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(q_nope)
+        if lse is None and return_lse:
+            lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
+        if workspace_t is None:
+            workspace_t = workspace(plan, q_nope.device)
     pool_u8 = pool.view(torch.uint8) if pool.dtype != torch.uint8 else pool
     xpool_u8 = extra_pool.view(torch.uint8) if extra_pool.dtype != torch.uint8 else extra_pool
     rc = getattr(load(), _entry)(
@@ -427,10 +471,11 @@ def mla_splitk_reduce(o_part, lse_part, out_scale: float = 1.0, o=None, lse=None
                       stream=None, return_lse: bool = True):
     """Merge o_part fp32 [rows, ns, d_v] with lse_part fp32 [rows, ns]; returns (o, lse)."""
     rows, ns, d_v = o_part.shape
-    if o is None:
-        o = torch.empty(rows, d_v, dtype=torch.bfloat16, device=o_part.device)
-    if lse is None and return_lse:
-        lse = torch.empty(rows, dtype=torch.float32, device=o_part.device)
+    with _on(stream):
+        if o is None:
+            o = torch.empty(rows, d_v, dtype=torch.bfloat16, device=o_part.device)
+        if lse is None and return_lse:
+            lse = torch.empty(rows, dtype=torch.float32, device=o_part.device)
     rc = load().mla_splitk_reduce(
         _dev_ptr(o_part, "o_part", torch.float32), _dev_ptr(lse_part, "lse_part", torch.float32),
         rows, ns, d_v, float(out_scale), _dev_ptr(o, "o", torch.bfloat16),
@@ -457,12 +502,12 @@ def mla_debug_gather(pool, indices, workspace_t=None, stream=None):
     out-of-range index gives a zero row.  pool: uint8 [N, 576] or [N, 512]
     (a [N, 1, 576] cache is accepted); indices: int32 [n].  Returns
     (rows uint8 [n, row_bytes], workspace)."""
-    p = pool.reshape(pool.shape[0], -1)
-    row_bytes = p.shape[1]
     n = indices.numel()
-    out = torch.empty(n, row_bytes, dtype=torch.uint8, device=p.device)
-    ws = workspace_t if workspace_t is not None else torch.zeros(
-        MLA_WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=p.device)
+    with _on(stream):
+        p = pool.reshape(pool.shape[0], -1)
+        row_bytes = p.shape[1]
+        out = torch.empty(n, row_bytes, dtype=torch.uint8, device=p.device)
+        ws = workspace_t if workspace_t is not None else _workspace(0, p.device)
     _check(load().mla_debug_gather(_dev_ptr(p, "pool", torch.uint8), p.shape[0], row_bytes,
                                    _dev_ptr(indices, "indices", torch.int32), n,
                                    _dev_ptr(out, "out"), _dev_ptr(ws, "workspace"),
@@ -532,11 +577,6 @@ def _cuda_device(t: torch.Tensor) -> torch.device:
     return t.device
 
 
-def _stream_arg(stream) -> Optional[int]:
-    """None (the current stream) or a stream's handle."""
-    return None if stream is None else _stream_ptr(stream)
-
-
 # ---- decode over a shared prefix -----------------------------------------------------
 
 def mla_prefix_decode_plan(batch: int, q_len: int, num_heads: int, prefix_cap: int,
@@ -557,25 +597,29 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
     int32 [1] on the device: how many of prefix_indices are in use (None: all)."""
     if not isinstance(plan, mla_prefix_plan_t):
         raise TypeError("plan must come from mla_prefix_decode_plan")
+    if stream is not None:
+        with _on(stream):
+            return mla_prefix_decode(plan, q_lat, q_pe, pool, prefix_indices, seq_lens, kv_indices,
+                                     kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace_t,
+                                     None, return_lse)
     if workspace_t is None:
         workspace_t = workspace(plan, _cuda_device(q_lat))
     return (_binding or _native()).prefix_decode(
         ctypes.addressof(plan), q_lat, q_pe, pool, prefix_indices, seq_lens, kv_indices,
-        kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace_t, _stream_arg(stream),
-        return_lse)
+        kv_indptr, scale, kv_scale, prefix_len, o, lse, workspace_t, return_lse)
 
 
 # ---- the cache: append, fork, compact ------------------------------------------------
 
 def cache_workspace(pool_rows: int = 0, device=None) -> torch.Tensor:
-    """A zeroed workspace for mla_cache_append and mla_cache_fork, and with the
-    pool's row count for mla_cache_compact too."""
-    n = MLA_WORKSPACE_HEADER_BYTES
+    """A workspace with a zeroed header for mla_cache_append and mla_cache_fork, and
+    with the pool's row count for mla_cache_compact too."""
+    n = 0
     if pool_rows:
         n = int(load().mla_cache_compact_workspace_bytes(int(pool_rows)))
         if n == 0:
             raise ValueError(f"pool_rows {pool_rows} is not supported")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _workspace(n, device)
 
 
 def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0, q=None,
@@ -589,12 +633,17 @@ def mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale: float = 1.0,
     queries), rows contiguous, other strides free in steps of 8 elements;
     positions int32 [T]; cos_sin fp32 [max_positions, 64], 32 cosines then 32
     sines.  q_nope is None when q_cols is 64 (or without queries)."""
+    if stream is not None:
+        with _on(stream):
+            return mla_cache_append(kv, slots, pool, positions, cos_sin, kv_scale, q, kv_weight,
+                                    kv_norm_cols, q_weight, q_norm, eps, half_split, q_nope, q_pe,
+                                    workspace_t)
     if workspace_t is None:
         first = kv if kv is not None else q
         workspace_t = None if first is None else cache_workspace(device=_cuda_device(first))
     return (_binding or _native()).cache_append(
         kv, slots, pool, positions, cos_sin, kv_scale, q, kv_weight, kv_norm_cols, q_weight,
-        q_norm, eps, half_split, q_nope, q_pe, workspace_t, _stream_arg(stream))
+        q_norm, eps, half_split, q_nope, q_pe, workspace_t)
 
 
 def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, total: int, fresh,
@@ -602,11 +651,15 @@ def mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, tot
     """Page tables of requests that continue `parents`, sharing their first
     keep[f] slots and copying the other rows to fresh slots; returns the
     children's kv_indices int32 [total] (their kv_indptr is child_indptr)."""
+    if stream is not None:
+        with _on(stream):
+            return mla_cache_fork(pool, kv_indices, kv_indptr, parents, keep, child_indptr, total,
+                                  fresh, fresh_indptr, table, workspace_t)
     if workspace_t is None:
         workspace_t = cache_workspace(device=_cuda_device(pool))
     return (_binding or _native()).cache_fork(
         pool, kv_indices, kv_indptr, parents, keep, child_indptr, total, fresh, fresh_indptr,
-        table, workspace_t, _stream_arg(stream))
+        table, workspace_t)
 
 
 def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t=None,
@@ -614,7 +667,9 @@ def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t
     """Move the rows that kv_indices names to the front of the pool, in place;
     returns (new_indices, live): the rewritten table and the live row count
     int32 [1] (rows from there on are free).  new_indices may be kv_indices."""
+    if stream is not None:
+        with _on(stream):
+            return mla_cache_compact(pool, kv_indices, new_indices, live, workspace_t)
     if workspace_t is None:
         workspace_t = cache_workspace(pool.shape[0], device=_cuda_device(pool))
-    return (_binding or _native()).cache_compact(pool, kv_indices, new_indices, live, workspace_t,
-                                                 _stream_arg(stream))
+    return (_binding or _native()).cache_compact(pool, kv_indices, new_indices, live, workspace_t)

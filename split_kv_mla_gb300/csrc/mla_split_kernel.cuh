@@ -1118,11 +1118,9 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.s_free[st]);
             const bool kval = ms.kvalid[st][ti] != 0;
-            // A key with NaN codes has a NaN dot product with every row (so has every
-            // key with a NaN query: nothing is found then).  Rows that see it take a
-            // NaN weight from it; the others' weight is 0, and so V has to be
-            // finite, for them and for a later block that leaves this row in the stage.
-            if (s[0] != s[0]) clear_nan_codes(smem + C::kOffStage + st * C::kStageBytes + ti * 128);
+            // A key with NaN codes has a NaN dot product with every row (so has every key
+            // with a NaN query).  A sparse key is seen by every row of the CTA.
+            const bool nan_key = !SPARSE && s[0] != s[0];
             const int j = k0 + blk * kBlockN + ti;
             // Per-row logit scales and windows as 16-byte loads, and a
             // branch-free mask.  The draft window only bites in blocks that reach
@@ -1145,9 +1143,16 @@ split_tc_kernel(const __grid_constant__ CUtensorMap tm_lat,
                     need |= s[n] > m_ref[n] + kTau;
                 }
             }
-            if (softmax_bar_or(bar_id, !ok || *abort_flag)) {
-                alive = false;
-                break;
+            if (softmax_bar_or(bar_id, nan_key || !ok || *abort_flag)) {
+                if (SPARSE || softmax_bar_or(bar_id, !ok || *abort_flag)) {
+                    alive = false;
+                    break;
+                }
+                // Rows that see such a key take a NaN weight from it; the others' weight
+                // is 0, and so V has to be finite, for them and for a later block that
+                // leaves this row in the stage.  (Here, behind a branch that is there
+                // anyway: a branch of its own took 2 % of a call of 64 heads.)
+                if (nan_key) clear_nan_codes(smem + C::kOffStage + st * C::kStageBytes + ti * 128);
             }
             if (softmax_bar_or(bar_id, need)) {
                 // new references: block max over the 128 keys, the set's four warps

@@ -66,6 +66,9 @@ constexpr float kQLoBack = 1.f / (1 << kQLoBits);
 // The largest error of a base-2 logit that a tile's two terms may leave (by a bound
 // with every key at +-448; with random keys a thirtieth of it): half the LSE's bar.
 constexpr float kThirdAbove = 1.f / 2048.f;
+// Two terms carry a scaled bf16 element of at least 2^-7 exactly; of a smaller one
+// they leave up to 2^-15.
+constexpr float kTwoTerms = 1.f / 128.f, kTwoTermsLeave = 1.f / 32768.f;
 
 // A grid kernel launched as a programmatic dependent of its predecessor.
 template <typename... KArgs, typename... Args>
@@ -268,6 +271,19 @@ __device__ void prepare_tiles(const PrefixArgs& a)
     if (tid == 0) a.tile_start[a.tiles] = before;
 }
 
+// x * 2^k as two multiplications by powers of two (mul_pow2 with its branches taken
+// once: k is a row's).
+struct Pow2 {
+    float a, b;
+    __device__ __forceinline__ explicit Pow2(int k)
+    {
+        const int k0 = min(max(k, -126), 127);
+        a = __uint_as_float((uint32_t)(k0 + 127) << 23);
+        b = __uint_as_float((uint32_t)(k - k0 + 127) << 23);
+    }
+    __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
+};
+
 // Query row `item`, eight columns (lane + 32 i) 8 .. + 7 per lane and i, and the
 // largest magnitude in it.  The whole warp.
 constexpr int kQueryVec = (kWidth / 8 + 31) / 32;
@@ -305,9 +321,10 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
     uint4 v[kQueryVec];
     const float amax = load_query(a, item, lane, v);
     const int sh = q_shift(amax);
+    const Pow2 scale(sh);
     uint8_t* image = a.q_image + item / kRows * kPrefixImage;
     const int row = (int)(item % kRows);
-    float left = 0.f;   // sum of what the two terms leave of the (scaled) elements
+    int small = 0;   // elements that the two terms do not carry exactly
 #pragma unroll
     for (int i = 0; i < kQueryVec; ++i) {
         const int c = (lane + 32 * i) * 8;
@@ -316,18 +333,18 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
         uint16_t h[4], l[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float x0 = mul_pow2(__uint_as_float(w[k] << 16), sh);
-            const float x1 = mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh);
-            const float2 t = split_pair<kQLoBits>(x0, x1, h[k], l[k]);
-            left += fabsf(x0 - t.x) + fabsf(x1 - t.y);
+            const float x0 = scale(__uint_as_float(w[k] << 16));
+            const float x1 = scale(__uint_as_float(w[k] & 0xFFFF0000u));
+            split_pair<kQLoBits>(x0, x1, h[k], l[k]);
+            small += (x0 != 0.f && fabsf(x0) < kTwoTerms ? 1 : 0) +
+                     (x1 != 0.f && fabsf(x1) < kTwoTerms ? 1 : 0);
         }
         *reinterpret_cast<uint2*>(image + tile_offset(row, c, kKeys)) =
             make_uint2((uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16));
         *reinterpret_cast<uint2*>(image + tile_offset(kRows + row, c, kKeys)) =
             make_uint2((uint32_t)l[0] | ((uint32_t)l[1] << 16), (uint32_t)l[2] | ((uint32_t)l[3] << 16));
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) left += __shfl_xor_sync(0xffffffffu, left, off);
+    small = __reduce_add_sync(0xffffffffu, small);
     if (lane == 0) {
         // (rows past the batch's last see everything: a mask would cost every block)
         int64_t win = INT32_MAX;
@@ -343,7 +360,7 @@ __device__ void prepare_query(const PrefixArgs& a, int64_t item)
         }
         // (an infinite query has no finite terms: its logits are NaN)
         const float cq = !on ? 0.f : isinf(amax) ? CUDART_NAN_F : mul_pow2(a.logit_scale, -sh);
-        const bool third = left * 448.f * fabsf(cq) > kThirdAbove;
+        const bool third = (float)small * (kTwoTermsLeave * 448.f) * fabsf(cq) > kThirdAbove;
         a.q_scale[item] = cq;
         a.q_window[item] = (int32_t)win | (third ? INT32_MIN : 0);
     }
@@ -386,19 +403,22 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 // A tile with a row that wants its third term holds those terms (64 rows, 36 KB) in
 // one of the two stages, where warps 2 and 3 write them from the queries when a run
 // starts.  All of its blocks then pass through the other stage, each chunk behind the
-// P.V of the block before, and QK has a second set of MMAs, which adds the third
-// terms to the low terms' columns of S^T.  (Measured: 64 requests of 128 heads on
-// 32768 positions 445 us without such a row, 875 with one in the batch, 960 with all
-// rows; 4 of 16 heads on 1024 20.4, 25.7 and 45.5.  Nothing else held those 36 KB:
-// shared memory is full, and the workspace's layout is the plan's.)
+// P.V of the block before, and QK makes a second pass over the block, which adds the
+// third terms to the low terms' columns of S^T.  (Measured: 64 requests of 128 heads
+// on 32768 positions 464 us without such a row, 757 with one in the batch, 836 with
+// all rows; 4 of 16 heads on 1024 19.0, 23.4 and 38.6.  Nothing else held those 36
+// KB: shared memory is full, and the workspace's layout is the plan's.  A loop of its
+// own for such tiles slowed the others: the roles' loops together just fill the
+// instruction cache, 82 % of whose requests hit without that code, 70 % with it.)
 
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kTileWarp = 2, kSoftmaxWarp0 = 4;
 constexpr int kSets = 2, kSetRows = kRows / kSets;
 constexpr int kSoftmaxWarps = 4 * kSets;
 // 168 registers a thread at launch (384 x 168 <= 65536); the first warpgroup
-// gives back what the softmax warpgroups take.
-constexpr uint32_t kRegsLow = 56, kRegsHigh = 224;
+// gives back what the softmax warpgroups take.  (With 56 and 224 the MMA role's
+// descriptors spilled: 528 us instead of 463 at 64 requests of 128 heads.)
+constexpr uint32_t kRegsLow = 72, kRegsHigh = 216;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split");
 
 // Softmax constants, in base-2 logit units: a row's reference moves when a
@@ -415,7 +435,7 @@ constexpr int kOffMisc = kOffP + 2 * kPTerm;
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
 static_assert(kRows * kDv * 4 <= kOffRope, "the epilogue stages its rows in the idle stages");
-static_assert(kRows * kWidth <= 4 * kChunk, "the third terms fit in a stage");
+static_assert(2 * kRows * 128 <= kChunk && kRows * 64 <= kRows * 128, "the third terms fit in a stage");
 
 struct PrefixShared {
     uint64_t k_full[2][4], k_empty[2][4];   // per stage and chunk
@@ -527,7 +547,15 @@ __device__ __forceinline__ int stage_of(const Run& r, int64_t jj, bool third)
     return (int)((third ? r.j0 : jj) & 1);
 }
 
-// Where a run keeps its tile's third terms.
+// Where a run keeps its tile's third terms: their chunks as far apart as those of the
+// other terms (so that QK's second pass differs from its first in a base address), the
+// RoPE chunk in the first gap.
+constexpr int kThirdRope = kRows * 128;
+__device__ __forceinline__ int third_at(int row, int c)
+{
+    const int at = tile_offset(row, c, kRows);
+    return c < kDv ? at + c / 128 * (kChunk - kRows * 128) : at - 4 * kRows * 128 + kThirdRope;
+}
 __device__ __forceinline__ uint32_t third_offset(const Run& r)
 {
     return (uint32_t)((r.j0 + 1) & 1) * (4 * kChunk);
@@ -653,7 +681,11 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
     auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __shfl_sync(0xffffffffu, mbar_try_wait(bar, parity) ? 1 : 0, 0) != 0;
     };
+    // the third terms: a second pass of QK, into the low terms' columns
+    constexpr uint32_t id_q3 = idesc_e4m3(128, kRows, false, false, true);
+    const bool third = any_third(third_flags(a, r, threadIdx.x & 31));
     bool ok = warp_wait(&ms.q_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
+    if (third && ok) ok = warp_wait(&ms.q3_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
     int next_qk = 0, next_pv = 0;
     long long t_last = clock64();
     for (uint32_t idle = 0; ok && next_pv < n;) {
@@ -662,7 +694,7 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
         if (next_pv < next_qk && ready(&ms.p_full, (uint32_t)jp & 1)) {
             tc_fence_after();
             const int st = (int)(jp & 1);
-            const uint64_t v0 = v_lat + (uint64_t)((st * 4 * kChunk) >> 4);
+            const uint64_t v0 = v_lat + (uint64_t)((stage_of(r, jp, third) * 4 * kChunk) >> 4);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -685,26 +717,36 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
             if (ready(&ms.k_full[st][0], ph) &&
                 (jq < 2 || ready(&ms.s_free[st], (uint32_t)((jq - 2) >> 1) & 1))) {
                 tc_fence_after();
-                const uint64_t soff = (uint64_t)((st * 4 * kChunk) >> 4);
-                const uint32_t d = tmem + kColS + st * 2 * kRows;
+                const uint64_t k0 = k_lat + (uint64_t)((stage_of(r, jq, third) * 4 * kChunk) >> 4);
+                uint64_t q0 = q_lat, q1 = q_rope;
+                uint32_t id = id_qk, d = tmem + kColS + st * 2 * kRows;
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c > 0 && ok)
-                        ok = warp_wait(&ms.k_full[st][c], ph, abort_flag, 0, a.wait_limit);
-                    if (ok) {
+                    for (int c = 0; c < 4; ++c) {
+                        if (c > 0 && ok)
+                            ok = warp_wait(&ms.k_full[st][c], ph, abort_flag, 0, a.wait_limit);
+                        if (ok) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f8_warp(d, k_lat + soff + (uint64_t)((c * kChunk + kk * 32) >> 4),
-                                         q_lat + (uint64_t)((c * kChunk + kk * 32) >> 4), id_qk,
-                                         (c > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_f8_warp(d, k0 + (uint64_t)((c * kChunk + kk * 32) >> 4),
+                                             q0 + (uint64_t)((c * kChunk + kk * 32) >> 4), id,
+                                             (c > 0 || kk > 0) ? 1u : (uint32_t)pass);
+                        }
                     }
-                }
-                if (ok) ok = warp_wait(&ms.r_full, (uint32_t)jq & 1, abort_flag, 0, a.wait_limit);
-                if (!ok) break;
+                    if (ok) ok = warp_wait(&ms.r_full, (uint32_t)jq & 1, abort_flag, 0, a.wait_limit);
+                    if (!ok) break;
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    umma_f8_warp(d, k_rope + (uint64_t)((kk * 32) >> 4),
-                                 q_rope + (uint64_t)((kk * 32) >> 4), id_qk, 1u);
+                    for (int kk = 0; kk < 2; ++kk)
+                        umma_f8_warp(d, k_rope + (uint64_t)((kk * 32) >> 4),
+                                     q1 + (uint64_t)((kk * 32) >> 4), id, 1u);
+                    if (!third || pass > 0) break;
+                    q0 = smem_desc(smem_base + third_offset(r), 16, 1024, kSw128);
+                    q1 = smem_desc(smem_base + third_offset(r) + kThirdRope, 16, 512, kSw64);
+                    id = id_q3;
+                    d += kRows;
+                }
+                if (!ok) break;
                 umma_commit_warp(&ms.s_full[st]);
                 umma_commit_warp(&ms.r_empty);
                 ++next_qk;
@@ -728,84 +770,13 @@ __device__ __forceinline__ void mma_role(const PrefixArgs& a, uint32_t smem_base
     drain_after_abort(ms);
 }
 
-// The same for a tile with third terms: all blocks in one stage, so each in turn, QK
-// (with the third terms' MMAs) and then P.V.  A loop of its own: one loop for both ways
-// took 8 % longer a block of the ordinary one, and so did a second loop unrolled like
-// it (the compiler's registers for both).
-__device__ __forceinline__ void mma_role_third(const PrefixArgs& a, uint32_t smem_base,
-                                               uint32_t tmem, PrefixShared& ms, const Run& r)
-{
-    volatile int* abort_flag = &ms.abort;
-    const int n = r.x1 - r.x0;
-    constexpr uint32_t id_qk = idesc_e4m3(128, 2 * kRows, false, false);
-    constexpr uint32_t id_q3 = idesc_e4m3(128, kRows, false, false, true);
-    constexpr uint32_t id_hi = idesc_e4m3(128, kRows, true, true);
-    constexpr uint32_t id_lo = idesc_e4m3(128, kRows, true, true, true);
-    const uint32_t stage = smem_base + (uint32_t)(r.j0 & 1) * (4 * kChunk);
-    const uint32_t q3 = smem_base + third_offset(r);
-    bool ok = warp_wait(&ms.q_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit) &&
-              warp_wait(&ms.q3_full, (uint32_t)r.run & 1, abort_flag, 0, a.wait_limit);
-#pragma unroll 1
-    for (int j = 0; j < n && ok; ++j) {
-        const int64_t jj = r.j0 + j;
-        const int st = (int)(jj & 1);
-        const uint32_t ph = (uint32_t)(jj >> 1) & 1;
-        const uint32_t s = tmem + kColS + st * 2 * kRows;
-        ok = jj < 2 || warp_wait(&ms.s_free[st], (uint32_t)((jj - 2) >> 1) & 1, abort_flag, 0,
-                                 a.wait_limit);
-#pragma unroll 1
-        for (int c = 0; c < 4 && ok; ++c) {
-            ok = warp_wait(&ms.k_full[st][c], ph, abort_flag, 0, a.wait_limit);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t k = smem_desc(stage + c * kChunk + kk * 32, 16, 1024, kSw128);
-                umma_f8_warp(s, k, smem_desc(smem_base + kOffQ + c * kChunk + kk * 32, 16, 1024, kSw128),
-                             id_qk, (c > 0 || kk > 0) ? 1u : 0u);
-                umma_f8_warp(s + kRows, k,
-                             smem_desc(q3 + c * (kRows * 128) + kk * 32, 16, 1024, kSw128), id_q3, 1u);
-            }
-        }
-        ok = ok && warp_wait(&ms.r_full, (uint32_t)jj & 1, abort_flag, 0, a.wait_limit);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const uint64_t k = smem_desc(smem_base + kOffRope + kk * 32, 16, 512, kSw64);
-            umma_f8_warp(s, k, smem_desc(smem_base + kOffQ + 4 * kChunk + kk * 32, 16, 512, kSw64),
-                         id_qk, 1u);
-            umma_f8_warp(s + kRows, k, smem_desc(q3 + kRows * kDv + kk * 32, 16, 512, kSw64), id_q3, 1u);
-        }
-        umma_commit_warp(&ms.s_full[st]);
-        umma_commit_warp(&ms.r_empty);
-        ok = warp_wait(&ms.p_full, (uint32_t)jj & 1, abort_flag, 0, a.wait_limit);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t v = smem_desc(stage + c * kChunk + kk * 4096, kChunk, 1024, kSw128);
-                const uint32_t p = smem_base + kOffP + kk * 512, d = tmem + kColO + c * kRows;
-                umma_f8_warp(d, v, smem_desc(p, 128, 2048, kSwNone), id_hi,
-                             (j > 0 || kk > 0) ? 1u : 0u);
-                umma_f8_warp(d, v, smem_desc(p + kPTerm, 128, 2048, kSwNone), id_lo, 1u);
-            }
-            umma_commit_warp(&ms.k_empty[st][c]);
-        }
-        umma_commit_warp(&ms.pv_done);
-    }
-    drain_after_abort(ms);
-}
-
 // Row `item`'s third terms into row `row` of the 64 at `tile`: what split_pair leaves
 // of q_lo, in q_lo's units.  One warp.
 __device__ __forceinline__ void third_terms(const PrefixArgs& a, int64_t item, int row, int lane,
                                             uint8_t* tile)
 {
     uint4 v[kQueryVec];
-    const int sh = q_shift(load_query(a, item, lane, v));
+    const Pow2 scale(q_shift(load_query(a, item, lane, v)));
 #pragma unroll
     for (int i = 0; i < kQueryVec; ++i) {
         const int c = (lane + 32 * i) * 8;
@@ -814,13 +785,13 @@ __device__ __forceinline__ void third_terms(const PrefixArgs& a, int64_t item, i
         uint16_t t[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float x0 = mul_pow2(__uint_as_float(w[k] << 16), sh);
-            const float x1 = mul_pow2(__uint_as_float(w[k] & 0xFFFF0000u), sh);
+            const float x0 = scale(__uint_as_float(w[k] << 16));
+            const float x1 = scale(__uint_as_float(w[k] & 0xFFFF0000u));
             uint16_t h, l;
             const float2 p = split_pair<kQLoBits>(x0, x1, h, l);
             t[k] = f32x2_to_e5m2x2((x0 - p.x) * (1 << kQLoBits), (x1 - p.y) * (1 << kQLoBits));
         }
-        *reinterpret_cast<uint2*>(tile + tile_offset(row, c, kRows)) =
+        *reinterpret_cast<uint2*>(tile + third_at(row, c)) =
             make_uint2((uint32_t)t[0] | ((uint32_t)t[1] << 16), (uint32_t)t[2] | ((uint32_t)t[3] << 16));
     }
 }
@@ -844,7 +815,7 @@ __device__ __forceinline__ void third_role(const PrefixArgs& a, uint8_t* smem, P
                 third_terms(a, r.tile * kRows + row, row, lane, tile);
             } else {
                 for (int c = lane * 16; c < kWidth; c += 512)
-                    *reinterpret_cast<uint4*>(tile + tile_offset(row, c, kRows)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(tile + third_at(row, c)) = make_uint4(0, 0, 0, 0);
             }
         }
         fence_proxy_async_smem();
@@ -1269,8 +1240,6 @@ prefix_split_kernel(const PrefixArgs a)
         regs_lower<kRegsLow>();
         while (next_run()) {
             if (warp == kLoadWarp) load_role(a, smem, ms, r, lane);
-            else if (warp == kMmaWarp && any_third(third_flags(a, r, lane)))
-                mma_role_third(a, smem_base, tmem, ms, r);
             else if (warp == kMmaWarp) mma_role(a, smem_base, tmem, ms, r);
             else third_role(a, smem, ms, r, warp, lane);
             tc_fence_before();

@@ -3,6 +3,7 @@
 // the contract of every entry point.
 #include <cmath>
 #include <cstring>
+#include <numeric>
 
 #include "mla_internal.h"
 
@@ -649,6 +650,11 @@ namespace {
 constexpr double kPrefixBlockUs = 1.9;   // a 128-key block of one 64-row tile
 constexpr double kPrefixRunUs = 9.0;     // a run's start (query tile, first block) and epilogue
 constexpr double kOwnCallUs = 3.0;       // one more kernel in the call
+// A row's merge has 80 partials in flight; each one past them takes this much longer
+// (one request of 16 heads on 8192 + 8192 positions: 21.7 us at 64 parts, 21.8 at 80,
+// 22.8 at 81, 23.6 at 96, with two blocks a part, 24.6 at 128 with one).
+constexpr double kPrefixPartUs = 0.08;
+constexpr double kPrefixParts = 80.0;
 constexpr int64_t kMaxJoinedKeys = 1 << 24;
 
 struct PrefixLayout {   // byte offsets in the workspace
@@ -739,9 +745,14 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
         // sequence into equal runs, which end and start inside tiles: the first has
         // one run per CTA, the second no idle SM.
         const int64_t per = (int64_t)q_len * num_heads;
-        const double own_blocks = (double)ceil_div(ceil_div(total_keys, batch), kPrefixKeys) *
-                                  (per >= kPrefixRows ? 1.0 : (double)kPrefixRows / per);
         const int64_t own_keys = ceil_div(total_keys, batch);
+        const double own_of_one = (double)ceil_div(own_keys, kPrefixKeys);
+        // Requests in a full tile, and pairs of a tile and a request with rows in it (the
+        // pieces that the tiles' and the requests' borders cut the rows into).
+        const double full = std::fmin((double)batch,
+                                      per >= kPrefixRows ? 1.0 : (double)kPrefixRows / per);
+        const int64_t pairs = tiles + batch - 1 -
+                              (rows - 1) / (kPrefixRows / std::gcd(per, (int64_t)kPrefixRows) * per);
         const int32_t rpc = out->own.rows_per_cta;
         const double own_us =
             total_keys == 0 ? 0.0
@@ -750,14 +761,14 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
                                                         rpc).us;
         double best = 0.0;
         auto consider = [&](bool joined, int64_t splits) {
-            const double nb = (double)blocks + (joined ? own_blocks : 0.0);
+            const double nb = (double)blocks + (joined ? own_of_one * full : 0.0);
             double ctas, at_most, runs;
             if (splits > 0) {
                 ctas = (double)(tiles * splits);
                 at_most = std::ceil(nb / (double)splits);
                 runs = 1.0;
             } else {
-                const double U = nb * (double)tiles;
+                const double U = (double)blocks * tiles + (joined ? own_of_one * pairs : 0.0);
                 const int64_t most = sm_count < MLA_MAX_SPLITS ? sm_count : MLA_MAX_SPLITS;
                 ctas = U < (double)most ? U : (double)most;
                 at_most = std::ceil(U / ctas);
@@ -766,6 +777,7 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
             const double parts = splits > 0 ? (double)splits : ctas / (double)tiles + 2.0;
             const double us = at_most * kPrefixBlockUs + runs * kPrefixRunUs +
                               (double)rows * parts * kDenseDv * 8.0 / kBytesPerUs +
+                              std::fmax(0.0, parts - kPrefixParts) * kPrefixPartUs +
                               (joined ? (double)total_keys * 1152.0 / kBytesPerUs : own_us);
             if (out->ctas == 0 || us < best) {
                 best = us;
@@ -777,7 +789,10 @@ int mla_prefix_decode_plan(int32_t batch, int32_t q_len, int32_t num_heads, int6
         for (int joined = 0; joined <= (total_keys > 0 && total_keys <= kMaxJoinedKeys ? 1 : 0);
              ++joined) {
             consider(joined != 0, 0);
-            for (int64_t s = 1; s <= blocks && s <= MLA_MAX_SPLITS && s * tiles <= sm_count; ++s)
+            // (up to a part a block: measured, equal parts of a block each are 0.5 to 0.9
+            // us faster than equal runs of one)
+            const int64_t most = blocks + (joined ? (int64_t)(own_of_one * full) : 0);
+            for (int64_t s = 1; s <= most && s <= MLA_MAX_SPLITS && s * tiles <= sm_count; ++s)
                 consider(joined != 0, s);
         }
     }

@@ -551,14 +551,13 @@ def mla_decode_noalloc(plan: mla_plan_t, q_lat, q_pe, pool, seq_lens, kv_indices
 
 def _native():
     """The module that checks the calls' arguments and makes them, on the loaded
-    library (built first if it is missing)."""
+    library (built first if it is missing or older than its source or the headers,
+    whose structures it reads)."""
     global _binding
     lib = load()
     with _lock:
         if _binding is None:
-            path = _build.binding_path()
-            if not os.path.exists(path):
-                _build.build_binding()
+            path = _build.build_binding()
             loader = importlib.machinery.ExtensionFileLoader("mla_binding", path)
             module = importlib.util.module_from_spec(
                 importlib.util.spec_from_loader("mla_binding", loader))

@@ -27,16 +27,17 @@
 //   p = p_hi + p_lo is an e4m3 term and the residual in e5m2, whose 2^-16
 //   smallest step lets both terms accumulate into the same columns without a
 //   scale of their own (a second set of columns does not fit: O^T takes 256 of
-//   TMEM's 512 columns at 64 rows, the two S^T buffers the others).  The pair
-//   carries about seven bits down to 2^-14 of p's unit, two more than that
-//   below the row's reference, where bf16 carries eight.
+//   TMEM's 512 columns at 64 rows, the two S^T buffers the others).  The pair is
+//   off by at most 4.2e-3 of p (1.3e-3 in the mean square; rounding to bf16: 3.9e-3
+//   and 1.6e-3) down to 2^-12 of the row's reference, by 1.4e-2 at 2^-14 and 0.11
+//   from 2^-17 on.  O is divided by the sum of what was fed, so common errors cancel.
 // * prefix_merge: joins a row's partials by their base-2 LSEs.
 //
 // What bounds the split kernel: shared memory's 128 bytes a cycle.  A block of
 // 128 keys and 64 rows reads 18 x 8 KB for QK (both terms stacked along N, so K
 // is read once) and 32 x 6 KB for P.V (V once per term), the bulk copies write
 // 72 KB and the softmax 16 KB: 435 KB, 3,400 cycles, against 2,176 of
-// multiplying at the bf16 rate.  It takes 3,670 (1.9 us; the MMAs alone, back
+// multiplying at the bf16 rate.  It takes 1.92 us, about 3,700 (the MMAs alone, back
 // to back: 18 x 73 + 32 x 58 = 3,170).  More rows per tile would read less per
 // row, but O^T and the S^T buffers fill TMEM and the stages, queries and P fill
 // shared memory.

@@ -392,9 +392,9 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 // ---- prefix_split -----------------------------------------------------------------------------
 //
 // Warp 0 loads, warp 1 issues the MMAs, warp 2 looks up the tile's requests, warps 2
-// and 3 write third terms, warps 4-11 are two softmax sets of four warps; set s owns query rows 32 s .. 32 s + 31,
-// warp w % 4 of a set the TMEM lanes (keys) 32 (w % 4) .. + 31, one key per thread,
-// as in the split kernel.
+// and 3 write third terms, warps 4-11 are two softmax sets of four warps; set s owns
+// query rows 32 s .. 32 s + 31, warp w % 4 of a set the TMEM lanes (keys) 32 (w % 4)
+// .. + 31, one key per thread, as in the split kernel.
 //
 // A stage's four latent chunks are released one by one, as the P.V MMAs of that
 // chunk finish, so the next block's chunks stream in behind them; the RoPE

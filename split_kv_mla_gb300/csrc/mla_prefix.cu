@@ -406,8 +406,8 @@ prefix_prepare_kernel(const PrefixArgs a, int own_ctas, int query_ctas)
 // starts.  All of its blocks then pass through the other stage, each chunk behind the
 // P.V of the block before, and QK makes a second pass over the block, which adds the
 // third terms to the low terms' columns of S^T.  (Measured: 64 requests of 128 heads
-// on 32768 positions 464 us without such a row, 757 with one in the batch, 836 with
-// all rows; 4 of 16 heads on 1024 19.0, 23.4 and 38.6.  Nothing else held those 36
+// on 32768 positions 462 us without such a row, 757 with one in the batch, 836 with
+// all rows; 4 of 16 heads on 1024 18.5, 23.0 and 38.2.  Nothing else held those 36
 // KB: shared memory is full, and the workspace's layout is the plan's.  A loop of its
 // own for such tiles slowed the others: the roles' loops together just fill the
 // instruction cache, 82 % of whose requests hit without that code, 70 % with it.)
@@ -1104,8 +1104,10 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs& a, uint8_t* smem,
         scl[4 * g + 2] = s.z;
         scl[4 * g + 3] = s.w;
     }
-    // (without `have` the columns may hold anything: the rows are zero then)
-#pragma unroll
+    // (without `have` the columns may hold anything: the rows are zero then.  The loop
+    // is rolled for the instruction cache: unrolled, 44.4 us instead of 42.6 at 64
+    // requests of 16 heads with 1000 + 1000 positions, 18.9 instead of 18.5 at 4 of 16.)
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tmem_ld32(lanes + kColO + c * kRows + r0, o);

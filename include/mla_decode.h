@@ -72,12 +72,18 @@ extern "C" {
 #define MLA_DEVERR_BAD_LENGTH 4u     /* seq_lens[b] outside [0, kv_indptr[b+1]-kv_indptr[b]];
                                         a fork's child longer than its parent */
 #define MLA_DEVERR_BAD_POSITION 8u   /* mla_cache_append: a position outside the table */
-#define MLA_DEVERR_BAD_TABLE 16u     /* mla_cache_fork: a parent outside [0, num_parents), or
-                                        table offsets outside their lists */
+#define MLA_DEVERR_BAD_TABLE 16u     /* mla_cache_fork, mla_cache_extend, mla_beam_reorder: a
+                                        parent outside [0, num_parents), or table offsets
+                                        outside their lists */
+#define MLA_DEVERR_BAD_LOGITS 32u    /* mla_beam_select: a row with a NaN or +inf, or a score
+                                        that is one */
+#define MLA_DEVERR_NO_SLOT 64u       /* mla_cache_extend: no free slot was left */
 
-/* Element types of the DCP share buffers (mla_decode_dcp, mla_dcp_lse_merge_ranks). */
+/* Element types: the DCP share buffers (mla_decode_dcp, mla_dcp_lse_merge_ranks) take
+ * the first two, the logits of mla_beam_select all three. */
 #define MLA_DTYPE_BF16 0
 #define MLA_DTYPE_F32 1
+#define MLA_DTYPE_F16 2
 
 /* Largest split count the reducer accepts (hip_mha_decoding_num_partitions: the
  * reducer's 256-partition specialization caps the MLA-style split count). */
@@ -569,6 +575,118 @@ int mla_cache_compact(void* pool, int64_t pool_rows, int32_t row_bytes,
 /* Workspace bytes of mla_cache_compact for a pool of pool_rows rows; 0 for an
  * unsupported count. */
 int64_t mla_cache_compact_workspace_bytes(int64_t pool_rows);
+
+/*
+ * Beam selection: the num_select best continuations of each request's beams.  Row
+ * b * beams + w of the logits belongs to beam w of request b; with x its logits,
+ *   score(b, w, v) = scores[b, w] + x_v - log sum_u exp(x_u)       (rounded to fp32)
+ * and the request's candidates (w, v) are taken by their score, equal scores by the
+ * lower w * vocab + v:
+ *   tokens[b, k]       = v
+ *   parents[b, k]      = b * beams + w, the row that continues (what mla_cache_fork,
+ *                        mla_cache_extend and mla_beam_reorder take as parents)
+ *   scores_out[b, k]   = the score
+ *   finished_out[b, k] = 1 when v is end_token or the beam had finished, else 0
+ * A beam with finished[b, w] != 0 has one candidate, end_token, whose score is the
+ * beam's own.  A beam whose score is -inf has none (an unused beam; a first step
+ * gives one beam of a request a score of 0 and the others -inf).  The logits of
+ * both are not looked at.  A logit of -inf is no candidate.  A NaN or +inf among a
+ * row's logits, or as its score, leaves the beam without candidates and sets
+ * MLA_DEVERR_BAD_LOGITS.  Where a request has fewer than num_select candidates the
+ * rest is token -1, parent b * beams, score -inf, finished 1.
+ *   logits    bf16, fp16 or fp32 (dtype MLA_DTYPE_*) [batch * beams, vocab], row r at
+ *             logits + r * row_stride (elements; rows may overlap, stride 0 is one row for
+ *             all), aligned to its elements; 16-byte aligned rows are read fastest
+ *   scores    fp32 [batch, beams]
+ *   finished  uint8 [batch, beams] or NULL (none has; needs an end_token)
+ *   end_token in [0, vocab), or -1: there is none
+ *   tokens, parents int32, scores_out fp32, finished_out uint8 (may be NULL)
+ *             [batch, num_select].  scores_out may be scores, and finished_out
+ *             finished, when num_select equals beams; else nothing overlaps.
+ *   workspace of mla_beam_select_workspace_bytes(batch, beams, vocab) bytes, 256-byte
+ *             aligned, zeroed header (calls that overlap do not share it)
+ * batch <= 65535; beams and num_select in [1, MLA_MAX_BEAMS]; vocab <= 2^20.
+ */
+#define MLA_MAX_BEAMS 32
+int mla_beam_select(const void* logits, int32_t dtype, int64_t row_stride, const float* scores,
+                    const uint8_t* finished, int32_t batch, int32_t beams, int32_t vocab,
+                    int32_t num_select, int32_t end_token, int32_t* tokens, int32_t* parents,
+                    float* scores_out, uint8_t* finished_out, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of mla_beam_select; 0 for an unsupported shape. */
+int64_t mla_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab);
+
+/*
+ * Beam state reordering: row f of out becomes row p = parents[f] of state, as bytes.
+ *   state     [num_parents] rows of row_bytes contiguous bytes, state_stride bytes apart
+ *             (rows may overlap)
+ *   out       [num_rows] rows, out_stride bytes apart (at least row_bytes); overlaps no
+ *             other argument
+ *   parents   int32 [num_rows].  One outside [0, num_parents) sets
+ *             MLA_DEVERR_BAD_TABLE and leaves its row as it was (out_lens[f] = 0).
+ *   lens      int32 [num_parents], the elements of elem_bytes bytes (1, 2, 4 or 8;
+ *             row_bytes is a multiple) in use, or NULL: whole rows.  Only the first
+ *             lens[p] elements are copied, the rest of out's row stays as it was.
+ *             Outside [0, row_bytes / elem_bytes] it is clamped and sets
+ *             MLA_DEVERR_BAD_LENGTH.
+ *   tokens    int32 [num_rows] or NULL (else lens is given and elem_bytes is 4):
+ *             element lens[p] of out's row becomes tokens[f].  A row without room
+ *             for it sets MLA_DEVERR_BAD_LENGTH and does not take it.
+ *   out_lens  int32 [num_rows] or NULL (lens given): the elements in use of out's row;
+ *             not lens itself
+ *   workspace as for mla_cache_append: the error word
+ * state and out need no alignment; 16-byte aligned rows move fastest.
+ */
+int mla_beam_reorder(const void* state, int64_t state_stride, int32_t num_parents,
+                     int64_t row_bytes, int32_t elem_bytes, const int32_t* parents,
+                     int32_t num_rows, const int32_t* lens, const int32_t* tokens, void* out,
+                     int64_t out_stride, int32_t* out_lens, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/*
+ * Cache extension: the page tables, lengths, slots and positions of the next step,
+ * from the lengths of the requests.  Request f of num_requests continues request
+ * p = parents[f] (NULL: p = f) of the current tables: it keeps that one's first
+ * L_f = seq_lens[p] positions, sharing their slots (lengths below the table's drop
+ * its last positions, drafts that were not accepted), and takes n_f = new_tokens[f]
+ * (NULL: one) more.  With t_f the tokens of the requests before f, token
+ * t = t_f + i, i < n_f, is the request's position L_f + i and takes the next free
+ * slot in turn:
+ *   slots[t]        = free_slots[c + t], c = cursor[0]  (free_slots NULL: c + t, the
+ *                     slots from c on, which is what mla_cache_compact's live leaves)
+ *   positions[t]    = L_f + i + prefix_len[0]           (prefix_len NULL: + 0)
+ *   token_indptr[f] = t_f, and the total behind the last request
+ *   new_lens[f]     = L_f + n_f
+ *   new_indptr      = the new lengths' sums, as kv_indptr
+ *   new_indices[new_indptr[f] + j] = kv_indices[kv_indptr[p] + j]   j < L_f
+ *                                  = slots[t_f + j - L_f]            otherwise
+ *   new_cursor[0]   = c + the tokens (may be cursor itself)
+ * so that slots and positions are what mla_cache_append takes for the tokens and
+ * new_indices, new_indptr and new_lens what mla_decode takes after it.
+ *   kv_indices int32 [num_indices]; kv_indptr int32 [num_parents + 1]; seq_lens int32
+ *   [num_parents]; parents, new_tokens int32 [num_requests]; free_slots int32
+ *   [num_free], distinct slots that no table names; cursor int32 [1]; prefix_len int32 [1]
+ *   new_indices int32 [total]; new_indptr, token_indptr int32 [num_requests + 1];
+ *   new_lens int32 [num_requests]; slots, positions int32 [num_tokens]; new_cursor
+ *   int32 [1]; they overlap nothing else but cursor and new_cursor each other.
+ * total and num_tokens are room (shapes): tokens past the last are padding (slot -1,
+ * position 0) and entries of new_indices past the last stay as they were.
+ * Found on the device: a length outside [0, its table's] or a negative count
+ * (MLA_DEVERR_BAD_LENGTH: clamped); a parent or offset outside its list (the request
+ * keeps nothing and gets its tokens) or tokens or entries without room, which the last
+ * requests lose (MLA_DEVERR_BAD_TABLE); no free slot left (MLA_DEVERR_NO_SLOT) and a
+ * free slot outside [0, pool_rows) (MLA_DEVERR_BAD_SLOT): slot and entry are -1.
+ * workspace as for mla_cache_append.
+ */
+int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32_t* kv_indptr,
+                     const int32_t* seq_lens, int32_t num_parents, const int32_t* parents,
+                     const int32_t* new_tokens, int32_t num_requests, const int32_t* free_slots,
+                     int64_t num_free, const int32_t* cursor, int64_t pool_rows,
+                     const int32_t* prefix_len, int32_t* new_indices, int64_t total,
+                     int32_t* new_indptr, int32_t* new_lens, int32_t* slots, int32_t* positions,
+                     int64_t num_tokens, int32_t* token_indptr, int32_t* new_cursor,
+                     void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* mla_status_string(int status);

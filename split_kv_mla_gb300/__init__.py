@@ -9,9 +9,13 @@ plumbing of decode context parallelism (rank page tables, the exchange step).
 """
 from .mla import (  # noqa: F401
     MlaError,
+    beam_workspace,
     cache_workspace,
+    mla_beam_reorder,
+    mla_beam_select,
     mla_cache_append,
     mla_cache_compact,
+    mla_cache_extend,
     mla_cache_fork,
     mla_dcp_lse_merge_ranks,
     mla_decode,

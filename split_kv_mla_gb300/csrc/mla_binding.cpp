@@ -1,4 +1,4 @@
-// mla_binding.cpp -- argument checks and output tensors of the cache and
+// mla_binding.cpp -- argument checks and output tensors of the cache, beam and
 // shared-prefix entry points, for mla.py.
 //
 // A small call spends more of the host's time on its arguments than on its
@@ -19,6 +19,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <string>
+#include <vector>
 
 #include "mla_decode.h"
 
@@ -34,6 +35,9 @@ decltype(&mla_prefix_decode) prefix_decode_fn;
 decltype(&mla_cache_append) append_fn;
 decltype(&mla_cache_fork) fork_fn;
 decltype(&mla_cache_compact) compact_fn;
+decltype(&mla_cache_extend) extend_fn;
+decltype(&mla_beam_select) select_fn;
+decltype(&mla_beam_reorder) reorder_fn;
 PyObject* mla_error;   // the exception of a status other than MLA_OK
 
 const char* type_name(at::ScalarType t)
@@ -43,6 +47,7 @@ const char* type_name(at::ScalarType t)
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
     case at::kByte: return "torch.uint8";
+    case at::kBool: return "torch.bool";
     default: return c10::toString(t);
     }
 }
@@ -203,16 +208,19 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f)
     END_HANDLE_TH_ERRORS
 }
 
-// bind(prefix_decode, append, fork, compact, MlaError): addresses of the library's
-// entry points, and the exception to raise.
+// bind(prefix_decode, append, fork, compact, extend, select, reorder, MlaError):
+// addresses of the library's entry points, and the exception to raise.
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
-    return guarded(n, 5, [&]() -> PyObject* {
+    return guarded(n, 8, [&]() -> PyObject* {
         prefix_decode_fn = reinterpret_cast<decltype(prefix_decode_fn)>(integer(v[0]));
         append_fn = reinterpret_cast<decltype(append_fn)>(integer(v[1]));
         fork_fn = reinterpret_cast<decltype(fork_fn)>(integer(v[2]));
         compact_fn = reinterpret_cast<decltype(compact_fn)>(integer(v[3]));
-        Py_XSETREF(mla_error, Py_NewRef(v[4]));
+        extend_fn = reinterpret_cast<decltype(extend_fn)>(integer(v[4]));
+        select_fn = reinterpret_cast<decltype(select_fn)>(integer(v[5]));
+        reorder_fn = reinterpret_cast<decltype(reorder_fn)>(integer(v[6]));
+        Py_XSETREF(mla_error, Py_NewRef(v[7]));
         Py_RETURN_NONE;
     });
 }
@@ -424,10 +432,216 @@ PyObject* cache_compact(PyObject*, PyObject* const* v, Py_ssize_t n)
     });
 }
 
+// An int32 output of a call: the caller's, with at least n entries, or a new one.
+int32_t* entries(at::Tensor& t, const char* name, int64_t n, int dev)
+{
+    if (!t.defined()) t = allocate({n}, at::kInt, dev);
+    else if (t.numel() < n) bad(std::string(name) + " must have " + std::to_string(n) + " entries");
+    return static_cast<int32_t*>(address(t, name, at::kInt, dev));
+}
+
+// cache_extend(kv_indices, kv_indptr, seq_lens, cursor, total, num_tokens, pool_rows, parents,
+// new_tokens, prefix_len, free_slots, table, indptr, lens, slots, positions, token_indptr,
+// new_cursor, workspace)
+PyObject* cache_extend(PyObject*, PyObject* const* v, Py_ssize_t n)
+{
+    return guarded(n, 19, [&]() -> PyObject* {
+        const at::Tensor& indices = given(v[0], "kv_indices");
+        const at::Tensor& indptr = given(v[1], "kv_indptr");
+        const at::Tensor& lens = given(v[2], "seq_lens");
+        const at::Tensor& cursor = given(v[3], "cursor");
+        const int64_t total = integer(v[4]), T = integer(v[5]), pool_rows = integer(v[6]);
+        const at::Tensor& parents = tensor(v[7], "parents");
+        const at::Tensor& counts = tensor(v[8], "new_tokens");
+        const at::Tensor& prefix = tensor(v[9], "prefix_len");
+        const at::Tensor& free_slots = tensor(v[10], "free_slots");
+        at::Tensor out[7];
+        static const char* const names[7] = {"table", "indptr", "lens", "slots", "positions",
+                                             "token_indptr", "new_cursor"};
+        for (int i = 0; i < 7; ++i) out[i] = tensor(v[11 + i], names[i]);
+        const at::Tensor& ws = given(v[18], "workspace");
+        const int dev = call_device(indptr);
+        const int64_t P = lens.numel();
+        if (indptr.numel() != P + 1) bad("kv_indptr must have an entry more than seq_lens");
+        const int64_t F = parents.defined() ? parents.numel() : counts.defined() ? counts.numel() : P;
+        if (counts.defined() && counts.numel() != F) bad("new_tokens must match parents");
+        if (!parents.defined() && F > P) bad("new_tokens must have at most seq_lens' entries");
+        if (cursor.numel() != 1 || (prefix.defined() && prefix.numel() != 1))
+            bad("cursor and prefix_len must have one entry");
+        if (total < 0 || T < 0 || pool_rows < 0)
+            bad("total, num_tokens and pool_rows must not be negative");
+        const int32_t* ki = table(indices, "kv_indices", dev);
+        const int32_t* kp = table(indptr, "kv_indptr", dev);
+        const int32_t* sl = table(lens, "seq_lens", dev);
+        const int32_t* cu = table(cursor, "cursor", dev);
+        const int32_t* pa = table(parents, "parents", dev);
+        const int32_t* nt = table(counts, "new_tokens", dev);
+        const int32_t* pl = table(prefix, "prefix_len", dev);
+        const int32_t* fs = table(free_slots, "free_slots", dev);
+        // (an empty tensor's address is NULL, which means that none is given)
+        if (free_slots.defined() && fs == nullptr) bad("free_slots must not be empty");
+        if (parents.defined() && F == 0) pa = kp;
+        const int64_t sizes[7] = {total, F + 1, F, T, T, F + 1, 1};
+        int32_t* to[7];
+        for (int i = 0; i < 7; ++i) to[i] = entries(out[i], names[i], sizes[i], dev);
+        void* pw = address(ws, "workspace", at::kByte, dev);
+        void* stream = current_stream(dev);
+        const int p = size32(P), f = size32(F);
+        const int64_t ni = indices.numel(), nf = free_slots.defined() ? free_slots.numel() : 0;
+        int status;
+        Py_BEGIN_ALLOW_THREADS
+        status = extend_fn(ki, ni, kp, sl, p, pa, nt, f, fs, nf, cu, pool_rows, pl, to[0], total,
+                           to[1], to[2], to[3], to[4], T, to[5], to[6], pw, ws.numel(), stream);
+        Py_END_ALLOW_THREADS
+        check(status, "mla_cache_extend");
+        PyObject* r = PyTuple_New(7);
+        for (int i = 0; r != nullptr && i < 7; ++i) {
+            PyObject* o = output(v[11 + i], out[i]);
+            if (o == nullptr) {
+                Py_DECREF(r);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(r, i, o);
+        }
+        return r;
+    });
+}
+
+// Address of a contiguous tensor of truth values: of bools or of bytes.
+uint8_t* flags(const at::Tensor& t, const char* name, int dev)
+{
+    if (t.defined() && t.scalar_type() == at::kByte)
+        return static_cast<uint8_t*>(address(t, name, at::kByte, dev));
+    return static_cast<uint8_t*>(address(t, name, at::kBool, dev));
+}
+
+// beam_select(logits, scores, num_select, finished, end_token, tokens, parents, scores_out,
+// finished_out, workspace)
+PyObject* beam_select(PyObject*, PyObject* const* v, Py_ssize_t n)
+{
+    return guarded(n, 10, [&]() -> PyObject* {
+        const at::Tensor& logits = given(v[0], "logits");
+        const at::Tensor& scores = given(v[1], "scores");
+        const at::Tensor& finished = tensor(v[3], "finished");
+        at::Tensor tokens = tensor(v[5], "tokens"), parents = tensor(v[6], "parents");
+        at::Tensor scores_out = tensor(v[7], "scores_out"), ends = tensor(v[8], "finished_out");
+        const at::Tensor& ws = given(v[9], "workspace");
+        const int dev = call_device(logits);
+        const at::ScalarType type = logits.scalar_type();
+        int dtype = -1;
+        if (type == at::kBFloat16) dtype = MLA_DTYPE_BF16;
+        else if (type == at::kHalf) dtype = MLA_DTYPE_F16;
+        else if (type == at::kFloat) dtype = MLA_DTYPE_F32;
+        else bad(std::string("logits must be bf16, fp16 or fp32, got ") + type_name(type));
+        if (logits.dim() != 2 || scores.dim() != 2) bad("logits and scores must have two dimensions");
+        const int64_t B = scores.size(0), W = scores.size(1), V = logits.size(1);
+        if (logits.size(0) != B * W) bad("logits must have a row per score");
+        if (logits.stride(1) != 1 && V > 1) bad("logits must have contiguous rows");
+        if (finished.defined() && finished.sizes() != scores.sizes())
+            bad("finished must have scores' shape");
+        const int64_t K = v[2] == Py_None ? W : integer(v[2]);
+        const int32_t end = integer32(v[4], "end_token");
+        if (W < 1 || V < 1 || K < 1) bad("beams, vocabulary and num_select must be positive");
+        if (K > MLA_MAX_BEAMS) bad("num_select must be at most " + std::to_string(MLA_MAX_BEAMS));
+        if (!tokens.defined()) tokens = allocate({B, K}, at::kInt, dev);
+        if (!parents.defined()) parents = allocate({B, K}, at::kInt, dev);
+        if (!scores_out.defined()) scores_out = allocate({B, K}, at::kFloat, dev);
+        if (!ends.defined() && end >= 0) ends = allocate({B, K}, at::kBool, dev);
+        if (tokens.numel() != B * K || parents.numel() != B * K || scores_out.numel() != B * K ||
+            (ends.defined() && ends.numel() != B * K))
+            bad("tokens, parents, scores_out and finished_out must be [B, num_select]");
+        const float* ps = static_cast<const float*>(address(scores, "scores", at::kFloat, dev));
+        const uint8_t* pf = flags(finished, "finished", dev);
+        int32_t* pt = static_cast<int32_t*>(address(tokens, "tokens", at::kInt, dev));
+        int32_t* pp = static_cast<int32_t*>(address(parents, "parents", at::kInt, dev));
+        float* po = static_cast<float*>(address(scores_out, "scores_out", at::kFloat, dev));
+        uint8_t* pe = flags(ends, "finished_out", dev);
+        void* pw = address(ws, "workspace", at::kByte, dev);
+        void* stream = current_stream(dev);
+        const int b = size32(B), w = size32(W), c = size32(V), k = size32(K);
+        int status;
+        Py_BEGIN_ALLOW_THREADS
+        status = select_fn(logits.data_ptr(), dtype, logits.stride(0), ps, pf, b, w, c, k, end, pt,
+                           pp, po, pe, pw, ws.numel(), stream);
+        Py_END_ALLOW_THREADS
+        check(status, "mla_beam_select");
+        PyObject* r[4] = {output(v[5], tokens), output(v[6], parents), output(v[7], scores_out),
+                          output(v[8], ends)};
+        PyObject* all = r[0] && r[1] && r[2] && r[3] ? PyTuple_Pack(4, r[0], r[1], r[2], r[3])
+                                                    : nullptr;
+        for (PyObject* o : r) Py_XDECREF(o);
+        return all;
+    });
+}
+
+// beam_reorder(state, parents, lens, tokens, out, out_lens, workspace)
+PyObject* beam_reorder(PyObject*, PyObject* const* v, Py_ssize_t n)
+{
+    return guarded(n, 7, [&]() -> PyObject* {
+        const at::Tensor& state = given(v[0], "state");
+        const at::Tensor& parents = given(v[1], "parents");
+        const at::Tensor& lens = tensor(v[2], "lens");
+        const at::Tensor& tokens = tensor(v[3], "tokens");
+        at::Tensor out = tensor(v[4], "out"), out_lens = tensor(v[5], "out_lens");
+        const at::Tensor& ws = given(v[6], "workspace");
+        const int dev = call_device(state);
+        auto rows = [](const at::Tensor& t, const char* name) {   // elements of a row
+            int64_t size = 1;
+            for (int64_t d = t.dim() - 1; d >= 1; --d) {
+                if (t.size(d) > 1 && t.stride(d) != size)
+                    bad(std::string(name) + " must have contiguous rows");
+                size *= t.size(d);
+            }
+            return size;
+        };
+        if (state.dim() < 1) bad("state must have rows");
+        const int64_t R = state.size(0), F = parents.numel(), cols = rows(state, "state");
+        const int64_t size = state.element_size();
+        if (lens.defined() && lens.numel() != R) bad("lens must have an entry per row of state");
+        if (tokens.defined()) {
+            if (!lens.defined()) bad("tokens must come with lens");
+            if (state.scalar_type() != at::kInt) bad("tokens go to a state of torch.int32");
+            if (tokens.numel() != F) bad("tokens must match parents");
+        }
+        if (!out.defined()) {
+            std::vector<int64_t> shape(state.sizes().begin(), state.sizes().end());
+            shape[0] = F;
+            out = at::empty(shape, at::TensorOptions().dtype(state.scalar_type())
+                                       .device(at::kCUDA, dev));
+            // elements behind the lengths are not written
+            if (lens.defined()) out.zero_();
+        } else {
+            if (out.scalar_type() != state.scalar_type() || out.dim() != state.dim() ||
+                out.size(0) != F || rows(out, "out") != cols)
+                bad("out must have state's type and rows, one per parent");
+            on_device(out, "out", dev);
+        }
+        if (lens.defined() && !out_lens.defined()) out_lens = allocate({F}, at::kInt, dev);
+        if (out_lens.defined() && (!lens.defined() || out_lens.numel() != F))
+            bad("out_lens must come with lens and match parents");
+        const int32_t* pp = table(parents, "parents", dev);
+        const int32_t* pl = table(lens, "lens", dev);
+        const int32_t* pt = table(tokens, "tokens", dev);
+        int32_t* po = static_cast<int32_t*>(address(out_lens, "out_lens", at::kInt, dev));
+        void* pw = address(ws, "workspace", at::kByte, dev);
+        void* stream = current_stream(dev);
+        const int r = size32(R), f = size32(F);
+        int status;
+        Py_BEGIN_ALLOW_THREADS
+        status = reorder_fn(state.data_ptr(), state.stride(0) * size, r, cols * size, (int)size, pp, f,
+                            pl, pt, out.data_ptr(), out.stride(0) * size, po, pw, ws.numel(), stream);
+        Py_END_ALLOW_THREADS
+        check(status, "mla_beam_reorder");
+        return pair(output(v[4], out), output(v[5], out_lens));
+    });
+}
+
 #define MLA_METHOD(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MLA_METHOD(bind),       MLA_METHOD(prefix_decode), MLA_METHOD(cache_append),
-                         MLA_METHOD(cache_fork), MLA_METHOD(cache_compact), {nullptr, nullptr, 0, nullptr}};
+                         MLA_METHOD(cache_fork), MLA_METHOD(cache_compact), MLA_METHOD(cache_extend),
+                         MLA_METHOD(beam_select), MLA_METHOD(beam_reorder),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mla_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

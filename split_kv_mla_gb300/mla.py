@@ -1,5 +1,5 @@
 """Thin Python binding of libmla: argument marshalling only, through ctypes, and for
-the cache and shared-prefix calls, whose small sizes are bound by the host's time,
+the cache, beam and shared-prefix calls, whose small sizes are bound by the host's time,
 through an extension module (``csrc/mla_binding.cpp``).
 
 Every function has the name of the C entry point it calls (``mla_decode_plan``,
@@ -37,6 +37,9 @@ MLA_DEVERR_TIMEOUT = 2
 MLA_DEVERR_BAD_LENGTH = 4
 MLA_DEVERR_BAD_POSITION = 8
 MLA_DEVERR_BAD_TABLE = 16
+MLA_DEVERR_BAD_LOGITS = 32
+MLA_DEVERR_NO_SLOT = 64
+MLA_MAX_BEAMS = 32
 MLA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 HEADER = os.path.join(_build.ROOT, "include", "mla_decode.h")
 
@@ -142,6 +145,14 @@ def load(build_if_missing: bool = True, path: Optional[str] = None):
                                               i64, vp, vp, i64, vp, i64, vp]),
             "mla_cache_compact": (ctypes.c_int, [vp, i64, i32, vp, i64, vp, vp, vp, i64, vp]),
             "mla_cache_compact_workspace_bytes": (i64, [i64]),
+            "mla_cache_extend": (ctypes.c_int, [vp, i64, vp, vp, i32, vp, vp, i32, vp, i64, vp, i64,
+                                                vp, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64,
+                                                vp]),
+            "mla_beam_select": (ctypes.c_int, [vp, i32, i64, vp, vp, i32, i32, i32, i32, i32, vp,
+                                               vp, vp, vp, vp, i64, vp]),
+            "mla_beam_select_workspace_bytes": (i64, [i32, i32, i32]),
+            "mla_beam_reorder": (ctypes.c_int, [vp, i64, i32, i64, i32, vp, i32, vp, vp, vp, i64,
+                                                vp, vp, i64, vp]),
             "mla_dcp_lse_merge_ranks": (ctypes.c_int, [vp, i32, vp, i32, i64, i32, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
@@ -564,7 +575,8 @@ def _native():
             loader.exec_module(module)
             module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                           for n in ("mla_prefix_decode", "mla_cache_append", "mla_cache_fork",
-                                    "mla_cache_compact")), MlaError)
+                                    "mla_cache_compact", "mla_cache_extend", "mla_beam_select",
+                                    "mla_beam_reorder")), MlaError)
             _binding = module
     return _binding
 
@@ -611,8 +623,9 @@ def mla_prefix_decode(plan: mla_prefix_plan_t, q_lat, q_pe, pool, prefix_indices
 # ---- the cache: append, fork, compact ------------------------------------------------
 
 def cache_workspace(pool_rows: int = 0, device=None) -> torch.Tensor:
-    """A workspace with a zeroed header for mla_cache_append and mla_cache_fork, and
-    with the pool's row count for mla_cache_compact too."""
+    """A workspace with a zeroed header for mla_cache_append, mla_cache_fork,
+    mla_cache_extend and mla_beam_reorder, and with the pool's row count for
+    mla_cache_compact too."""
     n = 0
     if pool_rows:
         n = int(load().mla_cache_compact_workspace_bytes(int(pool_rows)))
@@ -672,3 +685,81 @@ def mla_cache_compact(pool, kv_indices, new_indices=None, live=None, workspace_t
     if workspace_t is None:
         workspace_t = cache_workspace(pool.shape[0], device=_cuda_device(pool))
     return (_binding or _native()).cache_compact(pool, kv_indices, new_indices, live, workspace_t)
+
+
+def mla_cache_extend(kv_indices, kv_indptr, seq_lens, cursor, total: int, num_tokens: int,
+                     pool_rows: int, parents=None, new_tokens=None, prefix_len=None,
+                     free_slots=None, table=None, indptr=None, lens=None, slots=None,
+                     positions=None, token_indptr=None, new_cursor=None, workspace_t=None,
+                     stream=None):
+    """The next step's page tables from the requests' lengths: request f keeps the first
+    seq_lens[p] positions of p = parents[f] (None: f) and gets new_tokens[f] (None: one)
+    free slots behind them, from free_slots[cursor] on (None: the slots from cursor on,
+    what mla_cache_compact's `live` leaves).  Returns (table, indptr, lens) for the
+    decode, (slots, positions) of the tokens for mla_cache_append, token_indptr and
+    new_cursor (which may be given as cursor itself).
+
+    total and num_tokens are the room of the table and of the tokens (shapes); prefix_len
+    int32 [1] is added to the positions, for tables that continue a shared prefix."""
+    if stream is not None:
+        with _on(stream):
+            return mla_cache_extend(kv_indices, kv_indptr, seq_lens, cursor, total, num_tokens,
+                                    pool_rows, parents, new_tokens, prefix_len, free_slots, table,
+                                    indptr, lens, slots, positions, token_indptr, new_cursor,
+                                    workspace_t)
+    if workspace_t is None:
+        workspace_t = cache_workspace(device=_cuda_device(kv_indptr))
+    return (_binding or _native()).cache_extend(
+        kv_indices, kv_indptr, seq_lens, cursor, total, num_tokens, pool_rows, parents, new_tokens,
+        prefix_len, free_slots, table, indptr, lens, slots, positions, token_indptr, new_cursor,
+        workspace_t)
+
+
+# ---- beams: selection and their states -----------------------------------------------
+
+def beam_workspace(batch: int, beams: int, vocab: int, device=None) -> torch.Tensor:
+    """A workspace with a zeroed header for mla_beam_select."""
+    n = int(load().mla_beam_select_workspace_bytes(int(batch), int(beams), int(vocab)))
+    if n == 0:
+        raise ValueError(f"{batch} requests of {beams} beams over {vocab} tokens are not supported")
+    return _workspace(n, device)
+
+
+def mla_beam_select(logits, scores, num_select: Optional[int] = None, finished=None,
+                    end_token: int = -1, tokens=None, parents=None, scores_out=None,
+                    finished_out=None, workspace_t=None, stream=None):
+    """The num_select (None: the beams' number) best continuations of each request's beams,
+    by scores[b, w] + log_softmax(logits[b * W + w])[v], equal ones by the lower
+    w * vocab + v; returns (tokens, parents, scores, finished), each [B, num_select].
+
+    logits bf16, fp16 or fp32 [B * W, vocab], rows contiguous; scores fp32 [B, W]; finished
+    bool or uint8 [B, W]: such a beam continues with end_token and its own score.  parents
+    are rows of logits.  The finished of the result is None without an end_token."""
+    if stream is not None:
+        with _on(stream):
+            return mla_beam_select(logits, scores, num_select, finished, end_token, tokens, parents,
+                                   scores_out, finished_out, workspace_t)
+    if workspace_t is None:
+        dev = _cuda_device(logits)
+        if scores.dim() != 2 or logits.dim() != 2:
+            raise ValueError("logits and scores must have two dimensions")
+        workspace_t = (_workspace(0, dev) if scores.shape[0] == 0 else
+                       beam_workspace(*scores.shape, logits.shape[1], device=dev))
+    return (_binding or _native()).beam_select(logits, scores, num_select, finished, end_token,
+                                               tokens, parents, scores_out, finished_out, workspace_t)
+
+
+def mla_beam_reorder(state, parents, lens=None, tokens=None, out=None, out_lens=None,
+                     workspace_t=None, stream=None):
+    """out[f] = state[parents[f]] for the rows of a state of any type; returns (out,
+    out_lens).  lens int32 [rows of state]: only that many of a row's elements are copied
+    (the rest of a given out stays, of a new one is zero).  tokens int32 [rows of out], for
+    a state of int32: tokens[f] behind them.  out_lens (None without lens) counts both.
+    out must not overlap state."""
+    if stream is not None:
+        with _on(stream):
+            return mla_beam_reorder(state, parents, lens, tokens, out, out_lens, workspace_t)
+    if workspace_t is None:
+        workspace_t = cache_workspace(device=_cuda_device(state))
+    return (_binding or _native()).beam_reorder(state, parents, lens, tokens, out, out_lens,
+                                                workspace_t)

@@ -127,6 +127,37 @@ at::Tensor allocate(at::IntArrayRef shape, at::ScalarType type, int dev)
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
 }
 
+// Small outputs of a call in one allocation (each takes 1.4 us of the host's time: an
+// extension with seven 12.9 us a call, with two 6.3).  add() before, take() after the
+// allocation, in the same order; every part starts on 16 bytes.
+class Parts {
+public:
+    void add(int64_t n, at::ScalarType type) { bytes_ += size(n, type); }
+
+    at::Tensor take(at::IntArrayRef shape, at::ScalarType type, int dev)
+    {
+        if (!all_.defined()) all_ = allocate({bytes_}, at::kByte, dev);
+        int64_t n = 1;
+        for (int64_t s : shape) n *= s;
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::Storage(all_.storage()), all_.key_set(), c10::scalarTypeToTypeMeta(type));
+        auto* impl = t.unsafeGetTensorImpl();
+        impl->set_storage_offset(at_ / (int64_t)c10::elementSize(type));
+        impl->set_sizes_contiguous(shape);
+        at_ += size(n, type);
+        return t;
+    }
+
+private:
+    static int64_t size(int64_t n, at::ScalarType type)
+    {
+        return (n * (int64_t)c10::elementSize(type) + 15) / 16 * 16;
+    }
+
+    at::Tensor all_;
+    int64_t bytes_ = 0, at_ = 0;
+};
+
 int64_t integer(PyObject* o)
 {
     const long long v = PyLong_AsLongLong(o);
@@ -432,14 +463,6 @@ PyObject* cache_compact(PyObject*, PyObject* const* v, Py_ssize_t n)
     });
 }
 
-// An int32 output of a call: the caller's, with at least n entries, or a new one.
-int32_t* entries(at::Tensor& t, const char* name, int64_t n, int dev)
-{
-    if (!t.defined()) t = allocate({n}, at::kInt, dev);
-    else if (t.numel() < n) bad(std::string(name) + " must have " + std::to_string(n) + " entries");
-    return static_cast<int32_t*>(address(t, name, at::kInt, dev));
-}
-
 // cache_extend(kv_indices, kv_indptr, seq_lens, cursor, total, num_tokens, pool_rows, parents,
 // new_tokens, prefix_len, free_slots, table, indptr, lens, slots, positions, token_indptr,
 // new_cursor, workspace)
@@ -483,7 +506,17 @@ PyObject* cache_extend(PyObject*, PyObject* const* v, Py_ssize_t n)
         if (parents.defined() && F == 0) pa = kp;
         const int64_t sizes[7] = {total, F + 1, F, T, T, F + 1, 1};
         int32_t* to[7];
-        for (int i = 0; i < 7; ++i) to[i] = entries(out[i], names[i], sizes[i], dev);
+        Parts parts;   // all but the table
+        for (int i = 1; i < 7; ++i)
+            if (!out[i].defined()) parts.add(sizes[i], at::kInt);
+        for (int i = 0; i < 7; ++i) {
+            if (out[i].defined() && out[i].numel() < sizes[i])
+                bad(std::string(names[i]) + " must have " + std::to_string(sizes[i]) + " entries");
+            if (!out[i].defined())
+                out[i] = i == 0 ? allocate({total}, at::kInt, dev)
+                                : parts.take({sizes[i]}, at::kInt, dev);
+            to[i] = static_cast<int32_t*>(address(out[i], names[i], at::kInt, dev));
+        }
         void* pw = address(ws, "workspace", at::kByte, dev);
         void* stream = current_stream(dev);
         const int p = size32(P), f = size32(F);
@@ -543,10 +576,19 @@ PyObject* beam_select(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int32_t end = integer32(v[4], "end_token");
         if (W < 1 || V < 1 || K < 1) bad("beams, vocabulary and num_select must be positive");
         if (K > MLA_MAX_BEAMS) bad("num_select must be at most " + std::to_string(MLA_MAX_BEAMS));
-        if (!tokens.defined()) tokens = allocate({B, K}, at::kInt, dev);
-        if (!parents.defined()) parents = allocate({B, K}, at::kInt, dev);
-        if (!scores_out.defined()) scores_out = allocate({B, K}, at::kFloat, dev);
-        if (!ends.defined() && end >= 0) ends = allocate({B, K}, at::kBool, dev);
+        Parts parts;
+        const struct {
+            at::Tensor& t;
+            bool wanted;
+            at::ScalarType type;
+        } outs[4] = {{tokens, true, at::kInt},
+                     {parents, true, at::kInt},
+                     {scores_out, true, at::kFloat},
+                     {ends, end >= 0, at::kBool}};
+        for (const auto& o : outs)
+            if (!o.t.defined() && o.wanted) parts.add(B * K, o.type);
+        for (const auto& o : outs)
+            if (!o.t.defined() && o.wanted) o.t = parts.take({B, K}, o.type, dev);
         if (tokens.numel() != B * K || parents.numel() != B * K || scores_out.numel() != B * K ||
             (ends.defined() && ends.numel() != B * K))
             bad("tokens, parents, scores_out and finished_out must be [B, num_select]");

@@ -16,12 +16,14 @@ namespace {
 // With `overlap` false it starts only when all earlier work on the stream is
 // done (after a memset, which is no kernel to depend on).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads,
-                             cudaStream_t stream, bool overlap, Args... args)
+inline cudaError_t launch_dependent_shared(void (*kernel)(KArgs...), dim3 grid, int threads,
+                                           int shared, cudaStream_t stream, bool overlap,
+                                           Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)shared;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -29,6 +31,14 @@ inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int thr
     cfg.attrs = at;
     cfg.numAttrs = overlap ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// The same without dynamic shared memory.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads,
+                                    cudaStream_t stream, bool overlap, Args... args)
+{
+    return launch_dependent_shared(kernel, grid, threads, 0, stream, overlap, args...);
 }
 
 __device__ __forceinline__ void wait_for_predecessor()

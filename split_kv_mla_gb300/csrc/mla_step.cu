@@ -34,10 +34,13 @@ namespace {
 // so equal rows give equal sums and their equal candidates are taken by their index.
 
 constexpr int kGroup = 256;             // columns
-constexpr int kPieces = 8;              // 16-byte loads of a lane per segment
+constexpr int kLongPieces = 8;          // 16-byte loads of a lane per segment, of large calls
+constexpr int kShortPieces = 2;         // and of small ones
 constexpr int kScanThreads = 256;
-constexpr int kPickThreads = 1024;
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickList = 1024;
+static_assert(kPickWarps == 16, "the halves of 16 warps are the 32 parts that pick_best takes");
 constexpr int kMaxVocab = 1 << 20;
 
 struct SelectArgs {
@@ -94,8 +97,8 @@ struct LogitType<__half> {
 template <typename T>
 constexpr int kElements = 16 / (int)sizeof(T);   // of a 16-byte piece
 
-template <typename T>
-constexpr int kSegment = kPieces * 32 * kElements<T>;   // columns
+template <typename T, int PIECES>
+constexpr int kSegment = PIECES * 32 * kElements<T>;   // columns
 
 // Maximum of a piece (a NaN is passed over: the sum shows it).
 template <typename T>
@@ -199,25 +202,31 @@ __device__ __forceinline__ bool row_is_live(const SelectArgs& a, int64_t row)
            (a.finished == nullptr || __ldg(a.finished + row) == 0);
 }
 
-template <typename T, bool ALIGNED>
+// A warp per segment.  The rows of beams without candidates are not read, except where
+// a call is so small that its logits are asked for before it is known which those are.
+template <typename T, bool ALIGNED, int PIECES>
 __global__ void __launch_bounds__(kScanThreads)
 scan_kernel(const SelectArgs a)
 {
+    constexpr bool kEager = PIECES == kShortPieces;
     constexpr int E = kElements<T>;
     constexpr int kPerGroup = kGroup / (32 * E);         // pieces of a group
-    constexpr int kGroups = kPieces / kPerGroup;         // groups of a segment
+    constexpr int kGroups = PIECES / kPerGroup;          // groups of a segment
     wait_for_predecessor();
     allow_dependents();
     const int lane = threadIdx.x & 31;
     const uint32_t id = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);   // below 2^31
     const int64_t row = id / (uint32_t)a.segments;
     const int seg = (int)(id % (uint32_t)a.segments);
-    if (row >= a.rows || !row_is_live(a, row)) return;
+    if (row >= a.rows) return;
+    const bool live = row_is_live(a, row);
+    if (!kEager && !live) return;
     const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    const int c0 = seg * kSegment<T> + lane * E;
-    uint4 v[kPieces];
+    const int c0 = seg * kSegment<T, PIECES> + lane * E;
+    uint4 v[PIECES];
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) v[p] = load_piece<T, ALIGNED>(x, c0 + p * 32 * E, a.vocab);
+    for (int p = 0; p < PIECES; ++p) v[p] = load_piece<T, ALIGNED>(x, c0 + p * 32 * E, a.vocab);
+    if (kEager && !live) return;
 
     int most = INT32_MIN, mine = 0;
 #pragma unroll
@@ -237,7 +246,7 @@ scan_kernel(const SelectArgs a)
     constexpr float kLog2e = 1.4426950408889634f;
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p)
+    for (int p = 0; p < PIECES; ++p)
         each_logit<T>(v[p], [&](int i, float t) { sum[i & 1] += ex2_approx((t - ref) * kLog2e); });
     float s = sum[0] + sum[1];
 #pragma unroll
@@ -274,12 +283,19 @@ __device__ __forceinline__ float2 row_base(float score, float m, float sum)
     return make_float2(hi, __fadd_rn(__fsub_rn(b.x, hi), rest));
 }
 
-// A candidate as a number: its score, then the lower index; 0: none.
-__device__ __forceinline__ uint64_t candidate(float score, uint32_t index)
+// A score as a number in its order; 0 for what is no candidate (-inf, or the NaN that
+// the base of a beam without candidates makes).
+__device__ __forceinline__ uint32_t rank_of(float2 base, float x)
 {
-    if (!(score > -INFINITY)) return 0;
-    const uint32_t s = (uint32_t)ordered(score + 0.f) ^ 0x80000000u;   // -0 as +0
-    return (uint64_t)s << 32 | (0xFFFFFFFFu - index);
+    const float2 s = two_sum(base.x, x);
+    const float score = __fadd_rn(__fadd_rn(s.x, __fadd_rn(s.y, base.y)), 0.f);   // -0 as +0
+    return score > -INFINITY ? (uint32_t)ordered(score) ^ 0x80000000u : 0u;
+}
+
+// With the index, a lower one first; 0: none.
+__device__ __forceinline__ uint64_t candidate(uint32_t rank, uint32_t index)
+{
+    return rank == 0 ? 0 : (uint64_t)rank << 32 | (0xFFFFFFFFu - index);
 }
 
 __device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xFFFFFFFFu - (uint32_t)c; }
@@ -289,88 +305,78 @@ __device__ __forceinline__ float score_of(uint64_t c)
     return from_ordered((int)((uint32_t)(c >> 32) ^ 0x80000000u));
 }
 
-__device__ __forceinline__ uint64_t candidate_of(float2 base, float x, uint32_t index)
-{
-    if (x == -INFINITY) return 0;
-    const float2 s = two_sum(base.x, x);
-    return candidate(__fadd_rn(s.x, __fadd_rn(s.y, base.y)), index);
-}
-
-__device__ __forceinline__ uint64_t warp_max(uint64_t v)
-{
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-    return (uint64_t)hi << 32 | lo;
-}
-
 struct Picker {
-    uint64_t best[kPickThreads / 32];   // of each warp
+    uint32_t best[32];            // of each half of a warp
     uint64_t list[kPickList];
-    uint64_t taken[MLA_MAX_BEAMS];
-    uint64_t least;
+    uint64_t last[kPickWarps];
+    uint32_t least;
     int count;
 };
 
-// The K largest of the CTA's candidates (distinct numbers, 0 for none) in p.taken, in
-// order.  each(f) calls f for each of this thread's.  With K of 32 warps' best at hand,
-// all of the K largest are at or above the K-th of those: what is, is listed and
-// ranked by counting.  A list that would overflow (one warp holds most of them, and
-// many) is not used: the K are taken one after the other.
-template <class Each>
-__device__ __forceinline__ void pick_best(Picker& p, int K, Each&& each)
+// The K largest of the CTA's candidates: done(k, c) is called once for each k < K, by
+// some thread, with the k-th of them (0 where there are fewer).  best is the largest
+// rank among this thread's, and each(least, f) calls f(candidate) for each of this
+// thread's of at least that rank.  Of the best of 32 parts the K-th is at or below the
+// K-th of all: what is not below it is listed and ranked by counting.  A list that
+// would overflow (many equal scores, or a part that holds most of the best and many) is
+// not used: the K are taken one after the other.
+template <class Each, class Done>
+__device__ __forceinline__ void pick_best(Picker& p, int K, uint32_t best, Each&& each, Done&& done)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint64_t best = 0;
-    each([&](uint64_t c) { best = c > best ? c : best; });
-    best = warp_max(best);
-    if (lane == 0) p.best[warp] = best;
+    const uint32_t half = lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+    best = __reduce_max_sync(half, best);
+    if ((lane & 15) == 0) p.best[2 * warp + (lane >> 4)] = best;
     if (tid == 0) {
         p.count = 0;
         p.least = 1;
     }
     __syncthreads();
     if (warp == 0) {
-        const uint64_t mine = p.best[lane];
-        int rank = 0;
+        const uint32_t mine = p.best[lane];
+        int above = 0;
 #pragma unroll
-        for (int w = 0; w < kPickThreads / 32; ++w) rank += p.best[w] > mine ? 1 : 0;
-        if (rank == K - 1 && mine != 0) p.least = mine;
+        for (int w = 0; w < 32; ++w) {
+            const uint32_t other = p.best[w];
+            above += other > mine || (other == mine && w < lane) ? 1 : 0;
+        }
+        if (above == K - 1 && mine != 0) p.least = mine;
     }
     __syncthreads();
-    const uint64_t least = p.least;
-    each([&](uint64_t c) {
-        if (c >= least) {
-            const int at = atomicAdd(&p.count, 1);
-            if (at < kPickList) p.list[at] = c;
-        }
+    each(p.least, [&](uint64_t c) {
+        const int at = atomicAdd(&p.count, 1);
+        if (at < kPickList) p.list[at] = c;
     });
     __syncthreads();
     const int n = p.count;
     if (n <= kPickList) {
-        if (tid < n) {
-            const uint64_t mine = p.list[tid];
-            int rank = 0;
-            for (int i = 0; i < n; ++i) rank += p.list[i] > mine ? 1 : 0;
-            if (rank < K) p.taken[rank] = mine;
+        for (int i = tid; i < n; i += kPickThreads) {
+            const uint64_t mine = p.list[i];
+            int above = 0;
+            for (int j = 0; j < n; ++j) above += p.list[j] > mine ? 1 : 0;
+            if (above < K) done(above, mine);
         }
-        if (tid >= n && tid < K) p.taken[tid] = 0;
+        if (tid >= n && tid < K) done(tid, 0);
     } else {
         uint64_t last = ~0ull;
         for (int k = 0; k < K; ++k) {
             uint64_t next = 0;
-            each([&](uint64_t c) { next = c < last && c > next ? c : next; });
-            next = warp_max(next);
+            each(1, [&](uint64_t c) { next = c < last && c > next ? c : next; });
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) {
+                const uint64_t other = __shfl_xor_sync(0xffffffffu, next, off);
+                next = other > next ? other : next;
+            }
+            if (lane == 0) p.last[warp] = next;
             __syncthreads();
-            if (lane == 0) p.best[warp] = next;
+            last = p.last[0];
+#pragma unroll
+            for (int w = 1; w < kPickWarps; ++w) last = p.last[w] > last ? p.last[w] : last;
+            if (tid == 0) done(k, last);
             __syncthreads();
-            last = warp_max(p.best[lane]);
-            if (tid == 0) p.taken[k] = last;
         }
     }
-    __syncthreads();
 }
-
-enum : int { kRowDead = 0, kRowLive = 1, kRowEnded = 2 };
 
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kPickThreads)
@@ -378,118 +384,203 @@ pick_kernel(const SelectArgs a)
 {
     constexpr int E = kElements<T>;
     constexpr int kPerGroup = kGroup / (32 * E);
+    constexpr int kItems = 8;      // group maxima of a thread that stay in registers
+    constexpr int kParts = 4;      // parts of a row, of a lane
+    constexpr int kTurns = MLA_MAX_BEAMS / kPickWarps;
     __shared__ Picker p;
-    __shared__ float2 base[MLA_MAX_BEAMS];   // (own score, -) of a beam that has ended
-    __shared__ int state[MLA_MAX_BEAMS];
+    __shared__ uint64_t taken[MLA_MAX_BEAMS];
+    __shared__ float2 base[MLA_MAX_BEAMS];   // -inf: no candidates; of an ended beam its score
+    __shared__ uint32_t ended;               // bit per beam
     wait_for_predecessor();
     allow_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
-    const int K = a.select;
+    const int K = a.select, W = a.beams;
+    const uint32_t G = (uint32_t)a.groups, items = (uint32_t)W * G;
 
-    if (warp < a.beams) {
-        const int64_t row = row0 + warp;
-        const float own = a.scores[row];
-        const bool ended = a.finished != nullptr && a.finished[row] != 0;
-        float m = -INFINITY, s = 0.f;
-        if (own != -INFINITY && !ended) {
-            const float2* parts = a.parts + row * a.segments;
-            for (int i = lane; i < a.segments; i += 32) m = fmaxf(m, __ldcg(&parts[i]).x);
-            m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
-            const float ref = m == -INFINITY ? 0.f : m;
-            constexpr float kLog2e = 1.4426950408889634f;
-            for (int i = lane; i < a.segments; i += 32) {
-                const float2 t = __ldcg(&parts[i]);
-                s += t.y * ex2_approx((t.x - ref) * kLog2e);
-            }
+    const float* maxima = a.group_max + row0 * G;
+    float gm[kItems];
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    for (int k = 0; k < kItems; ++k) {
+        const uint32_t i = tid + k * kPickThreads;
+        gm[k] = i < items ? __ldcg(maxima + i) : 0.f;
+    }
+    if (tid < 32) {
+        const bool e = tid < W && a.finished != nullptr && a.finished[row0 + tid] != 0;
+        const uint32_t bits = __ballot_sync(0xffffffffu, e);
+        if (tid == 0) ended = bits;
+    }
+#pragma unroll 1
+    for (int w = warp; w < W; w += kPickWarps) {
+        const int64_t row = row0 + w;
+        const float2* parts = a.parts + row * a.segments;
+        const float own = __ldg(a.scores + row);
+        const bool is_ended = a.finished != nullptr && a.finished[row] != 0;
+        float2 t[kParts];
+        float m = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            const int i = lane + 32 * k;
+            t[k] = i < a.segments ? __ldcg(parts + i) : make_float2(-INFINITY, 0.f);
         }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) m = fmaxf(m, t[k].x);
+        for (int i = lane + 32 * kParts; i < a.segments; i += 32) m = fmaxf(m, __ldcg(parts + i).x);
+        m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+        const float ref = m == -INFINITY ? 0.f : m;
+        constexpr float kLog2e = 1.4426950408889634f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) s += t[k].y * ex2_approx((t[k].x - ref) * kLog2e);
+        for (int i = lane + 32 * kParts; i < a.segments; i += 32) {
+            const float2 u = __ldcg(parts + i);
+            s += u.y * ex2_approx((u.x - ref) * kLog2e);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         if (lane == 0) {
+            // (what is not read of a beam without candidates may be anything)
+            const bool none = own == -INFINITY;
             // a NaN or +inf among the logits makes the sum one
-            const bool bad = !(own < INFINITY) || (!ended && own != -INFINITY && !(s < INFINITY));
+            const bool bad = !none && (!(own < INFINITY) || (!is_ended && !(s < INFINITY)));
             if (bad) atomicOr(a.err, MLA_DEVERR_BAD_LOGITS);
-            const bool dead = bad || own == -INFINITY || (!ended && s == 0.f);
-            state[warp] = dead ? kRowDead : ended ? kRowEnded : kRowLive;
-            base[warp] = dead || ended ? make_float2(own, 0.f) : row_base(own, m, s);
+            if (none || bad || (!is_ended && s == 0.f)) base[w] = make_float2(-INFINITY, 0.f);
+            else base[w] = is_ended ? make_float2(own, 0.f) : row_base(own, m, s);
         }
     }
     __syncthreads();
 
-    const uint32_t items = (uint32_t)a.beams * (uint32_t)a.groups;
-    pick_best(p, K, [&](auto&& take) {
-        for (uint32_t i = tid; i < items; i += kPickThreads) {
-            const uint32_t w = i / (uint32_t)a.groups;
-            const int st = state[w];
-            if (st == kRowLive)
-                take(candidate_of(base[w], __ldcg(a.group_max + row0 * a.groups + i), i));
-            else if (st == kRowEnded && i == w * a.groups)
-                take(candidate(base[w].x, i));
+    // groups: item i of beam i / G
+    const uint32_t ends = ended;
+    const uint32_t step_w = kPickThreads / G, step_g = kPickThreads % G;
+    auto rank_item = [&](uint32_t w, uint32_t g, float x) {
+        if ((ends >> w) & 1u) x = g == 0 ? 0.f : -INFINITY;
+        return rank_of(base[w], x);
+    };
+    auto next_item = [&](uint32_t& w, uint32_t& g) {
+        w += step_w;
+        g += step_g;
+        if (g >= G) {
+            g -= G;
+            ++w;
         }
-    });
-
-    // a warp's group, eight logits a lane
-    uint64_t c[kPerGroup * E];
+    };
+    uint32_t rank[kItems], best = 0;
+    uint32_t w = (uint32_t)tid / G, g = (uint32_t)tid % G;
 #pragma unroll
-    for (int i = 0; i < kPerGroup * E; ++i) c[i] = 0;
-    const uint64_t mine = warp < K ? p.taken[warp] : 0;
-    if (mine != 0) {
-        const uint32_t g = index_of(mine);
-        const uint32_t w = g / (uint32_t)a.groups;
-        if (state[w] == kRowEnded) {
-            if (lane == 0) c[0] = candidate(base[w].x, w * a.vocab + a.end_token);
-        } else {
-            const T* x = static_cast<const T*>(a.logits) + (row0 + w) * a.row_stride;
-            const int col = (int)(g - w * a.groups) * kGroup + lane * E;
-            const float2 b = base[w];
+    for (int k = 0; k < kItems; ++k) {
+        rank[k] = w < (uint32_t)W ? rank_item(w, g, gm[k]) : 0u;
+        best = max(best, rank[k]);
+        next_item(w, g);
+    }
+    const uint32_t w8 = w, g8 = g;   // of the first item that is not in registers
+    for (uint32_t i = tid + kItems * kPickThreads; i < items; i += kPickThreads) {
+        best = max(best, rank_item(w, g, __ldcg(maxima + i)));
+        next_item(w, g);
+    }
+    pick_best(
+        p, K, best,
+        [&](uint32_t least, auto&& take) {
 #pragma unroll
-            for (int q = 0; q < kPerGroup; ++q) {
-                const int c0 = col + q * 32 * E;
-                const uint4 v = load_piece<T, ALIGNED>(x, c0, a.vocab);
-                each_logit<T>(v, [&](int i, float t) {
-                    c[q * E + i] = candidate_of(b, t, w * a.vocab + c0 + i);
-                });
+            for (int k = 0; k < kItems; ++k)
+                if (rank[k] >= least) take(candidate(rank[k], tid + k * kPickThreads));
+            uint32_t iw = w8, ig = g8;
+            for (uint32_t i = tid + kItems * kPickThreads; i < items; i += kPickThreads) {
+                const uint32_t r = rank_item(iw, ig, __ldcg(maxima + i));
+                if (r >= least) take(candidate(r, i));
+                next_item(iw, ig);
             }
-        }
-    }
-    __syncthreads();   // everyone has read taken
-    pick_best(p, K, [&](auto&& take) {
-#pragma unroll
-        for (int i = 0; i < kPerGroup * E; ++i) take(c[i]);
-    });
+        },
+        [&](int k, uint64_t c) { taken[k] = c; });
+    __syncthreads();
 
-    if (tid < K) {
-        const uint64_t t = p.taken[tid];
-        const int64_t at = (int64_t)blockIdx.x * K + tid;
-        int token = -1, w = 0;
-        float score = -INFINITY;
-        bool end = true;
-        if (t != 0) {
-            const uint32_t i = index_of(t);
-            w = (int)(i / (uint32_t)a.vocab);
-            token = (int)(i - (uint32_t)w * a.vocab);
-            score = score_of(t);
-            end = token == a.end_token || state[w] == kRowEnded;
+    // the logits of a warp's groups, eight a lane
+    uint4 v[kTurns][kPerGroup];
+    uint32_t column[kTurns], beam[kTurns], top[kTurns];
+    best = 0;
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+        const int k = warp + q * kPickWarps;
+        const uint64_t mine = k < K ? taken[k] : 0;
+        const uint32_t i = index_of(mine);
+        beam[q] = mine != 0 ? i / G : 0u;
+        column[q] = (i - beam[q] * G) * kGroup + lane * E;
+        top[q] = 0;
+        if (mine == 0) continue;
+        if ((ends >> beam[q]) & 1u) {
+            column[q] = a.end_token;
+            top[q] = lane == 0 ? rank_of(base[beam[q]], 0.f) : 0u;
+        } else {
+            const T* x = static_cast<const T*>(a.logits) + (row0 + beam[q]) * a.row_stride;
+            float m = -INFINITY;
+#pragma unroll
+            for (int z = 0; z < kPerGroup; ++z)
+                v[q][z] = load_piece<T, ALIGNED>(x, column[q] + z * 32 * E, a.vocab);
+#pragma unroll
+            for (int z = 0; z < kPerGroup; ++z) m = fmaxf(m, piece_max<T>(v[q][z]));
+            top[q] = rank_of(base[beam[q]], m);
         }
-        a.tokens[at] = token;
-        a.parents[at] = (int32_t)(row0 + w);
-        a.scores_out[at] = score;
-        if (a.finished_out != nullptr) a.finished_out[at] = end ? 1 : 0;
+        best = max(best, top[q]);
     }
+    const int64_t out = (int64_t)blockIdx.x * K;
+    pick_best(
+        p, K, best,
+        [&](uint32_t least, auto&& take) {
+#pragma unroll
+            for (int q = 0; q < kTurns; ++q) {
+                if (top[q] < least) continue;
+                const uint32_t first = beam[q] * (uint32_t)a.vocab + column[q];
+                if ((ends >> beam[q]) & 1u) {
+                    take(candidate(top[q], first));
+                } else {
+#pragma unroll
+                    for (int z = 0; z < kPerGroup; ++z)
+                        each_logit<T>(v[q][z], [&](int i, float x) {
+                            const uint32_t r = rank_of(base[beam[q]], x);
+                            if (r >= least) take(candidate(r, first + z * 32 * E + i));
+                        });
+                }
+            }
+        },
+        [&](int k, uint64_t c) {
+            int token = -1, w = 0;
+            float score = -INFINITY;
+            bool end = true;
+            if (c != 0) {
+                const uint32_t i = index_of(c);
+                w = (int)(i / (uint32_t)a.vocab);
+                token = (int)(i - (uint32_t)w * a.vocab);
+                score = score_of(c);
+                end = token == a.end_token || ((ends >> w) & 1u) != 0;
+            }
+            a.tokens[out + k] = token;
+            a.parents[out + k] = (int32_t)(row0 + w);
+            a.scores_out[out + k] = score;
+            if (a.finished_out != nullptr) a.finished_out[out + k] = end ? 1 : 0;
+        });
 }
+
+template <typename T, bool ALIGNED, int PIECES>
+cudaError_t launch_scan(SelectArgs& a, cudaStream_t s)
+{
+    a.segments = (a.vocab + kSegment<T, PIECES> - 1) / kSegment<T, PIECES>;
+    const int64_t warps = a.rows * a.segments;
+    const int64_t ctas = (warps + kScanThreads / 32 - 1) / (kScanThreads / 32);
+    return launch_dependent(scan_kernel<T, ALIGNED, PIECES>, dim3((unsigned)ctas), kScanThreads, s,
+                            true, a);
+}
+
+// Segments of 1 KB instead of 4 while they are no more than the GPU's SMs hold at a time.
+constexpr int64_t kShortWarps = 152 * 32;
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_select(SelectArgs a, cudaStream_t s)
 {
-    a.segments = (a.vocab + kSegment<T> - 1) / kSegment<T>;
-    const int64_t warps = a.rows * a.segments;
-    const int64_t ctas = (warps + kScanThreads / 32 - 1) / (kScanThreads / 32);
-    cudaError_t e = launch_dependent(scan_kernel<T, ALIGNED>, dim3((unsigned)ctas), kScanThreads, s,
-                                     true, a);
-    if (e == cudaSuccess)
-        e = launch_dependent(pick_kernel<T, ALIGNED>, dim3((unsigned)a.batch), kPickThreads, s, true,
-                             a);
-    return e;
+    const int64_t n = kSegment<T, kShortPieces>;
+    const bool small = a.rows * ((a.vocab + n - 1) / n) <= kShortWarps;
+    const cudaError_t e = small ? launch_scan<T, ALIGNED, kShortPieces>(a, s)
+                                : launch_scan<T, ALIGNED, kLongPieces>(a, s);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(pick_kernel<T, ALIGNED>, dim3((unsigned)a.batch), kPickThreads, s, true, a);
 }
 
 template <typename T>
@@ -508,11 +599,13 @@ bool select_shape_ok(int64_t batch, int64_t beams, int64_t vocab)
 
 int64_t select_groups(int64_t vocab) { return (vocab + kGroup - 1) / kGroup; }
 
-// Bytes of the segments' parts (most for fp32, whose segments are shortest).
+// Bytes of the segments' parts: short segments are no more than kShortWarps, long ones
+// most for fp32.
 int64_t select_part_bytes(int64_t rows, int64_t vocab)
 {
-    const int64_t n = kSegment<float>;
-    return align256(rows * ((vocab + n - 1) / n) * (int64_t)sizeof(float2));
+    const int64_t n = kSegment<float, kLongPieces>;
+    const int64_t parts = rows * ((vocab + n - 1) / n);
+    return align256((parts > kShortWarps ? parts : kShortWarps) * (int64_t)sizeof(float2));
 }
 
 // ---- beam state reordering ------------------------------------------------------------------
@@ -592,10 +685,20 @@ reorder_kernel(const ReorderArgs a)
 
 // ---- cache extension --------------------------------------------------------------------------
 //
-// sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
-// fill   a thread per entry of the new table and per token.
 // Bytes: 8 per entry that is kept, 12 (16 with a list of free slots) per token.
+// Every CTA sums the requests' lengths and counts by itself, in shared memory, and
+// fills its part of the new table from there: one launch.  A kernel that left the sums
+// for a second one took 7.5 us where this takes 4.9 (8 requests of 8192), and looking a
+// request up in global memory, per entry, 103 us where this takes 9 (512 of 1024 to
+// 8192).  More requests than shared memory is given for go that way:
+//   sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
+//   fill   a thread per entry of the new table and per token.
 
+constexpr int kExtendThreads = 256;
+constexpr int kExtendRequests = 2048;   // 32 KB of sums
+constexpr int kExtendSpan = 8;          // entries in flight per thread
+constexpr int kExtendCtas = 4 * 152;
+constexpr int kLeadTokens = 2048;       // that one CTA takes
 constexpr int kSumThreads = 1024;
 constexpr int kFillThreads = 256;
 
@@ -648,72 +751,252 @@ __device__ __forceinline__ Kept kept_of(const ExtendArgs& a, int f, uint32_t& ba
     return Kept{(int32_t)from, (int32_t)len};
 }
 
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane)
+// a + b, or 2^32 - 1 where that is less: sums of lengths and counts, whose use is
+// bounded by less than 2^31.
+__device__ __forceinline__ uint32_t add_up(uint32_t a, uint32_t b)
+{
+    const uint32_t s = a + b;
+    return s < a ? 0xFFFFFFFFu : s;
+}
+
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane)
 {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += u;
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v = add_up(v, u);
     }
     return v;
 }
 
-// Inclusive sums over the CTA's threads; `part` holds one sum per warp.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& all)
+// Sum of the threads before this one's, and of all; `part` holds one sum per warp.
+template <int WARPS>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t& all)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = warp_scan(v, lane);
+    const uint32_t sum = warp_scan(v, lane);
+    uint32_t before = __shfl_up_sync(0xffffffffu, sum, 1);
+    if (lane == 0) before = 0;
     __syncthreads();
-    if (lane == 31) part[warp] = v;
+    if (lane == 31) part[warp] = sum;
     __syncthreads();
-    const int64_t w = warp_scan(part[lane], lane);
+    const uint32_t w = warp_scan(lane < WARPS ? part[lane] : 0u, lane);
     all = __shfl_sync(0xffffffffu, w, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    return v + (warp > 0 ? before : 0);
+    const uint32_t warps = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return warp > 0 ? add_up(warps, before) : before;
+}
+
+// The number of the token's free slot, in 32 bits as the cursor, to its slot (-1: none).
+__device__ __forceinline__ int32_t free_slot(const ExtendArgs& a, int32_t number, uint32_t& bad)
+{
+    if (number < 0 || number >= (a.free_slots == nullptr ? a.pool_rows : a.num_free)) {
+        bad |= MLA_DEVERR_NO_SLOT;
+        return -1;
+    }
+    const int32_t slot = a.free_slots == nullptr ? number : __ldg(a.free_slots + number);
+    if (slot >= 0 && slot < a.pool_rows) return slot;
+    bad |= MLA_DEVERR_BAD_SLOT;
+    return -1;
+}
+
+// The last f in [lo, hi) with start[f] <= i (start[lo] <= i).
+__device__ __forceinline__ int last_at_most(const int32_t* start, int lo, int hi, int32_t i)
+{
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// CTA 0 writes what is per request, and with `spread` false all of what is per token,
+// so that it alone reads the cursor that it then moves (which may be one and the
+// same); the others copy.
+__global__ void __launch_bounds__(kExtendThreads)
+extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
+{
+    extern __shared__ int32_t sums[];
+    __shared__ uint32_t part[kExtendThreads / 32];
+    wait_for_predecessor();
+    allow_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, F = a.num_requests;
+    int32_t* const start = sums;              // [F + 1] of the new table
+    int32_t* const token = start + F + 1;     // [F + 1] tokens before
+    int32_t* const length = token + F + 1;    // [F] kept
+    int32_t* const from = length + F;         // [F] kv_indices of the new table's entry 0
+    const bool lead = blockIdx.x == 0;
+    const uint32_t room = (uint32_t)a.total, token_room = (uint32_t)a.num_tokens;
+    uint32_t bad = 0;
+    for (int f = tid; f < F; f += kExtendThreads) {
+        int n = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
+        if (n < 0) {
+            n = 0;
+            bad |= MLA_DEVERR_BAD_LENGTH;
+        }
+        const Kept k = kept_of(a, f, bad);
+        token[f] = n;
+        length[f] = k.length;
+        from[f] = k.from;
+    }
+    __syncthreads();
+    const int per = (F + kExtendThreads - 1) / kExtendThreads;
+    const int f0 = min(tid * per, F), f1 = min(f0 + per, F);
+    uint32_t mine = 0, all;
+    for (int f = f0; f < f1; ++f) mine = add_up(mine, token[f]);
+    uint32_t at = block_scan<kExtendThreads / 32>(mine, part, all);
+    for (int f = f0; f < f1; ++f) {
+        const uint32_t n = token[f];
+        token[f] = (int32_t)min(at, token_room);
+        at = add_up(at, n);
+    }
+    if (all > token_room) bad |= MLA_DEVERR_BAD_TABLE;
+    const int tokens = (int)min(all, token_room);
+    if (tid == 0) token[F] = tokens;
+    __syncthreads();
+    mine = 0;
+    for (int f = f0; f < f1; ++f) mine = add_up(mine, length[f] + (token[f + 1] - token[f]));
+    at = block_scan<kExtendThreads / 32>(mine, part, all);
+    for (int f = f0; f < f1; ++f) {
+        start[f] = (int32_t)min(at, room);
+        from[f] -= start[f];
+        at = add_up(at, length[f] + (token[f + 1] - token[f]));
+    }
+    if (all > room) bad |= MLA_DEVERR_BAD_TABLE;
+    const int32_t total = (int32_t)min(all, room);
+    if (tid == 0) start[F] = total;
+    __syncthreads();
+
+    if (lead || spread) {
+        const int step = spread ? (int)gridDim.x * kExtendThreads : kExtendThreads;
+        const int32_t cursor = a.num_tokens > 0 ? __ldg(a.cursor) : 0;
+        const int32_t prefix = a.prefix_len == nullptr ? 0 : __ldg(a.prefix_len);
+        for (int64_t t = (int64_t)(spread ? blockIdx.x : 0) * kExtendThreads + tid; t < a.num_tokens;
+             t += step) {
+            int32_t slot = -1, position = 0;
+            if (t < tokens) {
+                const int f = last_at_most(token, 0, F, (int32_t)t);
+                const int32_t j = length[f] + ((int32_t)t - token[f]);
+                position = j + prefix;
+                if (j < start[f + 1] - start[f]) {
+                    slot = free_slot(a, (int32_t)((uint32_t)cursor + (uint32_t)t), bad);
+                    a.new_indices[start[f] + j] = slot;
+                }
+            }
+            a.slots[t] = slot;
+            a.positions[t] = position;
+        }
+    }
+    if (lead) {
+        for (int f = tid; f <= F; f += kExtendThreads) {
+            a.new_indptr[f] = start[f];
+            a.token_indptr[f] = token[f];
+            if (f < F) a.new_lens[f] = start[f + 1] - start[f];
+        }
+        if (move_cursor) {
+            const uint32_t c = tid == 0 ? (uint32_t)a.cursor[0] : 0;
+            __syncthreads();   // every thread has read it
+            if (tid == 0) a.new_cursor[0] = (int32_t)(c + (uint32_t)tokens);
+        }
+        if (bad != 0) atomicOr(a.err, bad);
+        return;
+    }
+    if (spread && (bad & (MLA_DEVERR_NO_SLOT | MLA_DEVERR_BAD_SLOT)) != 0) atomicOr(a.err, bad);
+
+    // a warp's part of the table, and the requests in it
+    constexpr int kSpan = 32 * kExtendSpan;   // entries at a time
+    const int warps = ((int)gridDim.x - 1) * (kExtendThreads / 32);
+    const int warp = ((int)blockIdx.x - 1) * (kExtendThreads / 32) + (tid >> 5);
+    const int64_t run = ((int64_t)total + (int64_t)warps * kSpan - 1) / ((int64_t)warps * kSpan) * kSpan;
+    const int64_t begin = warp * run;
+    if (begin >= total) return;
+    const int32_t end = (int32_t)min(begin + run, (int64_t)total);
+    int lo = last_at_most(start, 0, F, (int32_t)begin);
+    for (int32_t i0 = (int32_t)begin; i0 < end; i0 += kSpan) {
+        const int32_t past = min(i0 + kSpan, end);
+        if (start[lo + 1] <= i0) lo = last_at_most(start, lo + 1, F, i0);
+        int32_t v[kExtendSpan];
+        if (start[lo + 1] >= past) {   // one request's
+            const int32_t until = min(past, start[lo] + length[lo]);
+            const int32_t* src = a.kv_indices + from[lo];
+#pragma unroll
+            for (int k = 0; k < kExtendSpan; ++k) {
+                const int32_t i = i0 + 32 * k + lane;
+                if (i < until) v[k] = __ldg(src + i);
+            }
+#pragma unroll
+            for (int k = 0; k < kExtendSpan; ++k) {
+                const int32_t i = i0 + 32 * k + lane;
+                if (i < until) a.new_indices[i] = v[k];
+            }
+            continue;
+        }
+        const int hi = last_at_most(start, lo, F, past - 1) + 1;
+        bool kept[kExtendSpan];
+#pragma unroll
+        for (int k = 0; k < kExtendSpan; ++k) {
+            const int32_t i = i0 + 32 * k + lane;
+            kept[k] = i < past;
+            if (kept[k]) {
+                const int f = last_at_most(start, lo, hi, i);
+                kept[k] = i - start[f] < length[f];
+                if (kept[k]) v[k] = __ldg(a.kv_indices + (from[f] + i));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kExtendSpan; ++k)
+            if (kept[k]) a.new_indices[i0 + 32 * k + lane] = v[k];
+    }
+}
+
+// The cursor in place, when every CTA of the kernel before has read it.
+__global__ void cursor_kernel(const ExtendArgs a)
+{
+    wait_for_predecessor();
+    allow_dependents();
+    a.new_cursor[0] = (int32_t)((uint32_t)a.cursor[0] + (uint32_t)a.token_indptr[a.num_requests]);
 }
 
 __global__ void __launch_bounds__(kSumThreads)
 sums_kernel(const ExtendArgs a)
 {
-    __shared__ int64_t part[32];
+    __shared__ uint32_t part[32];
     wait_for_predecessor();
     allow_dependents();
     const int tid = threadIdx.x;
-    int64_t tokens = 0, entries = 0;   // of the requests before this turn's
+    const uint32_t room = (uint32_t)a.total, token_room = (uint32_t)a.num_tokens;
+    uint32_t tokens = 0, entries = 0;   // of the requests before this turn's
     uint32_t bad = 0;
     for (int f0 = 0; f0 < a.num_requests; f0 += kSumThreads) {
         const int f = f0 + tid;
-        int64_t n = 0, length = 0;
+        uint32_t n = 0, length = 0;
         if (f < a.num_requests) {
-            n = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
-            if (n < 0) {
-                n = 0;
-                bad |= MLA_DEVERR_BAD_LENGTH;
-            }
+            const int32_t want = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
+            n = max(want, 0);
+            if (want < 0) bad |= MLA_DEVERR_BAD_LENGTH;
             length = kept_of(a, f, bad).length;
         }
-        int64_t all;
-        const int64_t last = tokens + block_scan(n, part, all);
-        const int64_t begin = min(last - n, a.num_tokens), end = min(last, a.num_tokens);
-        if (end - begin != n) bad |= MLA_DEVERR_BAD_TABLE;
-        tokens += all;
-        length += end - begin;
-        const int64_t until = entries + block_scan(length, part, all);
-        const int64_t first = min(until - length, a.total), past = min(until, a.total);
-        if (past - first != length) bad |= MLA_DEVERR_BAD_TABLE;
-        entries += all;
+        uint32_t all;
+        const uint32_t t = add_up(tokens, block_scan<kSumThreads / 32>(n, part, all));
+        const uint32_t first_token = min(t, token_room);
+        length += min(add_up(t, n), token_room) - first_token;
+        tokens = add_up(tokens, all);
+        const uint32_t e = add_up(entries, block_scan<kSumThreads / 32>(length, part, all));
+        const uint32_t first = min(e, room);
+        entries = add_up(entries, all);
         if (f < a.num_requests) {
-            a.token_indptr[f] = (int32_t)begin;
+            a.token_indptr[f] = (int32_t)first_token;
             a.new_indptr[f] = (int32_t)first;
-            a.new_lens[f] = (int32_t)(past - first);
+            a.new_lens[f] = (int32_t)(min(add_up(e, length), room) - first);
         }
     }
+    if (tokens > token_room || entries > room) bad |= MLA_DEVERR_BAD_TABLE;
     if (tid == 0) {
-        const int64_t n = min(tokens, a.num_tokens);
+        const uint32_t n = min(tokens, token_room);
         a.token_indptr[a.num_requests] = (int32_t)n;
-        a.new_indptr[a.num_requests] = (int32_t)min(entries, a.total);
+        a.new_indptr[a.num_requests] = (int32_t)min(entries, room);
         // modulo 2^32, so that fill has the cursor from the new one
-        a.new_cursor[0] = (int32_t)((uint32_t)a.cursor[0] + (uint32_t)n);
+        a.new_cursor[0] = (int32_t)((uint32_t)a.cursor[0] + n);
     }
     if (bad != 0) atomicOr(a.err, bad);
 }
@@ -757,18 +1040,8 @@ fill_kernel(const ExtendArgs a, uint32_t entry_ctas)
         const int64_t j = k.length + (t - __ldcg(a.token_indptr + f));
         position = (int32_t)(j + (a.prefix_len == nullptr ? 0 : __ldg(a.prefix_len)));
         if (j < __ldcg(a.new_lens + f)) {
-            // the number of the free slot, in 32 bits as the cursor
-            const int64_t number = (int32_t)((uint32_t)__ldcg(a.new_cursor) - (uint32_t)tokens +
-                                             (uint32_t)t);
-            if (number < 0 || number >= (a.free_slots == nullptr ? a.pool_rows : a.num_free)) {
-                bad = MLA_DEVERR_NO_SLOT;
-            } else {
-                slot = a.free_slots == nullptr ? (int32_t)number : __ldg(a.free_slots + number);
-                if (slot < 0 || slot >= a.pool_rows) {
-                    slot = -1;
-                    bad = MLA_DEVERR_BAD_SLOT;
-                }
-            }
+            slot = free_slot(a, (int32_t)((uint32_t)__ldcg(a.new_cursor) - (uint32_t)tokens + (uint32_t)t),
+                             bad);
             a.new_indices[__ldcg(a.new_indptr + f) + j] = slot;
         }
     }
@@ -968,6 +1241,19 @@ int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32
                        prefix_len, new_indices, total, new_indptr, new_lens, slots, positions,
                        num_tokens, token_indptr, new_cursor, static_cast<uint32_t*>(workspace)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_requests <= kExtendRequests) {
+        const int64_t per = kExtendThreads * kExtendSpan;
+        const int64_t most = (total + per - 1) / per;
+        const bool spread = num_tokens > kLeadTokens;
+        const bool in_place = new_cursor == cursor;
+        const dim3 grid((unsigned)(1 + (most < 1 ? 1 : most < kExtendCtas ? most : kExtendCtas)));
+        const int bytes = (4 * num_requests + 2) * 4;
+        cudaError_t e = launch_dependent_shared(extend_kernel, grid, kExtendThreads, bytes, s, true, a,
+                                                spread, !(spread && in_place));
+        if (e == cudaSuccess && spread && in_place)
+            e = launch_dependent(cursor_kernel, dim3(1), 1, s, true, a);
+        return status_of(e);
+    }
     cudaError_t e = launch_dependent(sums_kernel, dim3(1), kSumThreads, s, true, a);
     const int64_t entry_ctas = num_requests == 0 ? 0 : (total + kFillThreads - 1) / kFillThreads;
     const int64_t token_ctas = (num_tokens + kFillThreads - 1) / kFillThreads;

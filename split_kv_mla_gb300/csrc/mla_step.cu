@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <cstddef>
 
 #include "mla_internal.h"
 #include "mla_launch.h"
@@ -40,8 +41,9 @@ constexpr int kScanThreads = 256;
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickList = 1024;
-static_assert(kPickWarps == 16, "the halves of 16 warps are the 32 parts that pick_best takes");
 constexpr int kMaxVocab = 1 << 20;
+constexpr int kPlaceBits = 20;          // of a column
+static_assert(kMaxVocab <= 1 << kPlaceBits && MLA_MAX_BEAMS <= 1 << (32 - kPlaceBits), "");
 
 struct SelectArgs {
     const void* logits;
@@ -202,38 +204,35 @@ __device__ __forceinline__ bool row_is_live(const SelectArgs& a, int64_t row)
            (a.finished == nullptr || __ldg(a.finished + row) == 0);
 }
 
-// A warp per segment.  The rows of beams without candidates are not read, except where
-// a call is so small that its logits are asked for before it is known which those are.
+template <typename T, int PIECES>
+struct Segment {
+    uint4 v[PIECES];
+};
+
 template <typename T, bool ALIGNED, int PIECES>
-__global__ void __launch_bounds__(kScanThreads)
-scan_kernel(const SelectArgs a)
+__device__ __forceinline__ void load_segment(const SelectArgs& a, int64_t row, int seg, int lane,
+                                             Segment<T, PIECES>& s)
 {
-    constexpr bool kEager = PIECES == kShortPieces;
     constexpr int E = kElements<T>;
-    constexpr int kPerGroup = kGroup / (32 * E);         // pieces of a group
-    constexpr int kGroups = PIECES / kPerGroup;          // groups of a segment
-    wait_for_predecessor();
-    allow_dependents();
-    const int lane = threadIdx.x & 31;
-    const uint32_t id = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);   // below 2^31
-    const int64_t row = id / (uint32_t)a.segments;
-    const int seg = (int)(id % (uint32_t)a.segments);
-    if (row >= a.rows) return;
-    const bool live = row_is_live(a, row);
-    if (!kEager && !live) return;
     const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
     const int c0 = seg * kSegment<T, PIECES> + lane * E;
-    uint4 v[PIECES];
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) v[p] = load_piece<T, ALIGNED>(x, c0 + p * 32 * E, a.vocab);
-    if (kEager && !live) return;
+    for (int p = 0; p < PIECES; ++p) s.v[p] = load_piece<T, ALIGNED>(x, c0 + p * 32 * E, a.vocab);
+}
 
+// A segment's group maxima and its part.
+template <typename T, int PIECES>
+__device__ __forceinline__ void scan_segment(const SelectArgs& a, int64_t row, int seg, int lane,
+                                             const Segment<T, PIECES>& s)
+{
+    constexpr int kPerGroup = kGroup / (32 * kElements<T>);   // pieces of a group
+    constexpr int kGroups = PIECES / kPerGroup;               // groups of a segment
     int most = INT32_MIN, mine = 0;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-        float m = piece_max<T>(v[g * kPerGroup]);
+        float m = piece_max<T>(s.v[g * kPerGroup]);
 #pragma unroll
-        for (int p = 1; p < kPerGroup; ++p) m = fmaxf(m, piece_max<T>(v[g * kPerGroup + p]));
+        for (int p = 1; p < kPerGroup; ++p) m = fmaxf(m, piece_max<T>(s.v[g * kPerGroup + p]));
         const int r = __reduce_max_sync(0xffffffffu, ordered(m));
         most = max(most, r);
         if (lane == g) mine = r;
@@ -247,11 +246,34 @@ scan_kernel(const SelectArgs a)
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < PIECES; ++p)
-        each_logit<T>(v[p], [&](int i, float t) { sum[i & 1] += ex2_approx((t - ref) * kLog2e); });
-    float s = sum[0] + sum[1];
+        each_logit<T>(s.v[p], [&](int i, float t) { sum[i & 1] += ex2_approx((t - ref) * kLog2e); });
+    float all = sum[0] + sum[1];
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) a.parts[row * a.segments + seg] = make_float2(top, s);
+    for (int off = 16; off >= 1; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    if (lane == 0) a.parts[row * a.segments + seg] = make_float2(top, all);
+}
+
+// A warp per segment.  The rows of beams without candidates are not read, except where
+// a call is so small that its logits are asked for before it is known which those are.
+// (Warps that take several segments, the next one's logits in flight while they work on
+// one, were slower with 16 to 40 of them on an SM: 45.5 us for 268 MB, 44.5 this way.)
+template <typename T, bool ALIGNED, int PIECES>
+__global__ void __launch_bounds__(kScanThreads)
+scan_kernel(const SelectArgs a)
+{
+    constexpr bool kEager = PIECES == kShortPieces;
+    wait_for_predecessor();
+    allow_dependents();
+    const int lane = threadIdx.x & 31;
+    const uint32_t id = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);   // below 2^31
+    const int64_t row = id / (uint32_t)a.segments;
+    const int seg = (int)(id % (uint32_t)a.segments);
+    if (row >= a.rows) return;
+    const bool live = row_is_live(a, row);
+    if (!kEager && !live) return;
+    Segment<T, PIECES> s;
+    load_segment<T, ALIGNED, PIECES>(a, row, seg, lane, s);
+    if (live) scan_segment<T, PIECES>(a, row, seg, lane, s);
 }
 
 // (hi, lo) of a + b.
@@ -292,293 +314,375 @@ __device__ __forceinline__ uint32_t rank_of(float2 base, float x)
     return score > -INFINITY ? (uint32_t)ordered(score) ^ 0x80000000u : 0u;
 }
 
-// With the index, a lower one first; 0: none.
-__device__ __forceinline__ uint64_t candidate(uint32_t rank, uint32_t index)
+// A candidate of a beam as a number: by rank, then by the lower beam and the lower place
+// (a column or a group) in it.
+__device__ __forceinline__ uint64_t candidate(uint32_t rank, uint32_t beam, uint32_t place)
 {
-    return rank == 0 ? 0 : (uint64_t)rank << 32 | (0xFFFFFFFFu - index);
+    return (uint64_t)rank << 32 | (0xFFFFFFFFu - (beam << kPlaceBits | place));
 }
 
-__device__ __forceinline__ uint32_t index_of(uint64_t c) { return 0xFFFFFFFFu - (uint32_t)c; }
+__device__ __forceinline__ uint32_t beam_of(uint64_t c) { return ~(uint32_t)c >> kPlaceBits; }
+
+__device__ __forceinline__ uint32_t place_of(uint64_t c)
+{
+    return ~(uint32_t)c & ((1u << kPlaceBits) - 1u);
+}
 
 __device__ __forceinline__ float score_of(uint64_t c)
 {
     return from_ordered((int)((uint32_t)(c >> 32) ^ 0x80000000u));
 }
 
+__device__ __forceinline__ uint64_t warp_max(uint64_t v)
+{
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
+
+constexpr int kChunk = 8;          // candidates of a thread at a time
+constexpr int kPickSlots = 256;
+
 struct Picker {
-    uint32_t best[32];            // of each half of a warp
+    uint32_t best[2][32];               // of each part: of the groups, of the logits
+    uint32_t least[2];
+    int slots[2], count[2];
+    alignas(16) float x[kPickSlots][kChunk];   // logits (group maxima) of the threads that have any
+    int beam[kPickSlots], place[kPickSlots];
     uint64_t list[kPickList];
-    uint64_t last[kPickWarps];
-    uint32_t least;
-    int count;
+    uint64_t warps[kPickWarps];
+    float2 base[MLA_MAX_BEAMS];         // -inf: no candidates; of an ended beam its score
+    int ended[MLA_MAX_BEAMS];
 };
 
-// The K largest of the CTA's candidates: done(k, c) is called once for each k < K, by
-// some thread, with the k-th of them (0 where there are fewer).  best is the largest
-// rank among this thread's, and each(least, f) calls f(candidate) for each of this
-// thread's of at least that rank.  Of the best of 32 parts the K-th is at or below the
-// K-th of all: what is not below it is listed and ranked by counting.  A list that
-// would overflow (many equal scores, or a part that holds most of the best and many) is
-// not used: the K are taken one after the other.
-template <class Each, class Done>
-__device__ __forceinline__ void pick_best(Picker& p, int K, uint32_t best, Each&& each, Done&& done)
+static_assert(offsetof(Picker, x) % 16 == 0 && kChunk % 4 == 0, "chunks are stored as float4");
+
+// The K-th largest of the parts' best, or 1 if there are not that many, after a barrier.  The
+// threads of a lane are one of 32 parts of the CTA's candidates, and best is the largest
+// rank of this thread's: K candidates or more have the rank returned, or a larger one.
+__device__ __forceinline__ uint32_t rank_of_part(Picker& p, int round, int K, uint32_t best)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    atomicMax(&p.best[round][lane], best);
+    __syncthreads();
+    const uint32_t other = p.best[round][lane];
+#pragma unroll
+    for (int h = 0; h < 32 / kPickWarps; ++h) {
+        const int part = warp * (32 / kPickWarps) + h;
+        const uint32_t mine = __shfl_sync(0xffffffffu, other, part);
+        const uint32_t above = __ballot_sync(0xffffffffu, other > mine || (other == mine && lane < part));
+        if (lane == 0 && __popc(above) == K - 1 && mine != 0) p.least[round] = mine;
+    }
+    __syncthreads();
+    return p.least[round];
+}
+
+// Lists the CTA's candidates with ranks of at least `least`, and returns how many, after a
+// barrier.  each(f) calls f(beam, place, x) for the threads that have any, of kChunk
+// logits x at a time, of which the i-th lies at place + step(i).  Those threads, a few,
+// hand their logits over, and a thread for each ranks them (in the threads themselves the
+// eight took 1,700 cycles of the warp, this way it is 700).  Lists that would overflow
+// (many equal scores, or most of the best in few groups, and many) are not used: the K
+// largest are then taken one after the other.
+template <class Each, class Step>
+__device__ __forceinline__ int list_candidates(Picker& p, int round, int K, uint32_t least,
+                                               Each&& each, Step&& step)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t half = lane < 16 ? 0xFFFFu : 0xFFFF0000u;
-    best = __reduce_max_sync(half, best);
-    if ((lane & 15) == 0) p.best[2 * warp + (lane >> 4)] = best;
-    if (tid == 0) {
-        p.count = 0;
-        p.least = 1;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t mine = p.best[lane];
-        int above = 0;
+    uint64_t last = ~0ull;
+#pragma unroll 1
+    for (int k = -1; k < K; ++k) {   // -1: the list; else the k-th by itself
+        uint64_t next = 0;
+        each([&](int beam, int place, const float (&x)[kChunk]) {
+            if (k < 0) {
+                const int at = atomicAdd(&p.slots[round], 1);
+                if (at >= kPickSlots) return;
+                float4* to = reinterpret_cast<float4*>(p.x[at]);
+                to[0] = make_float4(x[0], x[1], x[2], x[3]);
+                to[1] = make_float4(x[4], x[5], x[6], x[7]);
+                p.beam[at] = beam;
+                p.place[at] = place;
+            } else {
 #pragma unroll
-        for (int w = 0; w < 32; ++w) {
-            const uint32_t other = p.best[w];
-            above += other > mine || (other == mine && w < lane) ? 1 : 0;
-        }
-        if (above == K - 1 && mine != 0) p.least = mine;
-    }
-    __syncthreads();
-    each(p.least, [&](uint64_t c) {
-        const int at = atomicAdd(&p.count, 1);
-        if (at < kPickList) p.list[at] = c;
-    });
-    __syncthreads();
-    const int n = p.count;
-    if (n <= kPickList) {
-        for (int i = tid; i < n; i += kPickThreads) {
-            const uint64_t mine = p.list[i];
-            int above = 0;
-            for (int j = 0; j < n; ++j) above += p.list[j] > mine ? 1 : 0;
-            if (above < K) done(above, mine);
-        }
-        if (tid >= n && tid < K) done(tid, 0);
-    } else {
-        uint64_t last = ~0ull;
-        for (int k = 0; k < K; ++k) {
-            uint64_t next = 0;
-            each(1, [&](uint64_t c) { next = c < last && c > next ? c : next; });
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {
-                const uint64_t other = __shfl_xor_sync(0xffffffffu, next, off);
-                next = other > next ? other : next;
+                for (int i = 0; i < kChunk; ++i) {
+                    const uint32_t r = rank_of(p.base[beam], x[i]);
+                    const uint64_t c = candidate(r, beam, place + step(i));
+                    if (r >= least && c < last && c > next) next = c;
+                }
             }
-            if (lane == 0) p.last[warp] = next;
-            __syncthreads();
-            last = p.last[0];
-#pragma unroll
-            for (int w = 1; w < kPickWarps; ++w) last = p.last[w] > last ? p.last[w] : last;
-            if (tid == 0) done(k, last);
-            __syncthreads();
+        });
+        __syncthreads();
+        if (k < 0) {
+            const int slots = p.slots[round];
+            if (slots <= kPickSlots) {
+                for (int t = tid; t < slots * kChunk; t += kPickThreads) {
+                    const int slot = t / kChunk, i = t % kChunk, beam = p.beam[slot];
+                    const uint32_t r = rank_of(p.base[beam], p.x[slot][i]);
+                    if (r >= least) {
+                        const int at = atomicAdd(&p.count[round], 1);
+                        if (at < kPickList) p.list[at] = candidate(r, beam, p.place[slot] + step(i));
+                    }
+                }
+                __syncthreads();
+                if (p.count[round] <= kPickList) return p.count[round];
+            }
+            continue;
         }
+        next = warp_max(next);
+        if (lane == 0) p.warps[warp] = next;
+        __syncthreads();
+        last = warp_max(p.warps[lane % kPickWarps]);
+        if (tid == 0) p.list[k] = last;
+    }
+    __syncthreads();
+    return K;
+}
+
+// done(k, x) for each of the K largest x of n listed, the k-th, by counting those above:
+// a warp for each of a few, a thread for each of many.
+template <class Done>
+__device__ __forceinline__ void rank_list(const uint64_t* list, int n, int K, Done&& done)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (n <= 32) {
+        const uint64_t other = lane < n ? list[lane] : 0;
+        for (int i = tid >> 5; i < n; i += kPickWarps) {
+            const uint64_t mine = list[i];
+            const int above = __popc(__ballot_sync(0xffffffffu, other > mine));
+            if (lane == 0 && above < K) done(above, mine);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int i = tid; i < n; i += kPickThreads) {
+        const uint64_t mine = list[i];
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) above += list[j] > mine ? 1 : 0;
+        if (above < K) done(above, mine);
     }
 }
 
+// Bounded by latency: a request is one SM's, and a warp's instructions follow one another
+// at four cycles and more, so what counts is the longest chain of them.  A beam belongs to
+// one warp or several, each with the beam's base for itself, so that all a request needs
+// is asked for at once.  Groups' maxima are candidates, so the rank that K of them reach
+// bounds the logits' too, and only those that are left in the end are put in order.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kPickThreads)
 pick_kernel(const SelectArgs a)
 {
     constexpr int E = kElements<T>;
     constexpr int kPerGroup = kGroup / (32 * E);
-    constexpr int kItems = 8;      // group maxima of a thread that stay in registers
     constexpr int kParts = 4;      // parts of a row, of a lane
     constexpr int kTurns = MLA_MAX_BEAMS / kPickWarps;
+    static_assert(kPerGroup * E == kChunk, "a lane's logits of a group are one chunk");
     __shared__ Picker p;
-    __shared__ uint64_t taken[MLA_MAX_BEAMS];
-    __shared__ float2 base[MLA_MAX_BEAMS];   // -inf: no candidates; of an ended beam its score
-    __shared__ uint32_t ended;               // bit per beam
+    __shared__ uint64_t groups[MLA_MAX_BEAMS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = a.select, W = a.beams, G = a.groups;
+    const int share = W < kPickWarps ? kPickWarps / W : 1;   // warps of a beam
+    const int beam0 = warp / share, part0 = warp % share;
+    if (tid < 64) p.best[tid >> 5][tid & 31] = 0;
+    if (tid < 2) {
+        p.least[tid] = 1;
+        p.slots[tid] = p.count[tid] = 0;
+    }
+    __syncthreads();
     wait_for_predecessor();
     allow_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * a.beams;
-    const int K = a.select, W = a.beams;
-    const uint32_t G = (uint32_t)a.groups, items = (uint32_t)W * G;
+    const int64_t row0 = (int64_t)blockIdx.x * W;
 
-    const float* maxima = a.group_max + row0 * G;
-    float gm[kItems];
+    // A thread's groups in beam w are first_group(w) + 32 share k.  (Turned by the beam, so
+    // that beams of a few groups do not all lie in the same lanes.)
+    auto first_group = [&](int w) { return part0 * 32 + ((lane + 5 * w) & 31); };
+    float x[kChunk];
+    auto load_maxima = [&](int w, int g) {
+        const float* maxima = a.group_max + (row0 + w) * G;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const uint32_t i = tid + k * kPickThreads;
-        gm[k] = i < items ? __ldcg(maxima + i) : 0.f;
-    }
-    if (tid < 32) {
-        const bool e = tid < W && a.finished != nullptr && a.finished[row0 + tid] != 0;
-        const uint32_t bits = __ballot_sync(0xffffffffu, e);
-        if (tid == 0) ended = bits;
-    }
+        for (int k = 0; k < kChunk; ++k) {
+            x[k] = g < G ? __ldcg(maxima + g) : -INFINITY;
+            g += 32 * share;
+        }
+    };
+    auto largest = [&] {
+        return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                     fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    };
+    uint32_t top0 = 0, top1 = 0;   // largest rank of the thread's beams
+    static_assert(kTurns == 2, "");
 #pragma unroll 1
-    for (int w = warp; w < W; w += kPickWarps) {
+    for (int w = beam0; w < W; w += kPickWarps) {
         const int64_t row = row0 + w;
         const float2* parts = a.parts + row * a.segments;
-        const float own = __ldg(a.scores + row);
+        const float own = a.scores[row];
         const bool is_ended = a.finished != nullptr && a.finished[row] != 0;
         float2 t[kParts];
-        float m = -INFINITY, s = 0.f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
             const int i = lane + 32 * k;
             t[k] = i < a.segments ? __ldcg(parts + i) : make_float2(-INFINITY, 0.f);
         }
+        const int g0 = first_group(w);
+        load_maxima(w, g0);
+        float m = -INFINITY, s = 0.f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) m = fmaxf(m, t[k].x);
+#pragma unroll 1
         for (int i = lane + 32 * kParts; i < a.segments; i += 32) m = fmaxf(m, __ldcg(parts + i).x);
         m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
         const float ref = m == -INFINITY ? 0.f : m;
         constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) s += t[k].y * ex2_approx((t[k].x - ref) * kLog2e);
+#pragma unroll 1
         for (int i = lane + 32 * kParts; i < a.segments; i += 32) {
             const float2 u = __ldcg(parts + i);
             s += u.y * ex2_approx((u.x - ref) * kLog2e);
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == 0) {
-            // (what is not read of a beam without candidates may be anything)
-            const bool none = own == -INFINITY;
-            // a NaN or +inf among the logits makes the sum one
-            const bool bad = !none && (!(own < INFINITY) || (!is_ended && !(s < INFINITY)));
+        // (what is not read of a beam without candidates may be anything)
+        const bool none = own == -INFINITY;
+        // a NaN or +inf among the logits makes the sum one
+        const bool bad = !none && (!(own < INFINITY) || (!is_ended && !(s < INFINITY)));
+        float2 b = make_float2(-INFINITY, 0.f);
+        if (!none && !bad && (is_ended || s != 0.f))
+            b = is_ended ? make_float2(own, 0.f) : row_base(own, m, s);
+        if (lane == 0 && part0 == 0) {
+            p.base[w] = b;
+            p.ended[w] = is_ended ? 1 : 0;
             if (bad) atomicOr(a.err, MLA_DEVERR_BAD_LOGITS);
-            if (none || bad || (!is_ended && s == 0.f)) base[w] = make_float2(-INFINITY, 0.f);
-            else base[w] = is_ended ? make_float2(own, 0.f) : row_base(own, m, s);
         }
+        if (is_ended) {   // its one candidate is in its first group
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
+            if (g0 == 0) x[0] = 0.f;
+        }
+        float most = largest();
+        if (!is_ended) {
+            const float* maxima = a.group_max + row * G;
+#pragma unroll 1
+            for (int g = g0 + 32 * share * kChunk; g < G; g += 32 * share)
+                most = fmaxf(most, __ldcg(maxima + g));
+        }
+        (w < kPickWarps ? top0 : top1) = rank_of(b, most);
     }
-    __syncthreads();
+    uint32_t least = rank_of_part(p, 0, K, max(top0, top1));
 
-    // groups: item i of beam i / G
-    const uint32_t ends = ended;
-    const uint32_t step_w = kPickThreads / G, step_g = kPickThreads % G;
-    auto rank_item = [&](uint32_t w, uint32_t g, float x) {
-        if ((ends >> w) & 1u) x = g == 0 ? 0.f : -INFINITY;
-        return rank_of(base[w], x);
-    };
-    auto next_item = [&](uint32_t& w, uint32_t& g) {
-        w += step_w;
-        g += step_g;
-        if (g >= G) {
-            g -= G;
-            ++w;
-        }
-    };
-    uint32_t rank[kItems], best = 0;
-    uint32_t w = (uint32_t)tid / G, g = (uint32_t)tid % G;
+    bool reload = W > kPickWarps;   // (of two beams only the last's maxima are there)
+    int n = list_candidates(
+        p, 0, K, least,
+        [&](auto&& take) {
+#pragma unroll 1
+            for (int w = beam0; w < W; w += kPickWarps) {
+                if ((w < kPickWarps ? top0 : top1) < least) continue;
+                const int g0 = first_group(w);
+                const bool is_ended = p.ended[w] != 0;
+                if (is_ended) {
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        rank[k] = w < (uint32_t)W ? rank_item(w, g, gm[k]) : 0u;
-        best = max(best, rank[k]);
-        next_item(w, g);
-    }
-    const uint32_t w8 = w, g8 = g;   // of the first item that is not in registers
-    for (uint32_t i = tid + kItems * kPickThreads; i < items; i += kPickThreads) {
-        best = max(best, rank_item(w, g, __ldcg(maxima + i)));
-        next_item(w, g);
-    }
-    pick_best(
-        p, K, best,
-        [&](uint32_t least, auto&& take) {
-#pragma unroll
-            for (int k = 0; k < kItems; ++k)
-                if (rank[k] >= least) take(candidate(rank[k], tid + k * kPickThreads));
-            uint32_t iw = w8, ig = g8;
-            for (uint32_t i = tid + kItems * kPickThreads; i < items; i += kPickThreads) {
-                const uint32_t r = rank_item(iw, ig, __ldcg(maxima + i));
-                if (r >= least) take(candidate(r, i));
-                next_item(iw, ig);
+                    for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
+                    x[0] = 0.f;
+                } else if (reload) {
+                    load_maxima(w, g0);
+                }
+                const float2 b = p.base[w];
+                if (rank_of(b, largest()) >= least) take(w, g0, x);
+                if (is_ended) continue;
+#pragma unroll 1
+                for (int g = g0 + 32 * share * kChunk; g < G; g += 32 * share * kChunk) {
+                    load_maxima(w, g);
+                    reload = true;
+                    if (rank_of(b, largest()) >= least) take(w, g, x);
+                }
             }
         },
-        [&](int k, uint64_t c) { taken[k] = c; });
+        [&](int i) { return 32 * share * i; });
+    if (n > MLA_MAX_BEAMS) {   // (up to that many, more than K, are looked at as they are)
+        rank_list(p.list, n, K, [&](int k, uint64_t c) { groups[k] = c; });
+        n = K;
+    } else if (tid < n) {
+        groups[tid] = p.list[tid];
+    }
     __syncthreads();
 
     // the logits of a warp's groups, eight a lane
     uint4 v[kTurns][kPerGroup];
-    uint32_t column[kTurns], beam[kTurns], top[kTurns];
-    best = 0;
+    int beam[kTurns], column[kTurns];
 #pragma unroll
     for (int q = 0; q < kTurns; ++q) {
         const int k = warp + q * kPickWarps;
-        const uint64_t mine = k < K ? taken[k] : 0;
-        const uint32_t i = index_of(mine);
-        beam[q] = mine != 0 ? i / G : 0u;
-        column[q] = (i - beam[q] * G) * kGroup + lane * E;
-        top[q] = 0;
-        if (mine == 0) continue;
-        if ((ends >> beam[q]) & 1u) {
-            column[q] = a.end_token;
-            top[q] = lane == 0 ? rank_of(base[beam[q]], 0.f) : 0u;
+        beam[q] = -1;
+        if (k >= n) continue;
+        const uint64_t c = groups[k];
+        beam[q] = (int)beam_of(c);
+        column[q] = (int)place_of(c) * kGroup + lane * E;
+        if (p.ended[beam[q]] != 0) continue;
+        const T* row = static_cast<const T*>(a.logits) + (row0 + beam[q]) * a.row_stride;
+#pragma unroll
+        for (int z = 0; z < kPerGroup; ++z)
+            v[q][z] = load_piece<T, ALIGNED>(row, column[q] + z * 32 * E, a.vocab);
+    }
+    uint32_t top[kTurns];
+    auto unpack = [&](int q) {   // into x; an ended beam's one candidate is lane 0's
+        if (p.ended[beam[q]] != 0) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) x[i] = -INFINITY;
+            if (lane == 0) x[0] = 0.f;
         } else {
-            const T* x = static_cast<const T*>(a.logits) + (row0 + beam[q]) * a.row_stride;
-            float m = -INFINITY;
 #pragma unroll
             for (int z = 0; z < kPerGroup; ++z)
-                v[q][z] = load_piece<T, ALIGNED>(x, column[q] + z * 32 * E, a.vocab);
-#pragma unroll
-            for (int z = 0; z < kPerGroup; ++z) m = fmaxf(m, piece_max<T>(v[q][z]));
-            top[q] = rank_of(base[beam[q]], m);
+                each_logit<T>(v[q][z], [&](int i, float t) { x[z * E + i] = t; });
         }
-        best = max(best, top[q]);
+    };
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+        top[q] = 0;
+        if (beam[q] < 0) continue;
+        unpack(q);
+        top[q] = rank_of(p.base[beam[q]], largest());
     }
-    const int64_t out = (int64_t)blockIdx.x * K;
-    pick_best(
-        p, K, best,
-        [&](uint32_t least, auto&& take) {
+    if (least == 1)   // there were not K parts with groups
+        least = rank_of_part(p, 1, K, max(top[0], top[1]));
+    n = list_candidates(
+        p, 1, K, least,
+        [&](auto&& take) {
 #pragma unroll
             for (int q = 0; q < kTurns; ++q) {
                 if (top[q] < least) continue;
-                const uint32_t first = beam[q] * (uint32_t)a.vocab + column[q];
-                if ((ends >> beam[q]) & 1u) {
-                    take(candidate(top[q], first));
-                } else {
-#pragma unroll
-                    for (int z = 0; z < kPerGroup; ++z)
-                        each_logit<T>(v[q][z], [&](int i, float x) {
-                            const uint32_t r = rank_of(base[beam[q]], x);
-                            if (r >= least) take(candidate(r, first + z * 32 * E + i));
-                        });
-                }
+                unpack(q);
+                take(beam[q], p.ended[beam[q]] != 0 ? a.end_token : column[q], x);
             }
         },
-        [&](int k, uint64_t c) {
-            int token = -1, w = 0;
-            float score = -INFINITY;
-            bool end = true;
-            if (c != 0) {
-                const uint32_t i = index_of(c);
-                w = (int)(i / (uint32_t)a.vocab);
-                token = (int)(i - (uint32_t)w * a.vocab);
-                score = score_of(c);
-                end = token == a.end_token || ((ends >> w) & 1u) != 0;
-            }
-            a.tokens[out + k] = token;
-            a.parents[out + k] = (int32_t)(row0 + w);
-            a.scores_out[out + k] = score;
-            if (a.finished_out != nullptr) a.finished_out[out + k] = end ? 1 : 0;
-        });
-}
-
-template <typename T, bool ALIGNED, int PIECES>
-cudaError_t launch_scan(SelectArgs& a, cudaStream_t s)
-{
-    a.segments = (a.vocab + kSegment<T, PIECES> - 1) / kSegment<T, PIECES>;
-    const int64_t warps = a.rows * a.segments;
-    const int64_t ctas = (warps + kScanThreads / 32 - 1) / (kScanThreads / 32);
-    return launch_dependent(scan_kernel<T, ALIGNED, PIECES>, dim3((unsigned)ctas), kScanThreads, s,
-                            true, a);
+        [](int i) { return i / E * 32 * E + i % E; });
+    const int64_t out = (int64_t)blockIdx.x * K;
+    auto put = [&](int k, int token, int w, float score, bool end) {
+        a.tokens[out + k] = token;
+        a.parents[out + k] = (int32_t)(row0 + w);
+        a.scores_out[out + k] = score;
+        if (a.finished_out != nullptr) a.finished_out[out + k] = end ? 1 : 0;
+    };
+    rank_list(p.list, n, K, [&](int k, uint64_t c) {
+        const int w = (int)beam_of(c), token = (int)place_of(c);
+        put(k, token, w, score_of(c), token == a.end_token || p.ended[w] != 0);
+    });
+    if (tid >= n && tid < K) put(tid, -1, 0, -INFINITY, true);
 }
 
 // Segments of 1 KB instead of 4 while they are no more than the GPU's SMs hold at a time.
-constexpr int64_t kShortWarps = 152 * 32;
+constexpr int64_t kShortWarps = 152 * 48;
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_select(SelectArgs a, cudaStream_t s)
 {
-    const int64_t n = kSegment<T, kShortPieces>;
-    const bool small = a.rows * ((a.vocab + n - 1) / n) <= kShortWarps;
-    const cudaError_t e = small ? launch_scan<T, ALIGNED, kShortPieces>(a, s)
-                                : launch_scan<T, ALIGNED, kLongPieces>(a, s);
+    constexpr int kFew = kSegment<T, kShortPieces>, kMany = kSegment<T, kLongPieces>;
+    const int64_t few = a.rows * ((a.vocab + kFew - 1) / kFew);
+    const bool small = few <= kShortWarps;
+    a.segments = (a.vocab + (small ? kFew : kMany) - 1) / (small ? kFew : kMany);
+    const int64_t ctas = (a.rows * a.segments + kScanThreads / 32 - 1) / (kScanThreads / 32);
+    const cudaError_t e =
+        launch_dependent(small ? scan_kernel<T, ALIGNED, kShortPieces> : scan_kernel<T, ALIGNED, kLongPieces>,
+                         dim3((unsigned)ctas), kScanThreads, s, true, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(pick_kernel<T, ALIGNED>, dim3((unsigned)a.batch), kPickThreads, s, true, a);
 }
@@ -694,10 +798,10 @@ reorder_kernel(const ReorderArgs a)
 //   sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
 //   fill   a thread per entry of the new table and per token.
 
-constexpr int kExtendThreads = 256;
+constexpr int kExtendThreads = 512;
 constexpr int kExtendRequests = 2048;   // 32 KB of sums
 constexpr int kExtendSpan = 8;          // entries in flight per thread
-constexpr int kExtendCtas = 4 * 152;
+constexpr int kExtendCtas = 2 * 152;
 constexpr int kLeadTokens = 2048;       // that one CTA takes
 constexpr int kSumThreads = 1024;
 constexpr int kFillThreads = 256;
@@ -905,12 +1009,12 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
 
     // a warp's part of the table, and the requests in it
     constexpr int kSpan = 32 * kExtendSpan;   // entries at a time
-    const int warps = ((int)gridDim.x - 1) * (kExtendThreads / 32);
-    const int warp = ((int)blockIdx.x - 1) * (kExtendThreads / 32) + (tid >> 5);
-    const int64_t run = ((int64_t)total + (int64_t)warps * kSpan - 1) / ((int64_t)warps * kSpan) * kSpan;
-    const int64_t begin = warp * run;
-    if (begin >= total) return;
-    const int32_t end = (int32_t)min(begin + run, (int64_t)total);
+    const uint32_t warps = (gridDim.x - 1) * (kExtendThreads / 32);
+    const uint32_t warp = (blockIdx.x - 1) * (kExtendThreads / 32) + (tid >> 5);
+    const uint32_t run = ((uint32_t)total + warps * kSpan - 1) / (warps * kSpan) * kSpan;
+    const uint32_t begin = warp * run;   // at most total + warps * kSpan
+    if (begin >= (uint32_t)total) return;
+    const int32_t end = (int32_t)min(begin + run, (uint32_t)total);
     int lo = last_at_most(start, 0, F, (int32_t)begin);
     for (int32_t i0 = (int32_t)begin; i0 < end; i0 += kSpan) {
         const int32_t past = min(i0 + kSpan, end);

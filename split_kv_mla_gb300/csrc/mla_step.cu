@@ -35,12 +35,13 @@ namespace {
 // so equal rows give equal sums and their equal candidates are taken by their index.
 
 constexpr int kGroup = 256;             // columns
-constexpr int kLongPieces = 8;          // 16-byte loads of a lane per segment, of large calls
-constexpr int kShortPieces = 2;         // and of small ones
+constexpr int kShortPieces = 2, kMiddlePieces = 4, kLongPieces = 8;   // 16-byte loads of a lane
+                                                                    // per segment
 constexpr int kScanThreads = 256;
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickList = 1024;
+constexpr int kParts = 4;               // of a row, that a lane of pick asks for at once
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kPlaceBits = 20;          // of a column
 static_assert(kMaxVocab <= 1 << kPlaceBits && MLA_MAX_BEAMS <= 1 << (32 - kPlaceBits), "");
@@ -474,7 +475,6 @@ pick_kernel(const SelectArgs a)
 {
     constexpr int E = kElements<T>;
     constexpr int kPerGroup = kGroup / (32 * E);
-    constexpr int kParts = 4;      // parts of a row, of a lane
     constexpr int kTurns = MLA_MAX_BEAMS / kPickWarps;
     static_assert(kPerGroup * E == kChunk, "a lane's logits of a group are one chunk");
     __shared__ Picker p;
@@ -509,8 +509,7 @@ pick_kernel(const SelectArgs a)
         return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
     };
-    uint32_t top0 = 0, top1 = 0;   // largest rank of the thread's beams
-    static_assert(kTurns == 2, "");
+    uint32_t best = 0;   // largest rank of the thread's beams
 #pragma unroll 1
     for (int w = beam0; w < W; w += kPickWarps) {
         const int64_t row = row0 + w;
@@ -528,14 +527,14 @@ pick_kernel(const SelectArgs a)
         float m = -INFINITY, s = 0.f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) m = fmaxf(m, t[k].x);
-#pragma unroll 1
+#pragma unroll 4
         for (int i = lane + 32 * kParts; i < a.segments; i += 32) m = fmaxf(m, __ldcg(parts + i).x);
         m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
         const float ref = m == -INFINITY ? 0.f : m;
         constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) s += t[k].y * ex2_approx((t[k].x - ref) * kLog2e);
-#pragma unroll 1
+#pragma unroll 4
         for (int i = lane + 32 * kParts; i < a.segments; i += 32) {
             const float2 u = __ldcg(parts + i);
             s += u.y * ex2_approx((u.x - ref) * kLog2e);
@@ -562,27 +561,26 @@ pick_kernel(const SelectArgs a)
         float most = largest();
         if (!is_ended) {
             const float* maxima = a.group_max + row * G;
-#pragma unroll 1
+#pragma unroll 4
             for (int g = g0 + 32 * share * kChunk; g < G; g += 32 * share)
                 most = fmaxf(most, __ldcg(maxima + g));
         }
-        (w < kPickWarps ? top0 : top1) = rank_of(b, most);
+        best = max(best, rank_of(b, most));
     }
-    uint32_t least = rank_of_part(p, 0, K, max(top0, top1));
+    uint32_t least = rank_of_part(p, 0, K, best);
 
     bool reload = W > kPickWarps;   // (of two beams only the last's maxima are there)
     int n = list_candidates(
         p, 0, K, least,
         [&](auto&& take) {
 #pragma unroll 1
-            for (int w = beam0; w < W; w += kPickWarps) {
-                if ((w < kPickWarps ? top0 : top1) < least) continue;
+            for (int w = beam0; best >= least && w < W; w += kPickWarps) {
                 const int g0 = first_group(w);
                 const bool is_ended = p.ended[w] != 0;
                 if (is_ended) {
 #pragma unroll
                     for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
-                    x[0] = 0.f;
+                    if (g0 == 0) x[0] = 0.f;
                 } else if (reload) {
                     load_maxima(w, g0);
                 }
@@ -669,20 +667,32 @@ pick_kernel(const SelectArgs a)
     if (tid >= n && tid < K) put(tid, -1, 0, -INFINITY, true);
 }
 
-// Segments of 1 KB instead of 4 while they are no more than the GPU's SMs hold at a time.
-constexpr int64_t kShortWarps = 152 * 48;
+// Segments are as long as leaves the GPU's SMs a wave of warps, 64 each: 4 KB, 2 or 1; and
+// not so short that a row has more parts than pick asks for at once.
+// (us per call with 4 / 2 / 1 KB: 64 x 8 beams of 131072 fp32 logits 50.0 / 52.0 / -,
+// 32 x 4 of 100003 fp16 13.5 / 12.4 / 14.4, 8 x 8 of 50001 bf16 15.0 / - / 10.6.)
+constexpr int64_t kScanWarps = 152 * 64;
+
+template <typename T, bool ALIGNED, int PIECES>
+cudaError_t launch_scan(SelectArgs& a, cudaStream_t s)
+{
+    a.segments = (a.vocab + kSegment<T, PIECES> - 1) / kSegment<T, PIECES>;
+    const int64_t ctas = (a.rows * a.segments + kScanThreads / 32 - 1) / (kScanThreads / 32);
+    return launch_dependent(scan_kernel<T, ALIGNED, PIECES>, dim3((unsigned)ctas), kScanThreads, s,
+                            true, a);
+}
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_select(SelectArgs a, cudaStream_t s)
 {
-    constexpr int kFew = kSegment<T, kShortPieces>, kMany = kSegment<T, kLongPieces>;
-    const int64_t few = a.rows * ((a.vocab + kFew - 1) / kFew);
-    const bool small = few <= kShortWarps;
-    a.segments = (a.vocab + (small ? kFew : kMany) - 1) / (small ? kFew : kMany);
-    const int64_t ctas = (a.rows * a.segments + kScanThreads / 32 - 1) / (kScanThreads / 32);
+    auto parts = [&](int64_t columns) { return (a.vocab + columns - 1) / columns; };   // of a row
+    const int64_t many = parts(kSegment<T, kLongPieces>), some = parts(kSegment<T, kMiddlePieces>),
+                  few = parts(kSegment<T, kShortPieces>);
     const cudaError_t e =
-        launch_dependent(small ? scan_kernel<T, ALIGNED, kShortPieces> : scan_kernel<T, ALIGNED, kLongPieces>,
-                         dim3((unsigned)ctas), kScanThreads, s, true, a);
+        a.rows * many >= kScanWarps || some > 32 * kParts ? launch_scan<T, ALIGNED, kLongPieces>(a, s)
+        : a.rows * some >= kScanWarps || few > 32 * kParts
+            ? launch_scan<T, ALIGNED, kMiddlePieces>(a, s)
+            : launch_scan<T, ALIGNED, kShortPieces>(a, s);
     if (e != cudaSuccess) return e;
     return launch_dependent(pick_kernel<T, ALIGNED>, dim3((unsigned)a.batch), kPickThreads, s, true, a);
 }
@@ -703,13 +713,13 @@ bool select_shape_ok(int64_t batch, int64_t beams, int64_t vocab)
 
 int64_t select_groups(int64_t vocab) { return (vocab + kGroup - 1) / kGroup; }
 
-// Bytes of the segments' parts: short segments are no more than kShortWarps, long ones
-// most for fp32.
+// Bytes of the segments' parts.  Segments shorter than the longest are taken while those of
+// twice their length are less than a wave.
 int64_t select_part_bytes(int64_t rows, int64_t vocab)
 {
     const int64_t n = kSegment<float, kLongPieces>;
     const int64_t parts = rows * ((vocab + n - 1) / n);
-    return align256((parts > kShortWarps ? parts : kShortWarps) * (int64_t)sizeof(float2));
+    return align256((parts > 2 * kScanWarps ? parts : 2 * kScanWarps) * (int64_t)sizeof(float2));
 }
 
 // ---- beam state reordering ------------------------------------------------------------------

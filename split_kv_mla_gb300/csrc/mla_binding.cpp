@@ -506,15 +506,16 @@ PyObject* cache_extend(PyObject*, PyObject* const* v, Py_ssize_t n)
         if (parents.defined() && F == 0) pa = kp;
         const int64_t sizes[7] = {total, F + 1, F, T, T, F + 1, 1};
         int32_t* to[7];
-        Parts parts;   // all but the table
-        for (int i = 1; i < 7; ++i)
+        Parts parts;   // all but a large table, which would live as long as any of them
+        const bool large = total > 1 << 18;
+        for (int i = large ? 1 : 0; i < 7; ++i)
             if (!out[i].defined()) parts.add(sizes[i], at::kInt);
         for (int i = 0; i < 7; ++i) {
             if (out[i].defined() && out[i].numel() < sizes[i])
                 bad(std::string(names[i]) + " must have " + std::to_string(sizes[i]) + " entries");
             if (!out[i].defined())
-                out[i] = i == 0 ? allocate({total}, at::kInt, dev)
-                                : parts.take({sizes[i]}, at::kInt, dev);
+                out[i] = i == 0 && large ? allocate({total}, at::kInt, dev)
+                                         : parts.take({sizes[i]}, at::kInt, dev);
             to[i] = static_cast<int32_t*>(address(out[i], names[i], at::kInt, dev));
         }
         void* pw = address(ws, "workspace", at::kByte, dev);

@@ -96,6 +96,12 @@ LENS = dict(lens=BUF + 4 * FAR)
     (INVALID, dict(out=BUF + 63, state_stride=128, out_stride=128)),
     (INVALID, dict(out=BUF + 65, state_stride=128, out_stride=128)),
     (INVALID, dict(out=BUF, state_stride=0)),
+    # outputs over the other inputs and each other
+    (INVALID, dict(out=BUF + FAR - 255)), (INVALID, dict(out=BUF + 4 * FAR, **LENS)),
+    (INVALID, dict(tokens=BUF + 2 * FAR + 192, **LENS)),
+    (INVALID, dict(out_lens=BUF + 4 * FAR + 12, **LENS)),
+    (INVALID, dict(out_lens=BUF + FAR + 12, **LENS)),
+    (INVALID, dict(out_lens=BUF + 2 * FAR - 12, **LENS)),
     (0, dict(num_rows=0)), (0, dict(num_rows=0, parents=None, state=None, out=None))])
 def test_reorder_refusals(lib, want, kw):
     assert reorder(lib, **kw) == want

@@ -154,37 +154,79 @@ __device__ __noinline__ uint4 load_edge(const T* row, int col, int vocab)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The same.  Pieces of an aligned row are one load.  Otherwise a piece lies in two
-// aligned ones, and is shifted out of them where both are inside the row.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ uint4 load_piece(const T* row, int col, int vocab)
+// Segment `seg` of a row, -inf behind the row's end: PIECES of a lane.  Of an aligned row a
+// lane's piece is 16 bytes, neighbours in neighbouring lanes.  Otherwise, in every row of
+// the call, its words are 128 bytes apart, and those of a row of 16-bit logits that
+// starts on an odd one are shifted out of two.  (Pieces shifted out of two aligned ones
+// took 31 us a call for 57 MB, this way it is 21.)
+template <typename T, int PIECES>
+struct Segment {
+    uint4 v[PIECES];
+};
+
+template <typename T, bool ALIGNED, int PIECES>
+__device__ __forceinline__ void load_segment(const SelectArgs& a, int64_t row, int seg, int lane,
+                                             Segment<T, PIECES>& s)
 {
+    constexpr int E = kElements<T>;
+    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
+    const int c0 = seg * kSegment<T, PIECES>;
     if constexpr (ALIGNED) {
-        if (col + kElements<T> <= vocab)
-            return __ldcs(reinterpret_cast<const uint4*>(row + col));
-    } else {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
-        const uint32_t off = (uint32_t)at & 15u;
-        const uintptr_t from = at - off;
-        if (from >= reinterpret_cast<uintptr_t>(row) &&
-            from + 32 <= reinterpret_cast<uintptr_t>(row + vocab)) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(from));
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(from) + 1);
-            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            if (off & 8u) {
 #pragma unroll
-                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (off & 4u) {
-#pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-            }
-            const uint32_t s = (off & 2u) * 8u;
-            return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
-                              __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+        for (int p = 0; p < PIECES; ++p) {
+            const int col = c0 + (p * 32 + lane) * E;
+            s.v[p] = col + E <= a.vocab ? __ldcs(reinterpret_cast<const uint4*>(x + col))
+                                        : load_edge(x, col, a.vocab);
         }
+    } else {
+        constexpr int N = 4 * PIECES;
+        uint32_t w[N];
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(x) + c0 + lane;
+            const int left = a.vocab - c0 - lane;
+#pragma unroll
+            for (int k = 0; k < N; ++k) w[k] = 32 * k < left ? __ldcs(p + 32 * k) : 0xFF800000u;
+        } else {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(x + c0);
+            const int odd = (int)(at >> 1) & 1;
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(at - 2 * odd) + lane;
+            if (c0 - odd < 0 || c0 + kSegment<T, PIECES> + odd > a.vocab) {   // the row's ends
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(x) + c0 + 2 * lane;
+                const int left = a.vocab - c0 - 2 * lane;
+                constexpr uint32_t none = LogitType<T>::kNone;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const uint32_t lo = 64 * k < left ? __ldg(h + 64 * k) : none;
+                    const uint32_t hi = 64 * k + 1 < left ? __ldg(h + 64 * k + 1) : none;
+                    w[k] = lo | hi << 16;
+                }
+            } else if (odd) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    w[k] = __funnelshift_r(__ldg(p + 32 * k), __ldg(p + 32 * k + 1), 16);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) w[k] = __ldcs(p + 32 * k);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q)
+            s.v[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     }
-    return load_edge(row, col, vocab);
+}
+
+// The column of a lane's i-th logit of a segment, from the lane's first on, and that.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ int column_step(int i)
+{
+    constexpr int E = kElements<T>, N = E / 4;   // logits of a word
+    return ALIGNED ? i / E * 32 * E + i % E : i / N * 32 * N + i % N;
+}
+
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ int first_column(int lane)
+{
+    return lane * (ALIGNED ? kElements<T> : kElements<T> / 4);
 }
 
 // Floats as integers in the same order.
@@ -203,22 +245,6 @@ __device__ __forceinline__ bool row_is_live(const SelectArgs& a, int64_t row)
 {
     return __ldg(a.scores + row) != -INFINITY &&
            (a.finished == nullptr || __ldg(a.finished + row) == 0);
-}
-
-template <typename T, int PIECES>
-struct Segment {
-    uint4 v[PIECES];
-};
-
-template <typename T, bool ALIGNED, int PIECES>
-__device__ __forceinline__ void load_segment(const SelectArgs& a, int64_t row, int seg, int lane,
-                                             Segment<T, PIECES>& s)
-{
-    constexpr int E = kElements<T>;
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    const int c0 = seg * kSegment<T, PIECES> + lane * E;
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p) s.v[p] = load_piece<T, ALIGNED>(x, c0 + p * 32 * E, a.vocab);
 }
 
 // A segment's group maxima and its part.
@@ -352,6 +378,7 @@ __device__ __forceinline__ int next_place(int* count)
 
 constexpr int kChunk = 8;          // candidates of a thread at a time
 constexpr int kPickSlots = 256;
+constexpr int kManyThreads = 48;
 
 struct Picker {
     uint32_t best[2][32];               // of each part: of the groups, of the logits
@@ -614,7 +641,7 @@ pick_kernel(const SelectArgs a)
     __syncthreads();
 
     // the logits of a warp's groups, eight a lane
-    uint4 v[kTurns][kPerGroup];
+    Segment<T, kPerGroup> v[kTurns];
     int beam[kTurns], column[kTurns];
 #pragma unroll
     for (int q = 0; q < kTurns; ++q) {
@@ -622,13 +649,11 @@ pick_kernel(const SelectArgs a)
         beam[q] = -1;
         if (k >= n) continue;
         const uint64_t c = groups[k];
+        const int g = (int)place_of(c);
         beam[q] = (int)beam_of(c);
-        column[q] = (int)place_of(c) * kGroup + lane * E;
-        if (p.ended[beam[q]] != 0) continue;
-        const T* row = static_cast<const T*>(a.logits) + (row0 + beam[q]) * a.row_stride;
-#pragma unroll
-        for (int z = 0; z < kPerGroup; ++z)
-            v[q][z] = load_piece<T, ALIGNED>(row, column[q] + z * 32 * E, a.vocab);
+        column[q] = g * kGroup + first_column<T, ALIGNED>(lane);
+        if (p.ended[beam[q]] == 0)
+            load_segment<T, ALIGNED, kPerGroup>(a, row0 + beam[q], g, lane, v[q]);
     }
     uint32_t top[kTurns];
     auto unpack = [&](int q) {   // into x; an ended beam's one candidate is lane 0's
@@ -639,7 +664,7 @@ pick_kernel(const SelectArgs a)
         } else {
 #pragma unroll
             for (int z = 0; z < kPerGroup; ++z)
-                each_logit<T>(v[q][z], [&](int i, float t) { x[z * E + i] = t; });
+                each_logit<T>(v[q].v[z], [&](int i, float t) { x[z * E + i] = t; });
         }
     };
 #pragma unroll
@@ -649,8 +674,10 @@ pick_kernel(const SelectArgs a)
         unpack(q);
         top[q] = rank_of(p.base[beam[q]], largest());
     }
-    if (least == 1)   // there were not K parts with groups
-        least = rank_of_part(p, 1, K, max(top[0], top[1]));
+    // Where few groups hold most of the best (beams far ahead of the others, of a small
+    // vocabulary), the groups' bound leaves many logits, and theirs is needed.
+    best = max(top[0], top[1]);
+    if (__syncthreads_count(best >= least) > kManyThreads) least = max(least, rank_of_part(p, 1, K, best));
     n = list_candidates(
         p, 1, K, least,
         [&](auto&& take) {
@@ -661,7 +688,7 @@ pick_kernel(const SelectArgs a)
                 take(beam[q], p.ended[beam[q]] != 0 ? a.end_token : column[q], x);
             }
         },
-        [](int i) { return i / E * 32 * E + i % E; });
+        [](int i) { return column_step<T, ALIGNED>(i); });
     const int64_t out = (int64_t)blockIdx.x * K;
     auto put = [&](int k, int token, int w, float score, bool end) {
         a.tokens[out + k] = token;

@@ -440,9 +440,12 @@ __device__ __forceinline__ int list_candidates(Picker& p, int round, int K, uint
                 p.beam[at] = beam;
                 p.place[at] = place;
             } else {
+#pragma unroll 1
+                for (int i = 0; i < kChunk; ++i) {   // (short code: it is rarely reached)
+                    float xi = x[0];
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) {
-                    const uint32_t r = rank_of(p.base[beam], x[i]);
+                    for (int j = 1; j < kChunk; ++j) xi = i == j ? x[j] : xi;
+                    const uint32_t r = rank_of(p.base[beam], xi);
                     const uint64_t c = candidate(r, beam, place + step(i));
                     if (r >= least && c < last && c > next) next = c;
                 }
@@ -603,59 +606,11 @@ pick_kernel(const SelectArgs a)
         }
         best = max(best, rank_of(b, most));
     }
-    uint32_t least = rank_of_part(p, 0, K, best);
-
-    bool reload = W > kPickWarps;   // (of two beams only the last's maxima are there)
-    int n = list_candidates(
-        p, 0, K, least,
-        [&](auto&& take) {
-#pragma unroll 1
-            for (int w = beam0; best >= least && w < W; w += kPickWarps) {
-                const int g0 = first_group(w);
-                const bool is_ended = p.ended[w] != 0;
-                if (is_ended) {
-#pragma unroll
-                    for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
-                    if (g0 == 0) x[0] = 0.f;
-                } else if (reload) {
-                    load_maxima(w, g0);
-                }
-                const float2 b = p.base[w];
-                if (rank_of(b, largest()) >= least) take(w, g0, x);
-                if (is_ended) continue;
-#pragma unroll 1
-                for (int g = g0 + 32 * share * kChunk; g < G; g += 32 * share * kChunk) {
-                    load_maxima(w, g);
-                    reload = true;
-                    if (rank_of(b, largest()) >= least) take(w, g, x);
-                }
-            }
-        },
-        [&](int i) { return 32 * share * i; });
-    if (n > MLA_MAX_BEAMS) {   // (up to that many, more than K, are looked at as they are)
-        rank_list(p.list, n, K, [&](int k, uint64_t c) { groups[k] = c; });
-        n = K;
-    } else if (tid < n) {
-        groups[tid] = p.list[tid];
-    }
-    __syncthreads();
-
-    // the logits of a warp's groups, eight a lane
-    Segment<T, kPerGroup> v[kTurns];
-    int beam[kTurns], column[kTurns];
-#pragma unroll
-    for (int q = 0; q < kTurns; ++q) {
-        const int k = warp + q * kPickWarps;
-        beam[q] = -1;
-        if (k >= n) continue;
-        const uint64_t c = groups[k];
-        const int g = (int)place_of(c);
-        beam[q] = (int)beam_of(c);
-        column[q] = g * kGroup + first_column<T, ALIGNED>(lane);
-        if (p.ended[beam[q]] == 0)
-            load_segment<T, ALIGNED, kPerGroup>(a, row0 + beam[q], g, lane, v[q]);
-    }
-    uint32_t top[kTurns];
+    // Round 0 finds the groups, round 1 their logits.  (One copy of the code for both: a
+    // jump to code for the first time is 700 cycles.)
+    Segment<T, kPerGroup> v[kTurns];   // a warp's groups, eight logits a lane
+    int beam[kTurns] = {}, column[kTurns] = {}, n = 0;
+    uint32_t top[kTurns] = {}, least = 1;
     auto unpack = [&](int q) {   // into x; an ended beam's one candidate is lane 0's
         if (p.ended[beam[q]] != 0) {
 #pragma unroll
@@ -667,28 +622,80 @@ pick_kernel(const SelectArgs a)
                 each_logit<T>(v[q].v[z], [&](int i, float t) { x[z * E + i] = t; });
         }
     };
-#pragma unroll
-    for (int q = 0; q < kTurns; ++q) {
-        top[q] = 0;
-        if (beam[q] < 0) continue;
-        unpack(q);
-        top[q] = rank_of(p.base[beam[q]], largest());
-    }
-    // Where few groups hold most of the best (beams far ahead of the others, of a small
-    // vocabulary), the groups' bound leaves many logits, and theirs is needed.
-    best = max(top[0], top[1]);
-    if (__syncthreads_count(best >= least) > kManyThreads) least = max(least, rank_of_part(p, 1, K, best));
-    n = list_candidates(
-        p, 1, K, least,
-        [&](auto&& take) {
+    bool reload = W > kPickWarps;   // (of two beams only the last's maxima are there)
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        bool bound = true;
+        if (round == 1) {
 #pragma unroll
             for (int q = 0; q < kTurns; ++q) {
-                if (top[q] < least) continue;
-                unpack(q);
-                take(beam[q], p.ended[beam[q]] != 0 ? a.end_token : column[q], x);
+                const int k = warp + q * kPickWarps;
+                beam[q] = -1;
+                if (k >= n) continue;
+                const uint64_t c = groups[k];
+                const int g = (int)place_of(c);
+                beam[q] = (int)beam_of(c);
+                column[q] = g * kGroup + first_column<T, ALIGNED>(lane);
+                if (p.ended[beam[q]] == 0)
+                    load_segment<T, ALIGNED, kPerGroup>(a, row0 + beam[q], g, lane, v[q]);
             }
-        },
-        [](int i) { return column_step<T, ALIGNED>(i); });
+            best = 0;
+#pragma unroll
+            for (int q = 0; q < kTurns; ++q) {
+                top[q] = 0;
+                if (beam[q] < 0) continue;
+                unpack(q);
+                top[q] = rank_of(p.base[beam[q]], largest());
+                best = max(best, top[q]);
+            }
+            // Where few groups hold most of the best (beams far ahead of the others, of a
+            // small vocabulary), the groups' bound leaves many logits, and theirs is needed.
+            bound = __syncthreads_count(best >= least) > kManyThreads;
+        }
+        if (bound) least = max(least, rank_of_part(p, round, K, best));
+        n = list_candidates(
+            p, round, K, least,
+            [&](auto&& take) {
+                if (best < least) return;
+                if (round == 1) {
+#pragma unroll
+                    for (int q = 0; q < kTurns; ++q) {
+                        if (top[q] < least) continue;
+                        unpack(q);
+                        take(beam[q], p.ended[beam[q]] != 0 ? a.end_token : column[q], x);
+                    }
+                    return;
+                }
+#pragma unroll 1
+                for (int w = beam0; w < W; w += kPickWarps) {
+                    const int g0 = first_group(w);
+                    const bool is_ended = p.ended[w] != 0;
+                    if (is_ended) {
+#pragma unroll
+                        for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
+                        if (g0 == 0) x[0] = 0.f;
+                    }
+                    const float2 b = p.base[w];
+#pragma unroll 1
+                    for (int g = g0; g < G; g += 32 * share * kChunk) {
+                        if (reload && !is_ended) load_maxima(w, g);
+                        if (rank_of(b, largest()) >= least) take(w, g, x);
+                        if (is_ended) break;
+                        reload = reload || g + 32 * share * kChunk < G;
+                    }
+                }
+            },
+            [&](int i) { return round == 0 ? 32 * share * i : column_step<T, ALIGNED>(i); });
+        if (round == 1) break;
+        // (up to 32 groups, more than K, are looked at as they are)
+        if (n > MLA_MAX_BEAMS) {
+            rank_list(p.list, n, K, [&](int k, uint64_t c) { groups[k] = c; });
+            n = K;
+        } else if (tid < n) {
+            groups[tid] = p.list[tid];
+        }
+        __syncthreads();
+    }
     const int64_t out = (int64_t)blockIdx.x * K;
     auto put = [&](int k, int token, int w, float score, bool end) {
         a.tokens[out + k] = token;

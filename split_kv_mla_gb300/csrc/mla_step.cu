@@ -768,7 +768,10 @@ int64_t select_part_bytes(int64_t rows, int64_t vocab)
 // ---- beam state reordering ------------------------------------------------------------------
 //
 // A copy: bounded by HBM for large states, by latency for small ones.  A CTA takes a
-// part of one row.  Units are the largest that both tensors' rows are aligned to.
+// part of one row, in 16-byte pieces of out.  Where rows of state and out do not lie at the
+// same place of 16 bytes, a piece is shifted out of two aligned ones of state (512 rows of
+// 65535 bf16: 21.5 us, 43.7 by the 2 bytes that they are aligned to, 19 for 65536), and
+// the few bytes at a row's ends are copied one by one.
 
 constexpr int kReorderThreads = 256;
 constexpr int kReorderTurns = 4;   // units in flight per thread
@@ -790,7 +793,24 @@ struct ReorderArgs {
     uint32_t* err;
 };
 
-template <typename U>
+// Bytes [shift, shift + 16) of two pieces, 0 < shift < 16.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t shift)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (shift & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (shift & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t s = (shift & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                      __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+
+template <bool ALIGNED>
 __global__ void __launch_bounds__(kReorderThreads)
 reorder_kernel(const ReorderArgs a)
 {
@@ -821,23 +841,51 @@ reorder_kernel(const ReorderArgs a)
         }
     }
     const uint8_t* in = a.state + p * a.state_stride;
-    const int64_t units = bytes / (int64_t)sizeof(U);
-    const U* from = reinterpret_cast<const U*>(in);
-    U* to = reinterpret_cast<U*>(out);
-    const int64_t step = (int64_t)a.parts * kReorderThreads * kReorderTurns;
-    for (int64_t i = (int64_t)part * (kReorderThreads * kReorderTurns) + threadIdx.x; i < units;
-         i += step) {
-        U v[kReorderTurns];
-#pragma unroll
-        for (int k = 0; k < kReorderTurns; ++k)
-            if (i + k * kReorderThreads < units) v[k] = __ldg(from + i + k * kReorderThreads);
-#pragma unroll
-        for (int k = 0; k < kReorderTurns; ++k)
-            if (i + k * kReorderThreads < units) to[i + k * kReorderThreads] = v[k];
+    // pieces [begin, end) of out from its byte `head` on, of which piece j is shifted out of
+    // pieces j and j + 1 of state from its byte head - shift on, both inside the row
+    int64_t head = 0, begin = 0, end = bytes / 16;
+    uint32_t shift = 0;
+    if constexpr (!ALIGNED) {
+        head = (int64_t)((16u - (uint32_t)reinterpret_cast<uintptr_t>(out)) & 15u);
+        if (head > bytes) head = bytes;
+        end = (bytes - head) / 16;
+        shift = (uint32_t)reinterpret_cast<uintptr_t>(in + head) & 15u;
+        if (shift != 0) {
+            begin = head < (int64_t)shift ? 1 : 0;
+            const int64_t whole = (a.row_bytes - head + shift) / 16 - 1;
+            end = end < whole ? end : whole;
+        }
+        if (end <= begin) begin = end = 0;
     }
-    // what is left of the last unit
-    const int64_t at = units * (int64_t)sizeof(U) + threadIdx.x;
-    if (part == 0 && at < bytes) out[at] = in[at];
+    const uint4* from = reinterpret_cast<const uint4*>(in + head - shift);
+    uint4* to = reinterpret_cast<uint4*>(out + head);
+    const int64_t step = (int64_t)a.parts * kReorderThreads * kReorderTurns;
+    for (int64_t i = begin + (int64_t)part * (kReorderThreads * kReorderTurns) + threadIdx.x; i < end;
+         i += step) {
+        uint4 v[kReorderTurns];
+        if (ALIGNED || shift == 0) {
+#pragma unroll
+            for (int k = 0; k < kReorderTurns; ++k)
+                if (i + k * kReorderThreads < end) v[k] = __ldg(from + i + k * kReorderThreads);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kReorderTurns; ++k)
+                if (i + k * kReorderThreads < end) {
+                    const uint4* q = from + i + k * kReorderThreads;
+                    v[k] = shifted(__ldg(q), __ldg(q + 1), shift);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < kReorderTurns; ++k)
+            if (i + k * kReorderThreads < end) to[i + k * kReorderThreads] = v[k];
+    }
+    // what lies before and behind those, at most 31 and 63 bytes
+    if (part == 0) {
+        const int64_t before = begin == end ? 0 : head + begin * 16;
+        const int64_t behind = begin == end ? 0 : head + end * 16;
+        if ((int64_t)threadIdx.x < before) out[threadIdx.x] = in[threadIdx.x];
+        for (int64_t at = behind + threadIdx.x; at < bytes; at += kReorderThreads) out[at] = in[at];
+    }
 }
 
 // ---- cache extension --------------------------------------------------------------------------
@@ -845,8 +893,8 @@ reorder_kernel(const ReorderArgs a)
 // Bytes: 8 per entry that is kept, 12 (16 with a list of free slots) per token.
 // Every CTA sums the requests' lengths and counts by itself, in shared memory, and
 // fills its part of the new table from there: one launch.  A kernel that left the sums
-// for a second one took 7.5 us where this takes 4.9 (8 requests of 8192), and looking a
-// request up in global memory, per entry, 103 us where this takes 9 (512 of 1024 to
+// for a second one took 7.5 us where this takes 4.2 (8 requests of 8192), and looking a
+// request up in global memory, per entry, 103 us where this takes 8.6 (512 of 1024 to
 // 8192).  More requests than shared memory is given for go that way:
 //   sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
 //   fill   a thread per entry of the new table and per token.
@@ -970,8 +1018,10 @@ __device__ __forceinline__ int last_at_most(const int32_t* start, int lo, int hi
 // CTA 0 writes what is per request, and with `spread` false all of what is per token,
 // so that it alone reads the cursor that it then moves (which may be one and the
 // same); the others copy.
+// (Four CTAs on an SM for short spans: with three, at 40 registers, the next call's CTAs
+// start later, 7.4 us a call instead of 6.6 for 1.1 million entries.)
 template <int SPAN>
-__global__ void __launch_bounds__(kExtendThreads)
+__global__ void __launch_bounds__(kExtendThreads, SPAN == kShortSpan ? 4 : 0)
 extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
 {
     extern __shared__ int32_t sums[];
@@ -1065,7 +1115,8 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
     constexpr int kSpan = 32 * SPAN;   // entries at a time
     const uint32_t warps = (gridDim.x - 1) * (kExtendThreads / 32);
     const uint32_t warp = (blockIdx.x - 1) * (kExtendThreads / 32) + (tid >> 5);
-    const uint32_t run = ((uint32_t)total + warps * kSpan - 1) / (warps * kSpan) * kSpan;
+    uint32_t run = ((uint32_t)total + warps - 1) / warps;
+    run = run > kSpan ? (run + kSpan - 1) / kSpan * kSpan : (run + 31) / 32 * 32;
     const uint32_t begin = warp * run;   // at most total + warps * kSpan
     if (begin >= (uint32_t)total) return;
     const int32_t end = (int32_t)min(begin + run, (uint32_t)total);
@@ -1342,20 +1393,13 @@ int mla_beam_reorder(const void* state, int64_t state_stride, int32_t num_parent
     ReorderArgs a{static_cast<const uint8_t*>(state), state_stride, num_parents, row_bytes,
                   elem_bytes, parents, num_rows, lens, tokens, static_cast<uint8_t*>(out),
                   out_stride, out_lens, 1, static_cast<uint32_t*>(workspace)};
-    const int unit = (bits & 15u) == 0 ? 16 : (bits & 7u) == 0 ? 8 : (bits & 3u) == 0 ? 4
-                                                       : (bits & 1u) == 0 ? 2 : 1;
-    const int64_t per = (int64_t)unit * kReorderThreads * kReorderTurns;
+    const int64_t per = (int64_t)16 * kReorderThreads * kReorderTurns;
     const int64_t parts = (row_bytes + per - 1) / per;
     const int64_t most = INT32_MAX / num_rows;   // CTAs of the grid; a CTA loops over the rest
     a.parts = (uint32_t)(parts < 1 ? 1 : parts < most ? parts : most);
     const dim3 grid((unsigned)(a.parts * (uint32_t)num_rows));
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto* kernel = unit == 16  ? reorder_kernel<uint4>
-                   : unit == 8 ? reorder_kernel<uint2>
-                   : unit == 4 ? reorder_kernel<uint32_t>
-                   : unit == 2 ? reorder_kernel<uint16_t>
-                               : reorder_kernel<uint8_t>;
-    return status_of(launch_dependent(kernel, grid, kReorderThreads, s, true, a));
+    return status_of(launch_dependent((bits & 15u) == 0 ? reorder_kernel<true> : reorder_kernel<false>,
+                                      grid, kReorderThreads, static_cast<cudaStream_t>(stream), true, a));
 }
 
 int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32_t* kv_indptr,
@@ -1407,9 +1451,17 @@ int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32
         // (twice the entries in flight once that saves a turn of every warp: 9.6 -> 8.5 us
         // for 2.4 million entries, but 5.0 -> 6.1 for 65,536)
         const bool large = total > (int64_t)kExtendCtas * kExtendThreads * kShortSpan;
-        const int64_t per = kExtendThreads * (large ? kLongSpan : kShortSpan);
-        const int64_t most = (total + per - 1) / per;
         const bool spread = num_tokens > kLeadTokens;
+        // A CTA per SM while that leaves a thread two entries or more, then one for each turn
+        // of its threads: every CTA sums all the requests (65,536 entries by 17, 33 and 65
+        // CTAs: 5.0, 4.4 and 4.2 us; 1.1 million by 152, 260 and 305: 6.8, 6.5 and 7.5).
+        const int64_t units = spread && num_tokens > total ? num_tokens : total;
+        auto ctas = [&](int64_t per_thread) {
+            return (units + per_thread * kExtendThreads - 1) / (per_thread * kExtendThreads);
+        };
+        const int64_t spans = ctas(large ? kLongSpan : kShortSpan), pairs = ctas(2);
+        const int64_t few = pairs < kExtendCtas / 2 ? pairs : kExtendCtas / 2;
+        const int64_t most = spans > few ? spans : few;
         const bool in_place = new_cursor == cursor;
         const dim3 grid((unsigned)(1 + (most < 1 ? 1 : most < kExtendCtas ? most : kExtendCtas)));
         const int bytes = (4 * num_requests + 2) * 4;

@@ -105,7 +105,11 @@ def make(B, W, V, dtype, seed, pad=0, offset=0, spread=2.5):
     (2, 5, 1023, 5, 0, 0), (2, 5, 1024, 10, 0, 0), (2, 5, 1025, 10, 0, 0), (1, 32, 2047, 32, 0, 0),
     (1, 8, 2048, 8, 8, 0), (3, 8, 2049, 16, 0, 0), (2, 8, 5003, 16, 0, 3), (1, 4, 32000, 4, 0, 0),
     (2, 8, 50001, 16, 0, 0), (1, 2, 200003, 32, 5, 7), (5, 1, 4096, 1, 0, 1), (2, 2, 4100, 3, 4, 4),
-    (300, 3, 700, 3, 0, 0), (1, 2, 1 << 20, 4, 0, 0)])
+    (300, 3, 700, 3, 0, 0), (1, 2, 1 << 20, 4, 0, 0),
+    # beams far apart of a small vocabulary: one or two of them hold all of the best
+    (37, 16, 1084, 16, 0, 0), (13, 8, 1532, 8, 76, 0), (2, 8, 1247, 16, 0, 1), (7, 5, 1822, 10, 0, 0),
+    # more groups and parts than a thread keeps
+    (1, 16, 300001, 32, 0, 0), (1, 32, 140000, 32, 0, 0), (2, 1, 1000003, 5, 0, 1)])
 def test_random(dtype, B, W, V, K, pad, offset):
     x, s = make(B, W, V, dtype, seed=B + 7 * W + 11 * V, pad=pad, offset=offset)
     out, err = run(x, s, K)
@@ -175,12 +179,14 @@ def test_finished_and_unused_beams(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
-@pytest.mark.parametrize("bad", ["nan", "inf", "score nan", "score inf"])
+@pytest.mark.parametrize("bad", ["nan", "inf", "all nan", "all inf", "score nan", "score inf"])
 def test_bad_numbers_stay_in_their_beam(dtype, bad):
     W, V = 3, 5001
     x, s = make(2, W, V, dtype, seed=4)
     if bad.startswith("score"):
         s[0, 1] = float(bad.split()[1])
+    elif bad.startswith("all"):
+        x[1] = float(bad.split()[1])
     else:
         x[1, 4321] = float(bad)
     out, err = run(x, s, 3)

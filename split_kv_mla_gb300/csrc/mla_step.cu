@@ -897,7 +897,7 @@ reorder_kernel(const ReorderArgs a)
 // request up in global memory, per entry, 103 us where this takes 8.6 (512 of 1024 to
 // 8192).  More requests than shared memory is given for go that way:
 //   sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
-//   fill   a thread per entry of the new table and per token.
+//   fill   a warp per 256 entries of the new table, a thread per token.
 
 constexpr int kExtendThreads = 512;
 constexpr int kExtendRequests = 2048;   // 32 KB of sums
@@ -906,6 +906,7 @@ constexpr int kExtendCtas = 2 * 152;
 constexpr int kLeadTokens = 2048;       // that one CTA takes
 constexpr int kSumThreads = 1024;
 constexpr int kFillThreads = 256;
+constexpr int kFillSpan = 256;          // entries of a warp
 
 struct ExtendArgs {
     const int32_t* kv_indices;
@@ -1210,10 +1211,9 @@ sums_kernel(const ExtendArgs a)
     if (bad != 0) atomicOr(a.err, bad);
 }
 
-// The last f with indptr[f] <= i, of n >= 1 (indptr[0] <= i).
-__device__ __forceinline__ int find_request(const int32_t* indptr, int n, int64_t i)
+// The last f in [lo, hi) with indptr[f] <= i (indptr[lo] <= i).
+__device__ __forceinline__ int find_request(const int32_t* indptr, int lo, int hi, int64_t i)
 {
-    int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldcg(indptr + mid) <= i) lo = mid;
@@ -1230,12 +1230,37 @@ fill_kernel(const ExtendArgs a, uint32_t entry_ctas)
     const int F = a.num_requests;
     uint32_t bad = 0;
     if (blockIdx.x < entry_ctas) {
-        const int64_t i = (int64_t)blockIdx.x * kFillThreads + threadIdx.x;
-        if (i >= __ldcg(a.new_indptr + F)) return;
-        const int f = find_request(a.new_indptr, F, i);
-        const Kept k = kept_of(a, f, bad);
-        const int64_t j = i - __ldcg(a.new_indptr + f);
-        if (j < k.length) a.new_indices[i] = __ldg(a.kv_indices + k.from + j);
+        // a warp's span, and the requests in it
+        const int lane = threadIdx.x & 31;
+        const int64_t total = __ldcg(a.new_indptr + F);
+        const int64_t i0 = ((int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5)) * kFillSpan;
+        if (i0 >= total) return;
+        const int64_t past = min(i0 + kFillSpan, total);
+        const int lo = find_request(a.new_indptr, 0, F, i0);
+        const int hi = __ldcg(a.new_indptr + lo + 1) >= past
+                           ? lo + 1 : find_request(a.new_indptr, lo, F, past - 1) + 1;
+        const Kept own = kept_of(a, lo, bad);
+        const int64_t start = __ldcg(a.new_indptr + lo);
+        int32_t v[kFillSpan / 32];
+        bool kept[kFillSpan / 32];
+#pragma unroll
+        for (int k = 0; k < kFillSpan / 32; ++k) {
+            const int64_t i = i0 + 32 * k + lane;
+            kept[k] = i < past;
+            if (!kept[k]) continue;
+            Kept from = own;
+            int64_t j = i - start;
+            if (hi - lo > 1) {
+                const int f = find_request(a.new_indptr, lo, hi, i);
+                from = kept_of(a, f, bad);
+                j = i - __ldcg(a.new_indptr + f);
+            }
+            kept[k] = j < from.length;
+            if (kept[k]) v[k] = __ldg(a.kv_indices + from.from + j);
+        }
+#pragma unroll
+        for (int k = 0; k < kFillSpan / 32; ++k)
+            if (kept[k]) a.new_indices[i0 + 32 * k + lane] = v[k];
         return;
     }
     const int64_t t = (int64_t)(blockIdx.x - entry_ctas) * kFillThreads + threadIdx.x;
@@ -1243,7 +1268,7 @@ fill_kernel(const ExtendArgs a, uint32_t entry_ctas)
     const int32_t tokens = __ldcg(a.token_indptr + F);
     int32_t slot = -1, position = 0;
     if (t < tokens) {
-        const int f = find_request(a.token_indptr, F, t);
+        const int f = find_request(a.token_indptr, 0, F, t);
         const Kept k = kept_of(a, f, bad);
         bad = 0;   // the sums have told
         const int64_t j = k.length + (t - __ldcg(a.token_indptr + f));
@@ -1473,7 +1498,8 @@ int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32
         return status_of(e);
     }
     cudaError_t e = launch_dependent(sums_kernel, dim3(1), kSumThreads, s, true, a);
-    const int64_t entry_ctas = num_requests == 0 ? 0 : (total + kFillThreads - 1) / kFillThreads;
+    constexpr int64_t per = kFillThreads / 32 * kFillSpan;
+    const int64_t entry_ctas = num_requests == 0 ? 0 : (total + per - 1) / per;
     const int64_t token_ctas = (num_tokens + kFillThreads - 1) / kFillThreads;
     if (e == cudaSuccess && entry_ctas + token_ctas > 0)
         e = launch_dependent(fill_kernel, dim3((unsigned)(entry_ctas + token_ctas)), kFillThreads, s,

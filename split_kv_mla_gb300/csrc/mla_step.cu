@@ -118,6 +118,20 @@ __device__ __forceinline__ float piece_max(const uint4& v)
 }
 
 template <typename T, class F>
+__device__ __forceinline__ void each_pair(const uint4& v, F&& f)
+{
+    if constexpr (sizeof(T) == 4) {
+        f(make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
+        f(make_float2(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        f(LogitType<T>::unpack(v.x));
+        f(LogitType<T>::unpack(v.y));
+        f(LogitType<T>::unpack(v.z));
+        f(LogitType<T>::unpack(v.w));
+    }
+}
+
+template <typename T, class F>
 __device__ __forceinline__ void each_logit(const uint4& v, F&& f)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -270,37 +284,37 @@ __device__ __forceinline__ void scan_segment(const SelectArgs& a, int64_t row, i
     const float top = from_ordered(most);
     const float ref = top == -INFINITY ? 0.f : top;
     constexpr float kLog2e = 1.4426950408889634f;
-    float sum[2] = {0.f, 0.f};
+    const float2 back = make_float2(-ref, -ref), scale = make_float2(kLog2e, kLog2e);
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int p = 0; p < PIECES; ++p)
-        each_logit<T>(s.v[p], [&](int i, float t) { sum[i & 1] += ex2_approx((t - ref) * kLog2e); });
-    float all = sum[0] + sum[1];
+        each_pair<T>(s.v[p], [&](float2 t) {
+            t = __fmul2_rn(__fadd2_rn(t, back), scale);
+            sum = __fadd2_rn(sum, make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+        });
+    float all = sum.x + sum.y;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     if (lane == 0) a.parts[row * a.segments + seg] = make_float2(top, all);
 }
 
-// A warp per segment.  The rows of beams without candidates are not read, except where
-// a call is so small that its logits are asked for before it is known which those are.
-// (Warps that take several segments, the next one's logits in flight while they work on
-// one, were slower with 16 to 40 of them on an SM: 45.5 us for 268 MB, 44.5 this way.)
+// A warp per segment.  The rows of beams without candidates are not read.  (Warps that
+// take several segments, the next one's logits in flight while they work on one, were
+// slower with 16 to 40 of them on an SM: 45.5 us for 268 MB, 44.3 this way.)
 template <typename T, bool ALIGNED, int PIECES>
 __global__ void __launch_bounds__(kScanThreads)
 scan_kernel(const SelectArgs a)
 {
-    constexpr bool kEager = PIECES == kShortPieces;
     wait_for_predecessor();
     allow_dependents();
     const int lane = threadIdx.x & 31;
     const uint32_t id = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);   // below 2^31
     const int64_t row = id / (uint32_t)a.segments;
     const int seg = (int)(id % (uint32_t)a.segments);
-    if (row >= a.rows) return;
-    const bool live = row_is_live(a, row);
-    if (!kEager && !live) return;
+    if (row >= a.rows || !row_is_live(a, row)) return;
     Segment<T, PIECES> s;
     load_segment<T, ALIGNED, PIECES>(a, row, seg, lane, s);
-    if (live) scan_segment<T, PIECES>(a, row, seg, lane, s);
+    scan_segment<T, PIECES>(a, row, seg, lane, s);
 }
 
 // (hi, lo) of a + b.

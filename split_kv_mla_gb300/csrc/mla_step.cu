@@ -24,7 +24,7 @@ namespace {
 // these (a group is a range of columns, so of equal scores the lower index is also in
 // the lower group).  So
 //   scan   streams the rows and leaves, for each 256 columns, their maximum, and for
-//          each 4 KB segment of a row its maximum m and sum of e^(x - m);
+//          each segment of a row (1 to 4 KB) its maximum m and sum of e^(x - m);
 //   pick   (a CTA per request) joins a row's segments, takes the K best groups by
 //          their maxima, reads those 256 logits of each again and takes the K best.
 // What scan does per logit does not depend on the data, and pick reads 1/64 of the
@@ -431,10 +431,10 @@ __device__ __forceinline__ uint32_t rank_of_part(Picker& p, int round, int K, ui
 // Lists the CTA's candidates with ranks of at least `least`, and returns how many, after a
 // barrier.  each(f) calls f(beam, place, x) for the threads that have any, of kChunk
 // logits x at a time, of which the i-th lies at place + step(i).  Those threads, a few,
-// hand their logits over, and a thread for each ranks them (in the threads themselves the
-// eight took 1,700 cycles of the warp, this way it is 700).  Lists that would overflow
-// (many equal scores, or most of the best in few groups, and many) are not used: the K
-// largest are then taken one after the other.
+// hand their logits over, and a thread for each ranks them (1,600 cycles; with the eight
+// ranked in the threads themselves 2,150).  Lists that would overflow (many equal scores,
+// or most of the best in few groups, and many) are not used: the K largest are then taken
+// one after the other.
 template <class Each, class Step>
 __device__ __forceinline__ int list_candidates(Picker& p, int round, int K, uint32_t least,
                                                Each&& each, Step&& step)

@@ -336,6 +336,38 @@ def test_captured_and_two_workspaces():
             assert all(torch.equal(u, v) for u, v in zip(o[:3], want[k][:3]))
 
 
+@pytest.mark.parametrize("B,W,V", [(64, 4, 700), (300, 2, 3001), (7, 8, 30000)])
+def test_selections_right_behind_one_another(B, W, V):
+    # each call's kernels start while the last one's run, and find its scores and flags
+    x, s = make(B, W, V, BF, seed=18)
+    done = torch.zeros(B, W, dtype=torch.bool, device="cuda")
+    ws = mla.beam_workspace(B, W, V)
+    s1, d1 = s.clone(), done.clone()
+    for _ in range(40):
+        mla.mla_beam_select(x, s1, finished=d1, end_token=3, scores_out=s1, finished_out=d1,
+                            workspace_t=ws)
+        torch.cuda.synchronize()
+    s2, d2 = s.clone(), done.clone()
+    torch.cuda.synchronize()
+    for _ in range(40):
+        mla.mla_beam_select(x, s2, finished=d2, end_token=3, scores_out=s2, finished_out=d2,
+                            workspace_t=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(s1, s2) and torch.equal(d1, d2)
+    s3, d3 = s.clone(), done.clone()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for _ in range(20):
+            mla.mla_beam_select(x, s3, finished=d3, end_token=3, scores_out=s3, finished_out=d3,
+                                workspace_t=ws)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s1, s3) and torch.equal(d1, d3)
+    assert mla.mla_read_device_error(ws) == 0
+
+
 def test_no_requests_and_refusals():
     x, s = make(2, 4, 100, BF, seed=17)
     out = mla.mla_beam_select(x[:0], s[:0], 4)

@@ -255,6 +255,14 @@ __device__ __forceinline__ float from_ordered(int i)
     return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
 }
 
+// Maximum over the warp (a NaN is passed over).
+__device__ __forceinline__ float warp_max(float x)
+{
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
 __device__ __forceinline__ bool row_is_live(const SelectArgs& a, int64_t row)
 {
     return __ldg(a.scores + row) != -INFINITY &&
@@ -268,20 +276,19 @@ __device__ __forceinline__ void scan_segment(const SelectArgs& a, int64_t row, i
 {
     constexpr int kPerGroup = kGroup / (32 * kElements<T>);   // pieces of a group
     constexpr int kGroups = PIECES / kPerGroup;               // groups of a segment
-    int most = INT32_MIN, mine = 0;
+    float top = -INFINITY, mine = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         float m = piece_max<T>(s.v[g * kPerGroup]);
 #pragma unroll
         for (int p = 1; p < kPerGroup; ++p) m = fmaxf(m, piece_max<T>(s.v[g * kPerGroup + p]));
-        const int r = __reduce_max_sync(0xffffffffu, ordered(m));
-        most = max(most, r);
-        if (lane == g) mine = r;
+        m = warp_max(m);
+        top = fmaxf(top, m);
+        if (lane == g) mine = m;
     }
     const int group = seg * kGroups + lane;
-    if (lane < kGroups && group < a.groups) a.group_max[row * a.groups + group] = from_ordered(mine);
+    if (lane < kGroups && group < a.groups) a.group_max[row * a.groups + group] = mine;
 
-    const float top = from_ordered(most);
     const float ref = top == -INFINITY ? 0.f : top;
     constexpr float kLog2e = 1.4426950408889634f;
     const float2 back = make_float2(-ref, -ref), scale = make_float2(kLog2e, kLog2e);
@@ -582,7 +589,7 @@ pick_kernel(const SelectArgs a)
         for (int k = 0; k < kParts; ++k) m = fmaxf(m, t[k].x);
 #pragma unroll 4
         for (int i = lane + 32 * kParts; i < a.segments; i += 32) m = fmaxf(m, __ldcg(parts + i).x);
-        m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+        m = warp_max(m);
         const float ref = m == -INFINITY ? 0.f : m;
         constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll

@@ -11,6 +11,7 @@
 #include "mla_internal.h"
 #include "mla_launch.h"
 #include "mla_softmax.cuh"
+#include "mla_spans.h"
 
 namespace mla {
 namespace {
@@ -1041,9 +1042,10 @@ __device__ __forceinline__ int last_at_most(const int32_t* start, int lo, int hi
 // so that it alone reads the cursor that it then moves (which may be one and the
 // same); the others copy.
 // (Four CTAs on an SM for short spans: with three, at 40 registers, the next call's CTAs
-// start later, 7.4 us a call instead of 6.6 for 1.1 million entries.)
+// start later, 7.4 us a call instead of 6.6 for 1.1 million entries; the same with three
+// of two for long spans, 9.8 instead of 7.8 for 2.4 million.)
 template <int SPAN>
-__global__ void __launch_bounds__(kExtendThreads, SPAN == kShortSpan ? 4 : 0)
+__global__ void __launch_bounds__(kExtendThreads, SPAN == kShortSpan ? 4 : 2)
 extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
 {
     extern __shared__ int32_t sums[];
@@ -1137,38 +1139,35 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
     constexpr int kSpan = 32 * SPAN;   // entries at a time
     const uint32_t warps = (gridDim.x - 1) * (kExtendThreads / 32);
     const uint32_t warp = (blockIdx.x - 1) * (kExtendThreads / 32) + (tid >> 5);
-    uint32_t run = ((uint32_t)total + warps - 1) / warps;
-    run = run > kSpan ? (run + kSpan - 1) / kSpan * kSpan : (run + 31) / 32 * 32;
-    const uint32_t begin = warp * run;   // at most total + warps * kSpan
-    if (begin >= (uint32_t)total) return;
-    const int32_t end = (int32_t)min(begin + run, (uint32_t)total);
-    int lo = last_at_most(start, 0, F, (int32_t)begin);
-    for (int32_t i0 = (int32_t)begin; i0 < end; i0 += kSpan) {
-        const int32_t past = min(i0 + kSpan, end);
-        if (start[lo + 1] <= i0) lo = last_at_most(start, lo + 1, F, i0);
+    const Run run = warp_run((uint32_t)total, warp, warps, kSpan);
+    if (run.begin >= run.end) return;
+    int lo = last_at_most(start, 0, F, (int32_t)run.begin);
+    for (uint32_t i0 = run.begin; i0 < run.end; i0 += kSpan) {
+        const uint32_t past = span_end(i0, run.end, kSpan);
+        if (start[lo + 1] <= (int32_t)i0) lo = last_at_most(start, lo + 1, F, (int32_t)i0);
+        // the lane's entries are 32 apart from its first on: those below `left`
+        int32_t* const dst = a.new_indices + (i0 + lane);
         int32_t v[SPAN];
-        if (start[lo + 1] >= past) {   // one request's
-            const int32_t until = min(past, start[lo] + length[lo]);
-            const int32_t* src = a.kv_indices + from[lo];
+        if (start[lo + 1] >= (int32_t)past) {   // one request's
+            const uint32_t until = min(past, kept_end(start[lo], start[lo + 1], length[lo]));
+            const int32_t left = (int32_t)(until - i0) - lane;
+            const int32_t* src = a.kv_indices + from[lo] + (i0 + lane);
 #pragma unroll
-            for (int k = 0; k < SPAN; ++k) {
-                const int32_t i = i0 + 32 * k + lane;
-                if (i < until) v[k] = __ldg(src + i);
-            }
+            for (int k = 0; k < SPAN; ++k)
+                if (32 * k < left) v[k] = __ldg(src + 32 * k);
 #pragma unroll
-            for (int k = 0; k < SPAN; ++k) {
-                const int32_t i = i0 + 32 * k + lane;
-                if (i < until) a.new_indices[i] = v[k];
-            }
+            for (int k = 0; k < SPAN; ++k)
+                if (32 * k < left) dst[32 * k] = v[k];
             continue;
         }
-        const int hi = last_at_most(start, lo, F, past - 1) + 1;
+        const int hi = last_at_most(start, lo, F, (int32_t)past - 1) + 1;
+        const int32_t left = (int32_t)(past - i0) - lane;
         bool kept[SPAN];
 #pragma unroll
         for (int k = 0; k < SPAN; ++k) {
-            const int32_t i = i0 + 32 * k + lane;
-            kept[k] = i < past;
+            kept[k] = 32 * k < left;
             if (kept[k]) {
+                const int32_t i = (int32_t)i0 + lane + 32 * k;
                 const int f = last_at_most(start, lo, hi, i);
                 kept[k] = i - start[f] < length[f];
                 if (kept[k]) v[k] = __ldg(a.kv_indices + (from[f] + i));
@@ -1176,7 +1175,7 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
         }
 #pragma unroll
         for (int k = 0; k < SPAN; ++k)
-            if (kept[k]) a.new_indices[i0 + 32 * k + lane] = v[k];
+            if (kept[k]) dst[32 * k] = v[k];
     }
 }
 

@@ -1,5 +1,5 @@
 // mla_spans.h -- the whole-number arithmetic of cache extension: which entries of the new
-// table a warp copies, and which of a request's entries are kept.  Tables, lengths and
+// table a warp copies, which of a request's are kept, and which take its tokens.  Tables, lengths and
 // counts go up to 2^31 - 1, so what is added to them is held in 32 bits without a sign,
 // where neither two of them nor one and a span overflow.  For host code too.
 #pragma once
@@ -39,6 +39,15 @@ MLA_HD uint32_t span_end(uint32_t i0, uint32_t end, uint32_t span)
 MLA_HD uint32_t kept_end(uint32_t start, uint32_t next, uint32_t length)
 {
     return length < next - start ? start + length : next;
+}
+
+// The place in its request of the n-th token behind `length` kept entries, and whether the
+// request's entries [start, next) of the table have it.
+MLA_HD uint32_t token_place(uint32_t length, uint32_t n) { return length + n; }
+
+MLA_HD bool has_place(uint32_t start, uint32_t next, uint32_t place)
+{
+    return place < next - start;
 }
 
 }  // namespace mla

@@ -1087,12 +1087,12 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
     if (tid == 0) token[F] = tokens;
     __syncthreads();
     mine = 0;
-    for (int f = f0; f < f1; ++f) mine = add_up(mine, length[f] + (token[f + 1] - token[f]));
+    for (int f = f0; f < f1; ++f) mine = add_up(mine, token_place(length[f], token[f + 1] - token[f]));
     at = block_scan<kExtendThreads / 32>(mine, part, all);
     for (int f = f0; f < f1; ++f) {
         start[f] = (int32_t)min(at, room);
         from[f] -= start[f];
-        at = add_up(at, length[f] + (token[f + 1] - token[f]));
+        at = add_up(at, token_place(length[f], token[f + 1] - token[f]));
     }
     if (all > room) bad |= MLA_DEVERR_BAD_TABLE;
     const int32_t total = (int32_t)min(all, room);
@@ -1108,9 +1108,9 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
             int32_t slot = -1, position = 0;
             if (t < tokens) {
                 const int f = last_at_most(token, 0, F, (int32_t)t);
-                const int32_t j = length[f] + ((int32_t)t - token[f]);
-                position = j + prefix;
-                if (j < start[f + 1] - start[f]) {
+                const uint32_t j = token_place(length[f], (uint32_t)t - (uint32_t)token[f]);
+                position = (int32_t)(j + (uint32_t)prefix);
+                if (has_place(start[f], start[f + 1], j)) {
                     slot = free_slot(a, (int32_t)((uint32_t)cursor + (uint32_t)t), bad);
                     a.new_indices[start[f] + j] = slot;
                 }

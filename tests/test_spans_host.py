@@ -30,6 +30,8 @@ int spans_of(uint32_t begin, uint32_t end, uint32_t span, int64_t* out, int room
     return n;
 }
 int64_t kept(uint32_t start, uint32_t next, uint32_t length) { return kept_end(start, next, length); }
+int64_t place(uint32_t length, uint32_t n) { return token_place(length, n); }
+int has(uint32_t start, uint32_t next, uint32_t p) { return has_place(start, next, p) ? 1 : 0; }
 }
 """
 
@@ -44,6 +46,9 @@ def lib(tmp_path_factory):
     lib = ctypes.CDLL(so)
     lib.kept.restype = ctypes.c_int64
     lib.kept.argtypes = [ctypes.c_uint32] * 3
+    lib.place.restype = ctypes.c_int64
+    lib.place.argtypes = [ctypes.c_uint32] * 2
+    lib.has.argtypes = [ctypes.c_uint32] * 3
     lib.run_of.argtypes = [ctypes.c_uint32] * 4 + [ctypes.c_void_p]
     lib.spans_of.argtypes = [ctypes.c_uint32] * 3 + [ctypes.c_void_p, ctypes.c_int]
     return lib
@@ -92,3 +97,14 @@ def test_spans_end_with_their_run(lib, total, span):
     (LAST - 1, LAST, LAST), (5, 5, LAST)])
 def test_what_is_kept_ends_in_the_request(lib, start, next_, length):
     assert lib.kept(start, next_, length) == min(start + length, next_)
+
+
+@pytest.mark.parametrize("start,entries", [(0, 0), (0, 7), (LAST - 7, 7), (0, LAST), (1 << 30, 1 << 30)])
+@pytest.mark.parametrize("length", [0, 3, 6, 7, (1 << 30) - 1, 1 << 30, LAST - 1, LAST])
+@pytest.mark.parametrize("n", [0, 1, 2, 1 << 30, LAST - 1])
+def test_tokens_without_an_entry(lib, start, entries, length, n):
+    # `entries` of the table from start on are the request's: what it keeps, and its tokens,
+    # as far as there is room
+    assert lib.place(length, n) == length + n
+    next_ = min(start + entries, LAST)
+    assert lib.has(start, next_, lib.place(length, n)) == int(length + n < next_ - start)

@@ -1,7 +1,7 @@
 // mla_spans.h -- the whole-number arithmetic of cache extension: which entries of the new
-// table a warp copies, which of a request's are kept, and which take its tokens.  Tables, lengths and
-// counts go up to 2^31 - 1, so what is added to them is held in 32 bits without a sign,
-// where neither two of them nor one and a span overflow.  For host code too.
+// table a warp copies, which of a request's are kept, and which take its tokens.  Tables,
+// lengths and counts go up to 2^31 - 1, so what is added to them is held in 32 bits without
+// a sign, where neither two of them nor one and a span overflow.  For host code too.
 #pragma once
 #include <cstdint>
 
@@ -48,6 +48,12 @@ MLA_HD uint32_t token_place(uint32_t length, uint32_t n) { return length + n; }
 MLA_HD bool has_place(uint32_t start, uint32_t next, uint32_t place)
 {
     return place < next - start;
+}
+
+// Between lo and hi: lo itself where hi is the next.
+MLA_HD int32_t middle(int32_t lo, int32_t hi)
+{
+    return (int32_t)(((uint32_t)lo + (uint32_t)hi) >> 1);
 }
 
 }  // namespace mla

@@ -1031,7 +1031,7 @@ __device__ __forceinline__ int32_t free_slot(const ExtendArgs& a, int32_t number
 __device__ __forceinline__ int last_at_most(const int32_t* start, int lo, int hi, int32_t i)
 {
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = middle(lo, hi);
         if (start[mid] <= i) lo = mid;
         else hi = mid;
     }
@@ -1197,14 +1197,15 @@ sums_kernel(const ExtendArgs a)
     const uint32_t room = (uint32_t)a.total, token_room = (uint32_t)a.num_tokens;
     uint32_t tokens = 0, entries = 0;   // of the requests before this turn's
     uint32_t bad = 0;
-    for (int f0 = 0; f0 < a.num_requests; f0 += kSumThreads) {
-        const int f = f0 + tid;
+    const uint32_t F = (uint32_t)a.num_requests;
+    for (uint32_t f0 = 0; f0 < F; f0 += kSumThreads) {
+        const uint32_t f = f0 + tid;
         uint32_t n = 0, length = 0;
-        if (f < a.num_requests) {
+        if (f < F) {
             const int32_t want = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
             n = max(want, 0);
             if (want < 0) bad |= MLA_DEVERR_BAD_LENGTH;
-            length = kept_of(a, f, bad).length;
+            length = kept_of(a, (int)f, bad).length;
         }
         uint32_t all;
         const uint32_t t = add_up(tokens, block_scan<kSumThreads / 32>(n, part, all));
@@ -1214,7 +1215,7 @@ sums_kernel(const ExtendArgs a)
         const uint32_t e = add_up(entries, block_scan<kSumThreads / 32>(length, part, all));
         const uint32_t first = min(e, room);
         entries = add_up(entries, all);
-        if (f < a.num_requests) {
+        if (f < F) {
             a.token_indptr[f] = (int32_t)first_token;
             a.new_indptr[f] = (int32_t)first;
             a.new_lens[f] = (int32_t)(min(add_up(e, length), room) - first);
@@ -1223,8 +1224,8 @@ sums_kernel(const ExtendArgs a)
     if (tokens > token_room || entries > room) bad |= MLA_DEVERR_BAD_TABLE;
     if (tid == 0) {
         const uint32_t n = min(tokens, token_room);
-        a.token_indptr[a.num_requests] = (int32_t)n;
-        a.new_indptr[a.num_requests] = (int32_t)min(entries, room);
+        a.token_indptr[F] = (int32_t)n;
+        a.new_indptr[F] = (int32_t)min(entries, room);
         // modulo 2^32, so that fill has the cursor from the new one
         a.new_cursor[0] = (int32_t)((uint32_t)a.cursor[0] + n);
     }
@@ -1235,7 +1236,7 @@ sums_kernel(const ExtendArgs a)
 __device__ __forceinline__ int find_request(const int32_t* indptr, int lo, int hi, int64_t i)
 {
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = middle(lo, hi);
         if (__ldcg(indptr + mid) <= i) lo = mid;
         else hi = mid;
     }

@@ -31,6 +31,7 @@ int spans_of(uint32_t begin, uint32_t end, uint32_t span, int64_t* out, int room
 }
 int64_t kept(uint32_t start, uint32_t next, uint32_t length) { return kept_end(start, next, length); }
 int64_t place(uint32_t length, uint32_t n) { return token_place(length, n); }
+int mid(int lo, int hi) { return middle(lo, hi); }
 int has(uint32_t start, uint32_t next, uint32_t p) { return has_place(start, next, p) ? 1 : 0; }
 }
 """
@@ -108,3 +109,9 @@ def test_tokens_without_an_entry(lib, start, entries, length, n):
     assert lib.place(length, n) == length + n
     next_ = min(start + entries, LAST)
     assert lib.has(start, next_, lib.place(length, n)) == int(length + n < next_ - start)
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 1), (0, 2), (0, LAST), (1 << 30, (1 << 30) + 1), (1 << 30, LAST),
+                                   (LAST - 1, LAST), (LAST - 2, LAST)])
+def test_a_search_among_many_requests(lib, lo, hi):
+    assert lib.mid(lo, hi) == (lo + hi) // 2

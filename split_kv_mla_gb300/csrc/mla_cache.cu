@@ -12,6 +12,7 @@
 #include "mla_internal.h"
 #include "mla_launch.h"
 #include "mla_sm100.cuh"
+#include "mla_spans.h"
 
 namespace mla {
 namespace {
@@ -370,7 +371,7 @@ __device__ __forceinline__ void fork_entry(const ForkArgs& a, int64_t i, int32_t
     // the child whose range holds i: the last f with child_indptr[f] <= i
     int lo = 0, hi = a.num_children;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = middle(lo, hi);
         if (__ldg(a.child_indptr + mid) <= i) lo = mid;
         else hi = mid;
     }

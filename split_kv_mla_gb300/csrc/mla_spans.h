@@ -50,7 +50,7 @@ MLA_HD bool has_place(uint32_t start, uint32_t next, uint32_t place)
     return place < next - start;
 }
 
-// Between lo and hi: lo itself where hi is the next.
+// Between lo and hi: lo itself where hi is the next.  (Of a fork's children too.)
 MLA_HD int32_t middle(int32_t lo, int32_t hi)
 {
     return (int32_t)(((uint32_t)lo + (uint32_t)hi) >> 1);

@@ -115,3 +115,10 @@ def test_tokens_without_an_entry(lib, start, entries, length, n):
                                    (LAST - 1, LAST), (LAST - 2, LAST)])
 def test_a_search_among_many_requests(lib, lo, hi):
     assert lib.mid(lo, hi) == (lo + hi) // 2
+
+
+def test_every_search_takes_that_middle():
+    for name in ("mla_step.cu", "mla_cache.cu"):
+        with open(os.path.join(mla_build.CSRC, name)) as f:
+            text = f.read()
+        assert "middle(lo, hi)" in text and "(lo + hi)" not in text, name

@@ -579,9 +579,11 @@ int64_t mla_cache_compact_workspace_bytes(int64_t pool_rows);
 /*
  * Beam selection: the num_select best continuations of each request's beams.  Row
  * b * beams + w of the logits belongs to beam w of request b; with x its logits,
- *   score(b, w, v) = scores[b, w] + x_v - log sum_u exp(x_u)       (rounded to fp32)
- * and the request's candidates (w, v) are taken by their score, equal scores by the
- * lower w * vocab + v:
+ *   score(b, w, v) = scores[b, w] + x_v - log sum_u exp(x_u)       (fp32)
+ * rounded once, and off besides by at most 2^-15 (as a rule 2^-22) of the logarithm of
+ * sum_u exp(x_u - max x), which is near 0 where one token has most of the mass.  The
+ * request's candidates (w, v) are taken by their score, equal scores by the lower
+ * w * vocab + v:
  *   tokens[b, k]       = v
  *   parents[b, k]      = b * beams + w, the row that continues (what mla_cache_fork,
  *                        mla_cache_extend and mla_beam_reorder take as parents)

@@ -29,11 +29,17 @@ namespace {
 //   pick   (a CTA per request) joins a row's segments, takes the K best groups by
 //          their maxima, reads those 256 logits of each again and takes the K best.
 // What scan does per logit does not depend on the data, and pick reads 1/64 of the
-// bytes and K groups.
+// bytes, K groups, and of rows with a token of more than two thirds of their mass one
+// segment.
 //
 // A segment's sum is relative to its own maximum, so its largest term is 1, and is
 // held in fp32; which column goes to which lane does not depend on a row's address,
 // so equal rows give equal sums and their equal candidates are taken by their index.
+// Where one token has most of a row's mass, the logarithm is that of 1 + t with a small t,
+// of which a sum that has the 1 has lost all below 2^-24 (scores of -2e-8 came out as 0).
+// There pick sums the maximum's segment again without it, 0.6 to 1.9 us of a call whose
+// rows are such.  (In scan, where every segment has a maximum, leaving the 1 out took every
+// call longer: 11.7 -> 13.5 us for 32 x 4 of 100003 fp16, by its registers.)
 
 constexpr int kGroup = 256;             // columns
 constexpr int kShortPieces = 2, kMiddlePieces = 4, kLongPieces = 8;   // 16-byte loads of a lane
@@ -43,6 +49,7 @@ constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickList = 1024;
 constexpr int kParts = 4;               // of a row, that a lane of pick asks for at once
+constexpr float kPeakedSum = 1.5f;      // of a row, its maximum's term being 1
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kPlaceBits = 20;          // of a column
 static_assert(kMaxVocab <= 1 << kPlaceBits && MLA_MAX_BEAMS <= 1 << (32 - kPlaceBits), "");
@@ -55,6 +62,7 @@ struct SelectArgs {
     int32_t batch, beams, vocab, select, end_token;
     int32_t groups;        // of a row
     int32_t segments;      // of a row
+    int32_t segment_groups;
     int64_t rows;
     float* group_max;      // [rows, groups]
     float2* parts;         // [rows, segments]: maximum, sum
@@ -334,7 +342,8 @@ __device__ __forceinline__ float2 two_sum(float a, float b)
 }
 
 // score - m - ln(sum) as a sum of two floats, so that a candidate's score is rounded
-// once: the scores of different beams that fp32 tells apart come out in their order.
+// once: the scores of different beams that fp32 tells apart come out in their order, as far
+// as the sums are that exact (which is within 2^-15 of the logarithm).
 // ln(sum) = e ln 2 + ln f with f in [0.75, 1.5); ln 2 in two parts, of which the first
 // has 12 bits, so that e times it is exact.
 __device__ __forceinline__ float2 row_base(float score, float m, float sum)
@@ -349,9 +358,55 @@ __device__ __forceinline__ float2 row_base(float score, float m, float sum)
     constexpr double kHigh = 2839.0 / 4096.0;
     const float2 a = two_sum(score, -m);
     const float2 b = two_sum(a.x, -(float)e * (float)kHigh);
-    const float rest = (a.y + b.y) - fmaf((float)e, (float)(kLn2 - kHigh), logf(f));
-    const float hi = __fadd_rn(b.x, rest);
-    return make_float2(hi, __fadd_rn(__fsub_rn(b.x, hi), rest));
+    return two_sum(b.x, (a.y + b.y) - fmaf((float)e, (float)(kLn2 - kHigh), logf(f)));
+}
+
+// The same of a row whose maximum, which it has once, has more than two thirds of its mass:
+// of 1 + t with t the sum of e^(x - m) over the others.  The segment of the maximum is summed
+// again without it, and the other segments' sums are joined by expf, as their maxima are far
+// below m; head are those that the lane has.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ float2 peaked_base(const SelectArgs& a, int64_t row, int lane, float score,
+                                              float m, const float2 (&head)[kParts])
+{
+    constexpr int kPerGroup = kGroup / (32 * kElements<T>);
+    constexpr int kAtOnce = kPerGroup == 1 ? 2 : 4;   // groups (four of 16-bit logits spill)
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float2* parts = a.parts + row * a.segments;
+    float2 sum = make_float2(0.f, 0.f);
+    uint32_t at = 0;
+    auto join = [&](uint32_t i, float2 u) {
+        if (u.x == m) at = i;
+        else sum.x += u.y * expf(u.x - m);
+    };
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) join(lane + 32 * k, head[k]);
+#pragma unroll 1
+    for (int i = lane + 32 * kParts; i < a.segments; i += 32) join(i, __ldcg(parts + i));
+    int g = (int)__reduce_max_sync(0xffffffffu, at) * a.segment_groups;
+    const int end = min(g + a.segment_groups, a.groups);
+#pragma unroll 1
+    for (; g < end; g += kAtOnce) {
+        Segment<T, kPerGroup> v[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+            if (g + q < end) load_segment<T, ALIGNED, kPerGroup>(a, row, g + q, lane, v[q]);
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            if (g + q >= end) break;
+#pragma unroll
+            for (int p = 0; p < kPerGroup; ++p)
+                each_pair<T>(v[q].v[p], [&](float2 x) {
+                    sum.x += x.x == m ? 0.f : ex2_approx((x.x - m) * kLog2e);
+                    sum.y += x.y == m ? 0.f : ex2_approx((x.y - m) * kLog2e);
+                });
+        }
+    }
+    float rest = sum.x + sum.y;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+    const float2 b = two_sum(score, -m);
+    return two_sum(b.x, b.y - log1pf(rest));
 }
 
 // A score as a number in its order; 0 for what is no candidate (-inf, or the NaN that
@@ -608,7 +663,10 @@ pick_kernel(const SelectArgs a)
         const bool bad = !none && (!(own < INFINITY) || (!is_ended && !(s < INFINITY)));
         float2 b = make_float2(-INFINITY, 0.f);
         if (!none && !bad && (is_ended || s != 0.f))
-            b = is_ended ? make_float2(own, 0.f) : row_base(own, m, s);
+            b = is_ended ? make_float2(own, 0.f)
+                : __builtin_expect(s < kPeakedSum, 0)
+                    ? peaked_base<T, ALIGNED>(a, row, lane, own, m, t)
+                    : row_base(own, m, s);
         if (lane == 0 && part0 == 0) {
             p.base[w] = b;
             p.ended[w] = is_ended ? 1 : 0;
@@ -742,6 +800,7 @@ template <typename T, bool ALIGNED, int PIECES>
 cudaError_t launch_scan(SelectArgs& a, cudaStream_t s)
 {
     a.segments = (a.vocab + kSegment<T, PIECES> - 1) / kSegment<T, PIECES>;
+    a.segment_groups = kSegment<T, PIECES> / kGroup;
     const int64_t ctas = (a.rows * a.segments + kScanThreads / 32 - 1) / (kScanThreads / 32);
     return launch_dependent(scan_kernel<T, ALIGNED, PIECES>, dim3((unsigned)ctas), kScanThreads, s,
                             true, a);

@@ -1372,6 +1372,23 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m)
            b < a + (uintptr_t)n;
 }
 
+struct Bytes {
+    const void* p;
+    int64_t n;
+};
+
+bool overlap(const Bytes& a, const Bytes& b) { return overlap(a.p, a.n, b.p, b.n); }
+
+// Whether one of n rows of `bytes` at p, `stride` apart, has a byte in common with b.
+bool rows_reach(const void* p, int64_t n, int64_t stride, int64_t bytes, const Bytes& b)
+{
+    if (p == nullptr || b.p == nullptr || n < 1 || bytes < 1 || b.n < 1) return false;
+    const int64_t at = reinterpret_cast<const char*>(b.p) - static_cast<const char*>(p);
+    // the first row that does not end before b
+    const int64_t r = at < bytes || stride < 1 ? 0 : (at - bytes) / stride + 1;
+    return r < n && r * stride < at + b.n && at < r * stride + bytes;
+}
+
 // Whether two sets of rows of `bytes` have one in common: n rows at p, `ps` apart, and m
 // at q, `qs` apart.  Rows of one stride may lie between one another; otherwise sets
 // that reach into each other are taken to have one.
@@ -1420,17 +1437,32 @@ int mla_beam_select(const void* logits, int32_t dtype, int64_t row_stride, const
     const int64_t picks = (int64_t)batch * num_select;
     if (!logits || !scores || !tokens || !parents || !scores_out || row_stride < 0)
         return MLA_ERR_INVALID_ARG;
-    if ((overlap(scores_out, picks * 4, scores, rows * 4) &&
-         (scores_out != scores || num_select != beams)) ||
-        (overlap(finished_out, picks, finished, rows) &&
-         (finished_out != finished || num_select != beams)))
-        return MLA_ERR_INVALID_ARG;
+    const int64_t element = dtype == MLA_DTYPE_F32 ? 4 : 2;
+    const Bytes in[2] = {{scores, rows * 4}, {finished, rows}};
+    const Bytes out[4] = {{scores_out, picks * 4}, {finished_out, picks}, {tokens, picks * 4},
+                          {parents, picks * 4}};
+    auto on_logits = [&](const Bytes& b) {
+        return rows_reach(logits, rows, row_stride * element, vocab * element, b);
+    };
+    for (int i = 0; i < 4; ++i) {
+        // scores_out as scores and finished_out as finished, entry by entry
+        const bool in_place = i < 2 && out[i].p == in[i].p && num_select == beams;
+        for (int k = 0; k < 2; ++k)
+            if (overlap(out[i], in[k]) && !(i == k && in_place)) return MLA_ERR_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (overlap(out[i], out[k])) return MLA_ERR_INVALID_ARG;
+        // (flags in place are an input as well, and where inputs lie is the caller's)
+        if (!(i == 1 && in_place) && on_logits(out[i])) return MLA_ERR_INVALID_ARG;
+    }
     if ((reinterpret_cast<uintptr_t>(logits) & (dtype == MLA_DTYPE_F32 ? 3u : 1u)) != 0)
         return MLA_ERR_MISALIGNED;
     int rc = check_header(workspace, workspace_bytes);
     if (rc != MLA_OK) return rc;
-    if (workspace_bytes < mla_beam_select_workspace_bytes(batch, beams, vocab))
-        return MLA_ERR_WORKSPACE_TOO_SMALL;
+    const Bytes scratch = {workspace, mla_beam_select_workspace_bytes(batch, beams, vocab)};
+    if (workspace_bytes < scratch.n) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    for (const Bytes& b : {in[0], in[1], out[0], out[1], out[2], out[3]})
+        if (overlap(scratch, b)) return MLA_ERR_INVALID_ARG;
+    if (on_logits(scratch)) return MLA_ERR_INVALID_ARG;
     rc = device_ok();
     if (rc != MLA_OK) return rc;
 

@@ -1560,22 +1560,26 @@ int mla_cache_extend(const int32_t* kv_indices, int64_t num_indices, const int32
         (num_tokens > 0 && (!slots || !positions)))
         return MLA_ERR_INVALID_ARG;
     if (parents == nullptr && num_requests > num_parents) return MLA_ERR_INVALID_ARG;
-    struct Range {
-        const void* p;
-        int64_t n;
-    };
     const int64_t F = num_requests, P = num_parents;
-    const Range in[] = {{kv_indices, num_indices}, {kv_indptr, P + 1}, {seq_lens, P}, {parents, F},
-                        {new_tokens, F}, {free_slots, num_free}, {cursor, 1}, {prefix_len, 1}};
-    const Range out[] = {{new_indices, total}, {new_indptr, F + 1}, {new_lens, F},
-                         {slots, num_tokens}, {positions, num_tokens}, {token_indptr, F + 1},
-                         {new_cursor, 1}};
-    for (const Range& o : out)
-        for (const Range& i : in)
-            if (overlap(o.p, o.n * 4, i.p, i.n * 4) && !(o.p == new_cursor && i.p == cursor))
-                return MLA_ERR_INVALID_ARG;
+    const Bytes in[] = {{kv_indices, num_indices * 4}, {kv_indptr, (P + 1) * 4}, {seq_lens, P * 4},
+                        {parents, F * 4}, {new_tokens, F * 4}, {free_slots, num_free * 4},
+                        {cursor, 4}, {prefix_len, 4}};
+    const Bytes out[] = {{new_indices, total * 4}, {new_indptr, (F + 1) * 4}, {new_lens, F * 4},
+                         {slots, num_tokens * 4}, {positions, num_tokens * 4},
+                         {token_indptr, (F + 1) * 4}, {new_cursor, 4}};
+    for (const Bytes& o : out) {
+        for (const Bytes& i : in)
+            if (overlap(o, i) && !(o.p == new_cursor && i.p == cursor)) return MLA_ERR_INVALID_ARG;
+        for (const Bytes* other = out; other != &o; ++other)
+            if (overlap(o, *other)) return MLA_ERR_INVALID_ARG;
+    }
     int rc = check_header(workspace, workspace_bytes);
     if (rc != MLA_OK) return rc;
+    const Bytes header = {workspace, MLA_WORKSPACE_HEADER_BYTES};
+    for (const Bytes& o : out)
+        if (overlap(header, o)) return MLA_ERR_INVALID_ARG;
+    for (const Bytes& i : in)
+        if (overlap(header, i)) return MLA_ERR_INVALID_ARG;
     rc = device_ok();
     if (rc != MLA_OK) return rc;
 

@@ -3,7 +3,7 @@ workspace, but for the pairs that a call takes in place."""
 import pytest
 import torch
 
-from test_beam_host import BUF, FAR, INVALID, DEVICE, lib, select  # noqa: F401
+from test_beam_host import BUF, FAR, INVALID, DEVICE, WS, extend, lib, select  # noqa: F401
 
 # (with a device what is not refused would run, on addresses that are none)
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="has a device")
@@ -63,3 +63,44 @@ def test_select_side_by_side(lib):  # noqa: F811
     assert select(lib, **dict(four, scores_out=four["scores"], tokens=four["scores"])) == INVALID
     assert select(lib, **dict(four, scores=BUF, scores_out=BUF)) == INVALID
     assert select(lib, **dict(four, finished=BUF + FAR, finished_out=BUF + FAR)) == INVALID
+
+
+# the entries of the call's defaults, of four bytes; six requests of four, six tokens
+EXTEND = dict(kv_indices=BUF, kv_indptr=BUF + FAR, seq_lens=BUF + 2 * FAR, parents=BUF + 3 * FAR,
+              new_tokens=BUF + 4 * FAR, free_slots=BUF + 5 * FAR, cursor=BUF + 6 * FAR,
+              new_indices=BUF + 7 * FAR, new_indptr=BUF + 8 * FAR, new_lens=BUF + 9 * FAR,
+              slots=BUF + 10 * FAR, positions=BUF + 11 * FAR, token_indptr=BUF + 12 * FAR,
+              new_cursor=BUF + 13 * FAR, workspace=BUF + 14 * FAR, prefix_len=BUF + 15 * FAR)
+ENTRIES = {k: 4 * n for k, n in dict(
+    kv_indices=100, kv_indptr=5, seq_lens=4, parents=6, new_tokens=6, free_slots=50, cursor=1,
+    prefix_len=1, new_indices=150, new_indptr=7, new_lens=6, slots=6, positions=6, token_indptr=7,
+    new_cursor=1).items()}
+EXTENDED = ["new_indices", "new_indptr", "new_lens", "slots", "positions", "token_indptr",
+            "new_cursor"]
+
+
+@pytest.mark.parametrize("a,b,how", pairs(
+    ENTRIES, EXTENDED, [k for k in ENTRIES if k not in EXTENDED], [("new_cursor", "cursor")]))
+def test_extend(lib, a, b, how):    # noqa: F811
+    assert extend(lib, **{**EXTEND, a: placed(EXTEND, ENTRIES, a, b, how)}) == INVALID
+
+
+@pytest.mark.parametrize("a", list(ENTRIES))
+def test_extend_workspace(lib, a):  # noqa: F811
+    at = EXTEND["workspace"]
+    for x in (at, at + 4 - ENTRIES[a], at + WS - 4):
+        assert extend(lib, **{**EXTEND, a: x}) == INVALID
+    assert extend(lib, **{**EXTEND, a: at + WS}) in READY
+
+
+def test_extend_side_by_side(lib):  # noqa: F811
+    assert extend(lib, **EXTEND) in READY
+    at, kw = BUF + 20 * FAR, dict(EXTEND)
+    for name in EXTENDED:
+        kw[name] = at
+        at += ENTRIES[name]
+    assert extend(lib, **kw) in READY
+    assert extend(lib, **dict(kw, new_cursor=kw["cursor"])) in READY
+    # what has no entries overlaps nothing
+    none = dict(kw, num_tokens=0, slots=BUF, positions=BUF, total=0, new_indices=BUF)
+    assert extend(lib, **none) in READY

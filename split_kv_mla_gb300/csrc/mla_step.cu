@@ -1513,17 +1513,24 @@ int mla_beam_reorder(const void* state, int64_t state_stride, int32_t num_parent
         rows_overlap(state, num_parents, state_stride, out, num_rows, out_stride, row_bytes))
         return MLA_ERR_INVALID_ARG;
     const int64_t F = num_rows, span = (F - 1) * out_stride + row_bytes;
-    for (const int32_t* in : {parents, tokens, lens}) {
-        const int64_t n = (in == lens ? num_parents : F) * 4;
-        if (overlap(out_lens, F * 4, in, n) || overlap(out, span, in, n)) return MLA_ERR_INVALID_ARG;
-    }
-    if (overlap(out_lens, F * 4, out, span)) return MLA_ERR_INVALID_ARG;
+    const Bytes in[] = {{parents, F * 4}, {tokens, F * 4}, {lens, (int64_t)num_parents * 4}};
+    const Bytes rows = {out, span}, counts = {out_lens, F * 4};
+    auto on_state = [&](const Bytes& b) {
+        return rows_reach(state, num_parents, state_stride, row_bytes, b);
+    };
+    for (const Bytes& i : in)
+        if (overlap(counts, i) || overlap(rows, i)) return MLA_ERR_INVALID_ARG;
+    if (overlap(counts, rows) || on_state(counts)) return MLA_ERR_INVALID_ARG;
     uintptr_t bits = reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(out);
     if (num_parents > 1) bits |= (uintptr_t)state_stride;
     if (num_rows > 1) bits |= (uintptr_t)out_stride;
     if (tokens != nullptr && (bits & 3u) != 0) return MLA_ERR_MISALIGNED;
     int rc = check_header(workspace, workspace_bytes);
     if (rc != MLA_OK) return rc;
+    const Bytes header = {workspace, MLA_WORKSPACE_HEADER_BYTES};
+    for (const Bytes& b : {rows, counts, in[0], in[1], in[2]})
+        if (overlap(header, b)) return MLA_ERR_INVALID_ARG;
+    if (on_state(header)) return MLA_ERR_INVALID_ARG;
     rc = device_ok();
     if (rc != MLA_OK) return rc;
 

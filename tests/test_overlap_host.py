@@ -3,7 +3,7 @@ workspace, but for the pairs that a call takes in place."""
 import pytest
 import torch
 
-from test_beam_host import BUF, FAR, INVALID, DEVICE, WS, extend, lib, select  # noqa: F401
+from test_beam_host import BUF, FAR, INVALID, DEVICE, WS, extend, lib, reorder, select  # noqa: F401
 
 # (with a device what is not refused would run, on addresses that are none)
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="has a device")
@@ -104,3 +104,41 @@ def test_extend_side_by_side(lib):  # noqa: F811
     # what has no entries overlaps nothing
     none = dict(kw, num_tokens=0, slots=BUF, positions=BUF, total=0, new_indices=BUF)
     assert extend(lib, **none) in READY
+
+
+# four rows of 64 bytes of four
+REORDER = dict(state=BUF, parents=BUF + FAR, out=BUF + 2 * FAR, workspace=BUF + 3 * FAR,
+               lens=BUF + 4 * FAR, tokens=BUF + 5 * FAR, out_lens=BUF + 6 * FAR)
+ROWS = dict(state=256, parents=16, out=256, lens=16, tokens=16, out_lens=16)
+
+
+@pytest.mark.parametrize("a,b,how", pairs(ROWS, ["out", "out_lens"],
+                                          ["state", "parents", "lens", "tokens"]))
+def test_reorder(lib, a, b, how):   # noqa: F811
+    assert reorder(lib, **{**REORDER, a: placed(REORDER, ROWS, a, b, how)}) == INVALID
+
+
+@pytest.mark.parametrize("a", list(ROWS))
+def test_reorder_workspace(lib, a):     # noqa: F811
+    at = REORDER["workspace"]
+    for x in (at, at + 4 - ROWS[a], at + WS - 4):
+        assert reorder(lib, **{**REORDER, a: x}) == INVALID
+    assert reorder(lib, **{**REORDER, a: at + WS}) in READY
+
+
+def test_reorder_side_by_side(lib):     # noqa: F811
+    assert reorder(lib, **REORDER) in READY
+    # between the rows of the state, and of out
+    between = dict(REORDER, state_stride=128, out_stride=128)
+    assert reorder(lib, **dict(between, out_lens=BUF + 64)) in READY
+    assert reorder(lib, **dict(between, out_lens=BUF + 3 * 128 + 64)) in READY
+    assert reorder(lib, **dict(between, out_lens=BUF + 60)) == INVALID
+    assert reorder(lib, **dict(between, out_lens=BUF + 116)) == INVALID
+    assert reorder(lib, **dict(between, out_lens=BUF + 3 * 128 + 60)) == INVALID
+    # one row for all
+    assert reorder(lib, **dict(REORDER, state_stride=0, out_lens=BUF + 64)) in READY
+    assert reorder(lib, **dict(REORDER, num_parents=0, out_lens=BUF)) in READY
+    # one list as parents and as lengths is as long as both
+    same = dict(REORDER, lens=BUF + FAR, num_parents=2)
+    assert reorder(lib, **same) in READY
+    assert reorder(lib, **dict(same, out_lens=BUF + FAR + 12)) == INVALID

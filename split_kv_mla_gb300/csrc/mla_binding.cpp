@@ -59,7 +59,11 @@ const at::Tensor& tensor(PyObject* o, const char* name)
     static const at::Tensor none;
     if (o == Py_None) return none;
     if (!THPVariable_Check(o)) bad(std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    // (its memory holds other values)
+    if (t.is_conj() || t.is_neg())
+        bad(std::string(name) + " must not be a lazily conjugated or negated view: resolve it first");
+    return t;
 }
 
 const at::Tensor& given(PyObject* o, const char* name)

@@ -755,7 +755,7 @@ def mla_beam_reorder(state, parents, lens=None, tokens=None, out=None, out_lens=
     out_lens).  lens int32 [rows of state]: only that many of a row's elements are copied
     (the rest of a given out stays, of a new one is zero).  tokens int32 [rows of out], for
     a state of int32: tokens[f] behind them.  out_lens (None without lens) counts both.
-    out must not overlap state."""
+    out must not overlap state.  Neither is a lazily conjugated or negated view."""
     if stream is not None:
         with _on(stream):
             return mla_beam_reorder(state, parents, lens, tokens, out, out_lens, workspace_t)

@@ -268,7 +268,7 @@ __device__ __forceinline__ float from_ordered(int i)
 __device__ __forceinline__ float warp_max(float x)
 {
     float m;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
     return m;
 }
 

@@ -16,6 +16,10 @@
 namespace mla {
 namespace {
 
+// The kernels here start while the preceding one runs, which may write what they read, as one
+// call's outputs are the next one's inputs: nothing is read before the wait for it, and nothing
+// by __ldg, which is for what stays as it is for as long as the kernel runs.
+
 // ---- beam selection -------------------------------------------------------------------------
 //
 // The logits are read once.  For a row's score order only x matters, and the K best
@@ -164,13 +168,13 @@ __device__ __noinline__ uint4 load_edge(const T* row, int col, int vocab)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 4) {
-            w[i] = col + i < vocab ? __ldg(reinterpret_cast<const uint32_t*>(row) + col + i)
+            w[i] = col + i < vocab ? reinterpret_cast<const uint32_t*>(row)[col + i]
                                    : 0xFF800000u;
         } else {
             const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
             const uint32_t none = LogitType<T>::kNone;
-            const uint32_t lo = col + 2 * i < vocab ? __ldg(p + col + 2 * i) : none;
-            const uint32_t hi = col + 2 * i + 1 < vocab ? __ldg(p + col + 2 * i + 1) : none;
+            const uint32_t lo = col + 2 * i < vocab ? p[col + 2 * i] : none;
+            const uint32_t hi = col + 2 * i + 1 < vocab ? p[col + 2 * i + 1] : none;
             w[i] = lo | hi << 16;
         }
     }
@@ -219,14 +223,14 @@ __device__ __forceinline__ void load_segment(const SelectArgs& a, int64_t row, i
                 constexpr uint32_t none = LogitType<T>::kNone;
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const uint32_t lo = 64 * k < left ? __ldg(h + 64 * k) : none;
-                    const uint32_t hi = 64 * k + 1 < left ? __ldg(h + 64 * k + 1) : none;
+                    const uint32_t lo = 64 * k < left ? h[64 * k] : none;
+                    const uint32_t hi = 64 * k + 1 < left ? h[64 * k + 1] : none;
                     w[k] = lo | hi << 16;
                 }
             } else if (odd) {
 #pragma unroll
                 for (int k = 0; k < N; ++k)
-                    w[k] = __funnelshift_r(__ldg(p + 32 * k), __ldg(p + 32 * k + 1), 16);
+                    w[k] = __funnelshift_r(p[32 * k], p[32 * k + 1], 16);
             } else {
 #pragma unroll
                 for (int k = 0; k < N; ++k) w[k] = __ldcs(p + 32 * k);
@@ -274,8 +278,9 @@ __device__ __forceinline__ float warp_max(float x)
 
 __device__ __forceinline__ bool row_is_live(const SelectArgs& a, int64_t row)
 {
-    return __ldg(a.scores + row) != -INFINITY &&
-           (a.finished == nullptr || __ldg(a.finished + row) == 0);
+    const float score = a.scores[row];
+    const uint8_t finished = a.finished == nullptr ? 0 : a.finished[row];
+    return score != -INFINITY && finished == 0;
 }
 
 // A segment's group maxima and its part.
@@ -899,7 +904,7 @@ reorder_kernel(const ReorderArgs a)
     allow_dependents();
     const uint32_t f = blockIdx.x / a.parts, part = blockIdx.x - f * a.parts;
     const bool first = part == 0 && threadIdx.x == 0;
-    const int32_t p = __ldg(a.parents + f);
+    const int32_t p = a.parents[f];
     if (p < 0 || p >= a.num_parents) {
         if (first) {
             atomicOr(a.err, MLA_DEVERR_BAD_TABLE);
@@ -911,12 +916,12 @@ reorder_kernel(const ReorderArgs a)
     uint8_t* out = a.out + f * a.out_stride;
     if (a.lens != nullptr) {
         const int64_t room = a.row_bytes / a.elem_bytes;
-        const int64_t want = __ldg(a.lens + p);
+        const int64_t want = a.lens[p];
         const int64_t len = want < 0 ? 0 : want > room ? room : want;
         bytes = len * a.elem_bytes;
         if (first) {
             const bool add = a.tokens != nullptr && len < room;
-            if (add) *reinterpret_cast<int32_t*>(out + bytes) = __ldg(a.tokens + f);
+            if (add) *reinterpret_cast<int32_t*>(out + bytes) = a.tokens[f];
             if (a.out_lens != nullptr) a.out_lens[f] = (int32_t)(len + (add ? 1 : 0));
             if (len != want || (a.tokens != nullptr && !add)) atomicOr(a.err, MLA_DEVERR_BAD_LENGTH);
         }
@@ -947,13 +952,13 @@ reorder_kernel(const ReorderArgs a)
         if (ALIGNED || shift == 0) {
 #pragma unroll
             for (int k = 0; k < kReorderTurns; ++k)
-                if (i + k * kReorderThreads < end) v[k] = __ldg(from + i + k * kReorderThreads);
+                if (i + k * kReorderThreads < end) v[k] = from[i + k * kReorderThreads];
         } else {
 #pragma unroll
             for (int k = 0; k < kReorderTurns; ++k)
                 if (i + k * kReorderThreads < end) {
                     const uint4* q = from + i + k * kReorderThreads;
-                    v[k] = shifted(__ldg(q), __ldg(q + 1), shift);
+                    v[k] = shifted(q[0], q[1], shift);
                 }
         }
 #pragma unroll
@@ -1022,13 +1027,13 @@ struct Kept {
 
 __device__ __forceinline__ Kept kept_of(const ExtendArgs& a, int f, uint32_t& bad)
 {
-    const int p = a.parents == nullptr ? f : __ldg(a.parents + f);
+    const int p = a.parents == nullptr ? f : a.parents[f];
     if (p < 0 || p >= a.num_parents) {
         bad |= MLA_DEVERR_BAD_TABLE;
         return Kept{0, 0};
     }
-    const int64_t from = __ldg(a.kv_indptr + p), to = __ldg(a.kv_indptr + p + 1);
-    const int64_t want = __ldg(a.seq_lens + p);
+    const int64_t from = a.kv_indptr[p], to = a.kv_indptr[p + 1];
+    const int64_t want = a.seq_lens[p];
     if (from < 0 || to > a.num_indices || to < from) {
         bad |= MLA_DEVERR_BAD_TABLE;
         return Kept{0, 0};
@@ -1080,7 +1085,7 @@ __device__ __forceinline__ int32_t free_slot(const ExtendArgs& a, int32_t number
         bad |= MLA_DEVERR_NO_SLOT;
         return -1;
     }
-    const int32_t slot = a.free_slots == nullptr ? number : __ldg(a.free_slots + number);
+    const int32_t slot = a.free_slots == nullptr ? number : a.free_slots[number];
     if (slot >= 0 && slot < a.pool_rows) return slot;
     bad |= MLA_DEVERR_BAD_SLOT;
     return -1;
@@ -1120,7 +1125,7 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
     const uint32_t room = (uint32_t)a.total, token_room = (uint32_t)a.num_tokens;
     uint32_t bad = 0;
     for (int f = tid; f < F; f += kExtendThreads) {
-        int n = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
+        int n = a.new_tokens == nullptr ? 1 : a.new_tokens[f];
         if (n < 0) {
             n = 0;
             bad |= MLA_DEVERR_BAD_LENGTH;
@@ -1160,8 +1165,8 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
 
     if (lead || spread) {
         const int step = spread ? (int)gridDim.x * kExtendThreads : kExtendThreads;
-        const int32_t cursor = a.num_tokens > 0 ? __ldg(a.cursor) : 0;
-        const int32_t prefix = a.prefix_len == nullptr ? 0 : __ldg(a.prefix_len);
+        const int32_t cursor = a.num_tokens > 0 ? a.cursor[0] : 0;
+        const int32_t prefix = a.prefix_len == nullptr ? 0 : a.prefix_len[0];
         for (int64_t t = (int64_t)(spread ? blockIdx.x : 0) * kExtendThreads + tid; t < a.num_tokens;
              t += step) {
             int32_t slot = -1, position = 0;
@@ -1213,7 +1218,7 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
             const int32_t* src = a.kv_indices + from[lo] + (i0 + lane);
 #pragma unroll
             for (int k = 0; k < SPAN; ++k)
-                if (32 * k < left) v[k] = __ldg(src + 32 * k);
+                if (32 * k < left) v[k] = src[32 * k];
 #pragma unroll
             for (int k = 0; k < SPAN; ++k)
                 if (32 * k < left) dst[32 * k] = v[k];
@@ -1229,7 +1234,7 @@ extend_kernel(const ExtendArgs a, bool spread, bool move_cursor)
                 const int32_t i = (int32_t)i0 + lane + 32 * k;
                 const int f = last_at_most(start, lo, hi, i);
                 kept[k] = i - start[f] < length[f];
-                if (kept[k]) v[k] = __ldg(a.kv_indices + (from[f] + i));
+                if (kept[k]) v[k] = a.kv_indices[from[f] + i];
             }
         }
 #pragma unroll
@@ -1261,7 +1266,7 @@ sums_kernel(const ExtendArgs a)
         const uint32_t f = f0 + tid;
         uint32_t n = 0, length = 0;
         if (f < F) {
-            const int32_t want = a.new_tokens == nullptr ? 1 : __ldg(a.new_tokens + f);
+            const int32_t want = a.new_tokens == nullptr ? 1 : a.new_tokens[f];
             n = max(want, 0);
             if (want < 0) bad |= MLA_DEVERR_BAD_LENGTH;
             length = kept_of(a, (int)f, bad).length;
@@ -1336,7 +1341,7 @@ fill_kernel(const ExtendArgs a, uint32_t entry_ctas)
                 j = i - __ldcg(a.new_indptr + f);
             }
             kept[k] = j < from.length;
-            if (kept[k]) v[k] = __ldg(a.kv_indices + from.from + j);
+            if (kept[k]) v[k] = a.kv_indices[from.from + j];
         }
 #pragma unroll
         for (int k = 0; k < kFillSpan / 32; ++k)
@@ -1352,7 +1357,7 @@ fill_kernel(const ExtendArgs a, uint32_t entry_ctas)
         const Kept k = kept_of(a, f, bad);
         bad = 0;   // the sums have told
         const int64_t j = k.length + (t - __ldcg(a.token_indptr + f));
-        position = (int32_t)(j + (a.prefix_len == nullptr ? 0 : __ldg(a.prefix_len)));
+        position = (int32_t)(j + (a.prefix_len == nullptr ? 0 : a.prefix_len[0]));
         if (j < __ldcg(a.new_lens + f)) {
             slot = free_slot(a, (int32_t)((uint32_t)__ldcg(a.new_cursor) - (uint32_t)tokens + (uint32_t)t),
                              bad);

@@ -98,3 +98,42 @@ def test_one_token_left(dtype):
     s = torch.tensor([[-1e-7, -0.3, -1.5, -40.0]], device="cuda")
     got = check(x, s, W)
     assert torch.equal(got[0], s[0].cpu())
+
+
+def exact_rows(dtype, level, seed):
+    """Beams of 2^n equal logits and nothing else, so that their sums are exact, whose
+    scores lie one or two fp32 steps from one another: (logits, scores, float64 scores of
+    the beams' tokens)."""
+    g = torch.Generator().manual_seed(seed)
+    W, V = 8, 5003
+    n = torch.randint(0, 11, (W,), generator=g)
+    x = torch.full((W, V), -math.inf)
+    for w in range(W):
+        at = torch.randperm(V, generator=g)[:2 ** int(n[w])]
+        x[w, at] = [0.0, -3.0, 13.5, 7.25][w % 4]
+    step = 2.0 ** (math.floor(math.log2(-level)) - 23)
+    apart = torch.randint(0, 3, (W,), generator=g).cumsum(0)[torch.randperm(W, generator=g)]
+    s = (level + n.double() * math.log(2.0) - apart * step).float()
+    return x.to(dtype), s.view(1, W), s.double() - n.double() * math.log(2.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("level", [-1.3, -7.7, -41.0, -97.5])
+@pytest.mark.parametrize("seed", range(4))
+def test_steps_between_beams(dtype, level, seed):
+    """Before it is rounded such a score is off by less than 2^-32: the parts of cum - m - n ln 2
+    below the first float, 2^-17 at most, and n times what ln 2 has below its first part,
+    3.3e-4, are rounded three times each.  Scores that lie no nearer than that to the middle
+    of two numbers come out as the rounded ones, and in their order."""
+    x, s, score = exact_rows(dtype, level, seed)
+    step = torch.exp2(torch.floor(torch.log2(-score)) - 23)
+    middle = ((score / step) % 1 - 0.5).abs() * step
+    assert bool((middle > 2.0 ** -31).all())    # (of these inputs)
+    want = [(-float(score[w].float()), w, v) for w in range(x.shape[0])
+            for v in (x[w] > -math.inf).nonzero()[:, 0].tolist()]
+    want = sorted(want)[:32]
+    tokens, parents, got, _ = mla.mla_beam_select(x.cuda(), s.cuda(), 32)
+    n = len(want)
+    assert list(zip(parents[0, :n].tolist(), tokens[0, :n].tolist())) == [(w, v) for _, w, v in want]
+    assert got[0, :n].tolist() == [-a for a, _, _ in want]
+    assert bool((tokens[0, n:] == -1).all())

@@ -42,7 +42,7 @@ def lib(tmp_path_factory):
     d = tmp_path_factory.mktemp("spans")
     (d / "spans.cpp").write_text(CODE)
     so = str(d / "spans.so")
-    subprocess.run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-shared", "-fwrapv",
+    subprocess.run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-shared",
                     "-I", mla_build.CSRC, str(d / "spans.cpp"), "-o", so], check=True)
     lib = ctypes.CDLL(so)
     lib.kept.restype = ctypes.c_int64

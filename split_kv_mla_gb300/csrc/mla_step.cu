@@ -42,7 +42,7 @@ namespace {
 // so equal rows give equal sums and their equal candidates are taken by their index.
 // Where one token has most of a row's mass, the logarithm is that of 1 + t with a small t,
 // of which a sum that has the 1 has lost all below 2^-24 (scores of -2e-8 came out as 0).
-// There pick sums the maximum's segment again without it, 0.6 to 1.9 us of a call whose
+// There pick sums the maximum's segment again without it, 0.8 to 1.9 us of a call whose
 // rows are such.  (In scan, where every segment has a maximum, leaving the 1 out took every
 // call longer: 11.7 -> 13.5 us for 32 x 4 of 100003 fp16, by its registers.)
 
@@ -980,8 +980,8 @@ reorder_kernel(const ReorderArgs a)
 // Bytes: 8 per entry that is kept, 12 (16 with a list of free slots) per token.
 // Every CTA sums the requests' lengths and counts by itself, in shared memory, and
 // fills its part of the new table from there: one launch.  A kernel that left the sums
-// for a second one took 7.5 us where this takes 4.2 (8 requests of 8192), and looking a
-// request up in global memory, per entry, 103 us where this takes 8.6 (512 of 1024 to
+// for a second one took 7.5 us where this takes 4.3 (8 requests of 8192), and looking a
+// request up in global memory, per entry, 103 us where this takes 8.8 (512 of 1024 to
 // 8192).  More requests than shared memory is given for go that way:
 //   sums   (one CTA) the requests' lengths and counts, their sums, the cursor;
 //   fill   a warp per 256 entries of the new table, a thread per token.

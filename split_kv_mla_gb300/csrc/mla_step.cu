@@ -411,8 +411,9 @@ __device__ __forceinline__ float2 peaked_base(const SelectArgs& a, int64_t row, 
     float rest = sum.x + sum.y;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
-    const float2 b = two_sum(score, -m);
-    return two_sum(b.x, b.y - log1pf(rest));
+    // m last: the score and the logarithm may both be far below it
+    const float2 u = two_sum(score, -log1pf(rest)), b = two_sum(u.x, -m);
+    return two_sum(b.x, b.y + u.y);
 }
 
 // A score as a number in its order; 0 for what is no candidate (-inf, or the NaN that

@@ -137,3 +137,20 @@ def test_steps_between_beams(dtype, level, seed):
     assert list(zip(parents[0, :n].tolist(), tokens[0, :n].tolist())) == [(w, v) for _, w, v in want]
     assert got[0, :n].tolist() == [-a for a, _, _ in want]
     assert bool((tokens[0, n:] == -1).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("V", [12, 4099])
+@pytest.mark.parametrize("shift", [-45.0, 60.0, 777.0, -3000.0, 30000.0])
+def test_scores_far_below_the_logits(dtype, V, shift):
+    # (what a logit's size is does not matter: a score is a difference)
+    g = torch.Generator().manual_seed(V)
+    W = 16
+    x = torch.randn(W, V, generator=g) * 3
+    x[:, V // 2] = torch.linspace(8, 30, W)
+    step = {FP: 0.0, HF: 2.0 ** -10, BF: 2.0 ** -7}[dtype] * abs(shift)   # kept apart by the type
+    x = (x * max(1.0, step) + shift).to(dtype)
+    for size in (0.0, 1e-8, 1e-7, 1e-6, 1e-5, 1e-4, 1e-3, 1e-2):
+        s = -size * torch.rand(1, W, generator=g)
+        check(x.cuda(), s.cuda(), W)
+        check(x.cuda(), -s.cuda(), 2 * W)

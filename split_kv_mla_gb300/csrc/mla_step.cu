@@ -347,12 +347,12 @@ __device__ __forceinline__ float2 two_sum(float a, float b)
     return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
 
-// score - m - ln(sum) as a sum of two floats, so that a candidate's score is rounded
-// once: the scores of different beams that fp32 tells apart come out in their order, as far
-// as the sums are that exact (which is within 2^-15 of the logarithm).
+// score - m - ln(sum) as a sum of floats, the largest first, so that a candidate's score is
+// rounded once: the scores of different beams that fp32 tells apart come out in their order,
+// as far as the sums are that exact (which is within 2^-15 of the logarithm).
 // ln(sum) = e ln 2 + ln f with f in [0.75, 1.5); ln 2 in two parts, of which the first
 // has 12 bits, so that e times it is exact.
-__device__ __forceinline__ float2 row_base(float score, float m, float sum)
+__device__ __forceinline__ float3 row_base(float score, float m, float sum)
 {
     int e = ((__float_as_int(sum) >> 23) & 255) - 127;
     float f = __int_as_float((__float_as_int(sum) & 0x7FFFFF) | 0x3F800000);
@@ -364,7 +364,8 @@ __device__ __forceinline__ float2 row_base(float score, float m, float sum)
     constexpr double kHigh = 2839.0 / 4096.0;
     const float2 a = two_sum(score, -m);
     const float2 b = two_sum(a.x, -(float)e * (float)kHigh);
-    return two_sum(b.x, (a.y + b.y) - fmaf((float)e, (float)(kLn2 - kHigh), logf(f)));
+    const float2 c = two_sum(b.x, (a.y + b.y) - fmaf((float)e, (float)(kLn2 - kHigh), logf(f)));
+    return make_float3(c.x, c.y, 0.f);
 }
 
 // The same of a row whose maximum, which it has once, has more than two thirds of its mass:
@@ -372,7 +373,7 @@ __device__ __forceinline__ float2 row_base(float score, float m, float sum)
 // again without it, and the other segments' sums are joined by expf, as their maxima are far
 // below m; head are those that the lane has.
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ float2 peaked_base(const SelectArgs& a, int64_t row, int lane, float score,
+__device__ __forceinline__ float3 peaked_base(const SelectArgs& a, int64_t row, int lane, float score,
                                               float m, const float2 (&head)[kParts])
 {
     constexpr int kPerGroup = kGroup / (32 * kElements<T>);
@@ -411,17 +412,18 @@ __device__ __forceinline__ float2 peaked_base(const SelectArgs& a, int64_t row, 
     float rest = sum.x + sum.y;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
-    // m last: the score and the logarithm may both be far below it
+    // m last, and all three: the score and the logarithm may both be far below it
     const float2 u = two_sum(score, -log1pf(rest)), b = two_sum(u.x, -m);
-    return two_sum(b.x, b.y + u.y);
+    return make_float3(b.x, b.y, u.y);
 }
 
 // A score as a number in its order; 0 for what is no candidate (-inf, or the NaN that
 // the base of a beam without candidates makes).
-__device__ __forceinline__ uint32_t rank_of(float2 base, float x)
+__device__ __forceinline__ uint32_t rank_of(float3 base, float x)
 {
-    const float2 s = two_sum(base.x, x);
-    const float score = __fadd_rn(__fadd_rn(s.x, __fadd_rn(s.y, base.y)), 0.f);   // -0 as +0
+    const float2 s = two_sum(base.x, x), t = two_sum(s.x, base.y);
+    const float rest = __fadd_rn(__fadd_rn(t.y, s.y), base.z);
+    const float score = __fadd_rn(__fadd_rn(t.x, rest), 0.f);   // -0 as +0
     return score > -INFINITY ? (uint32_t)ordered(score) ^ 0x80000000u : 0u;
 }
 
@@ -472,7 +474,7 @@ struct Picker {
     int beam[kPickSlots], place[kPickSlots];
     uint64_t list[kPickList];
     uint64_t warps[kPickWarps];
-    float2 base[MLA_MAX_BEAMS];         // -inf: no candidates; of an ended beam its score
+    float3 base[MLA_MAX_BEAMS];         // -inf: no candidates; of an ended beam its score
     int ended[MLA_MAX_BEAMS];
 };
 
@@ -650,27 +652,35 @@ pick_kernel(const SelectArgs a)
         float m = -INFINITY, s = 0.f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) m = fmaxf(m, t[k].x);
-#pragma unroll 4
-        for (int i = lane + 32 * kParts; i < a.segments; i += 32) m = fmaxf(m, __ldcg(parts + i).x);
+        // of rows with more parts (kParts at once, whatever is made of the loop: one
+        // after the other they took 10.6 us for 1 x 1 x 1048576, this way 9.0)
+        auto more_parts = [&](auto&& each) {
+#pragma unroll 1
+            for (int i = lane + 32 * kParts; i < a.segments; i += 32 * kParts) {
+                float2 u[kParts];
+#pragma unroll
+                for (int k = 0; k < kParts; ++k)
+                    u[k] = i + 32 * k < a.segments ? __ldcg(parts + i + 32 * k) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) each(u[k]);
+            }
+        };
+        more_parts([&](float2 u) { m = fmaxf(m, u.x); });
         m = warp_max(m);
         const float ref = m == -INFINITY ? 0.f : m;
         constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) s += t[k].y * ex2_approx((t[k].x - ref) * kLog2e);
-#pragma unroll 4
-        for (int i = lane + 32 * kParts; i < a.segments; i += 32) {
-            const float2 u = __ldcg(parts + i);
-            s += u.y * ex2_approx((u.x - ref) * kLog2e);
-        }
+        more_parts([&](float2 u) { s += u.y * ex2_approx((u.x - ref) * kLog2e); });
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         // (what is not read of a beam without candidates may be anything)
         const bool none = own == -INFINITY;
         // a NaN or +inf among the logits makes the sum one
         const bool bad = !none && (!(own < INFINITY) || (!is_ended && !(s < INFINITY)));
-        float2 b = make_float2(-INFINITY, 0.f);
+        float3 b = make_float3(-INFINITY, 0.f, 0.f);
         if (!none && !bad && (is_ended || s != 0.f))
-            b = is_ended ? make_float2(own, 0.f)
+            b = is_ended ? make_float3(own, 0.f, 0.f)
                 : __builtin_expect(s < kPeakedSum, 0)
                     ? peaked_base<T, ALIGNED>(a, row, lane, own, m, t)
                     : row_base(own, m, s);
@@ -762,7 +772,7 @@ pick_kernel(const SelectArgs a)
                         for (int k = 0; k < kChunk; ++k) x[k] = -INFINITY;
                         if (g0 == 0) x[0] = 0.f;
                     }
-                    const float2 b = p.base[w];
+                    const float3 b = p.base[w];
 #pragma unroll 1
                     for (int g = g0; g < G; g += 32 * share * kChunk) {
                         if (reload && !is_ended) load_maxima(w, g);

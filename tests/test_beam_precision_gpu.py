@@ -154,3 +154,17 @@ def test_scores_far_below_the_logits(dtype, V, shift):
         s = -size * torch.rand(1, W, generator=g)
         check(x.cuda(), s.cuda(), W)
         check(x.cuda(), -s.cuda(), 2 * W)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("m", [27.25, 19.0, 61.0, 0.75])
+def test_scores_of_half_a_step_of_the_maximum(dtype, m):
+    # where cum - m rounds to a neighbour of m, one rounding must not follow another
+    W, V = 32, 10
+    g = torch.Generator().manual_seed(int(m))
+    x = torch.randn(W, V, generator=g) * 0.4 + (m - 25)
+    x[:, 3] = m
+    half = 2.0 ** (math.floor(math.log2(m)) - 24)
+    for lo, hi in ((0.98, 1.06), (0.5, 2.0)):
+        s = -half * (lo + (hi - lo) * torch.rand(4, W, generator=g))
+        check(x.repeat(4, 1).to(dtype).cuda(), s.cuda(), W)

@@ -42,7 +42,7 @@ namespace {
 // so equal rows give equal sums and their equal candidates are taken by their index.
 // Where one token has most of a row's mass, the logarithm is that of 1 + t with a small t,
 // of which a sum that has the 1 has lost all below 2^-24 (scores of -2e-8 came out as 0).
-// There pick sums the maximum's segment again without it, 0.8 to 1.9 us of a call whose
+// There pick sums the maximum's segment again without it, 0.6 to 1.8 us of a call whose
 // rows are such.  (In scan, where every segment has a maximum, leaving the 1 out took every
 // call longer: 11.7 -> 13.5 us for 32 x 4 of 100003 fp16, by its registers.)
 
